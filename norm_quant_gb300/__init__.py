@@ -1,9 +1,11 @@
-"""MoE combine/finalize on one GB300 -- Python binding of ``libnqg.so``.
+"""MoE combine/finalize and few-token serving operators on one GB300 --
+Python binding of ``libnqg.so``.
 
 Argument marshalling only: every step of the path runs in the library's
 CUDA kernels.  Tensors are torch CUDA tensors (torch provides device memory
 and streams); bf16 tensors may be ``torch.bfloat16`` or raw 16-bit views.
-The entry points have the names of the C ABI in ``include/moe_combine.h``.
+The entry points have the names of the C ABI in ``include/moe_combine.h`` and
+``include/moe_layer.h``.
 
 There is no fallback: if the library is not built, every call raises.
 Build it with ``norm_quant_gb300.build.build()`` (``__graft_entry__.build()``).
@@ -20,6 +22,10 @@ QUANT = {None: 0, "none": 0, "mxfp8": 1, "nvfp4": 2, "mxfp4": 3}
 IO_DTYPE = {"bf16": 0, "fp16": 1}
 WEIGHT_DTYPE = {"fp32": 0, "bf16": 1, "fp16": 2}
 LAYOUT = {"linear": 0, "swizzled": 1, "128x4": 1}
+W_FORMAT = {None: 0, "none": 0, "nvfp4": 1, "int4": 2}
+SCORING = {"softmax": 0, "sigmoid": 1}
+ACTIVATION = {"silu": 0, "gelu_tanh": 1}
+FEW_TOKENS = 64  # MOE_FEW_TOKENS
 EXPERT_LAYOUT = {"grouped": 0, "slot_major": 1}
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = 1
@@ -48,6 +54,31 @@ class MoeCombineArgs(C.Structure):
     ]
 
 
+class MoeLinearW4Args(C.Structure):
+    """Mirror of ``moe_linear_w4_args`` (include/moe_layer.h)."""
+    _fields_ = [
+        ("M", C.c_int64), ("N", C.c_int32), ("K", C.c_int32),
+        ("x", C.c_void_p), ("x_stride", C.c_int64),
+        ("w", C.c_void_p), ("w_scales", C.c_void_p), ("w_zeros", C.c_void_p),
+        ("global_scale", C.c_float), ("w_format", C.c_int32), ("group_size", C.c_int32), ("io_dtype", C.c_int32),
+        ("out", C.c_void_p), ("out_stride", C.c_int64),
+    ]
+
+
+class MoeLayerArgs(C.Structure):
+    """Mirror of ``moe_layer_args`` (include/moe_layer.h)."""
+    _fields_ = [
+        ("T", C.c_int64), ("H", C.c_int32), ("I", C.c_int32), ("E", C.c_int32), ("top_k", C.c_int32),
+        ("x", C.c_void_p), ("x_stride", C.c_int64), ("topk_ids", C.c_void_p), ("router_weights", C.c_void_p),
+        ("w13", C.c_void_p), ("w13_scales", C.c_void_p), ("w13_zeros", C.c_void_p), ("w13_global", C.c_void_p),
+        ("w2", C.c_void_p), ("w2_scales", C.c_void_p), ("w2_zeros", C.c_void_p), ("w2_global", C.c_void_p),
+        ("shared_out", C.c_void_p), ("residual", C.c_void_p), ("out", C.c_void_p),
+        ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t), ("status", C.c_void_p),
+        ("w_format", C.c_int32), ("group_size", C.c_int32), ("activation", C.c_int32),
+        ("io_dtype", C.c_int32), ("weight_dtype", C.c_int32),
+    ]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {moe_status_string(status)} ({status})")
@@ -57,7 +88,7 @@ class MoeError(RuntimeError):
 _lock = threading.Lock()
 _lib = None
 
-# C symbols declared in include/moe_combine.h, with (restype, argtypes).
+# C symbols declared in include/moe_combine.h and include/moe_layer.h, with (restype, argtypes).
 SYMBOLS = {
     "moe_abi_version": (C.c_int, []),
     "moe_status_string": (C.c_char_p, [C.c_int]),
@@ -78,6 +109,14 @@ SYMBOLS = {
     "moe_debug_stall": (C.c_int, [C.c_int64]),
     "moe_dispatch_permute": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int32,
                                        C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p]),
+    "moe_select_experts": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_int64, C.c_int32, C.c_int32,
+                                     C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_void_p, C.c_int32,
+                                     C.c_void_p]),
+    "moe_linear_w4": (C.c_int, [C.POINTER(MoeLinearW4Args), C.c_void_p]),
+    "moe_linear_w4_args_size": (C.c_size_t, []),
+    "moe_layer_workspace_size": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
+    "moe_layer": (C.c_int, [C.POINTER(MoeLayerArgs), C.c_void_p]),
+    "moe_layer_args_size": (C.c_size_t, []),
 }
 
 
@@ -98,6 +137,9 @@ def lib() -> C.CDLL:
                 raise RuntimeError("libnqg.so ABI version mismatch")
             if L.moe_combine_args_size() != C.sizeof(MoeCombineArgs):
                 raise RuntimeError("moe_combine_args layout mismatch")
+            if (L.moe_linear_w4_args_size() != C.sizeof(MoeLinearW4Args)
+                    or L.moe_layer_args_size() != C.sizeof(MoeLayerArgs)):
+                raise RuntimeError("moe_layer.h argument layout mismatch")
             _lib = L
     return _lib
 
@@ -274,3 +316,112 @@ def moe_combine(stream=None, **kw) -> None:
     """Enqueues the combine; keyword arguments as in combine_args()."""
     args = kw.pop("args", None) or combine_args(**kw)
     _check(lib().moe_combine(C.byref(args), _stream(stream)), "moe_combine")
+
+
+def _rows(t, rows: int, width: int, elem: int, name: str):
+    """(pointer, elements from row to row) of a 2-D tensor whose rows may be
+    strided; ValueError if it is not [rows, width] of elem-byte elements or
+    its rows are not contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensors must be CUDA tensors")
+    if tuple(t.shape) != (rows, width) or t.element_size() != elem:
+        raise ValueError(f"{name} is {tuple(t.shape)} of {t.element_size()}-byte elements; this call needs "
+                         f"{(rows, width)} of {elem}-byte elements")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 else width
+
+
+def _sized(t, nbytes: int, name: str):
+    """Pointer of a contiguous CUDA tensor (or None) that holds at least nbytes."""
+    if t is None:
+        return None
+    _need(t, nbytes, name)
+    return _ptr(t)
+
+
+def _scale_bytes(w_format, group_size: int, elements: int):
+    """(bytes of the scales, bytes of the zero points) of `elements` 4-bit weights."""
+    if w_format == "nvfp4":
+        return elements // 16, 0
+    if w_format == "int4" and group_size > 0:
+        return elements // group_size * 2, elements // group_size
+    return 0, 0
+
+
+def moe_select_experts(logits, topk_ids, router_weights, *, scoring="softmax", renormalize=True, scale=1.0,
+                       logits_dtype="fp32", weight_dtype="fp32", stream=None) -> None:
+    """logits [T, E] (rows may be strided) -> topk_ids int32 [T, k], the k
+    experts with the largest logits in descending order (ties by the lower
+    index; -1 where fewer are open), and router_weights [T, k]."""
+    T, E = logits.shape
+    k = topk_ids.shape[-1]
+    lp, stride = _rows(logits, T, E, 4 if logits_dtype == "fp32" else 2, "logits")
+    _check(lib().moe_select_experts(lp, T, E, stride, WEIGHT_DTYPE[logits_dtype], k, SCORING[scoring],
+                                    1 if renormalize else 0, scale, _sized(topk_ids, T * k * 4, "topk_ids"),
+                                    _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2),
+                                           "router_weights"),
+                                    WEIGHT_DTYPE[weight_dtype], _stream(stream)),
+           "moe_select_experts")
+
+
+def linear_w4_args(x, w, w_scales, out, *, w_format="nvfp4", group_size=0, zeros=None, global_scale=1.0,
+                   io_dtype="bf16") -> MoeLinearW4Args:
+    """Fills a MoeLinearW4Args from tensors: x [M, K], w uint8 [N, K / 2], out [M, N]."""
+    M, K = x.shape
+    N = out.shape[-1]
+    xp, xs = _rows(x, M, K, 2, "x")
+    op, os_ = _rows(out, M, N, 2, "out")
+    sb, zb = _scale_bytes(w_format, group_size, N * K)
+    return MoeLinearW4Args(M, N, K, xp, xs, _sized(w, N * K // 2, "w"), _sized(w_scales, sb, "w_scales"),
+                           _sized(zeros, zb, "zeros"), global_scale, W_FORMAT[w_format], group_size,
+                           IO_DTYPE[io_dtype], op, os_)
+
+
+def moe_linear_w4(x, w, w_scales, out, *, stream=None, **kw) -> None:
+    """out [M, N] = x [M, K] W^T with W in 4 bits; M <= 64.  Keyword arguments
+    as in linear_w4_args()."""
+    _check(lib().moe_linear_w4(C.byref(linear_w4_args(x, w, w_scales, out, **kw)), _stream(stream)),
+           "moe_linear_w4")
+
+
+def moe_layer_workspace_size(T: int, top_k: int, I: int) -> int:
+    n = C.c_size_t(0)
+    _check(lib().moe_layer_workspace_size(T, top_k, I, C.byref(n)), "moe_layer_workspace_size")
+    return n.value
+
+
+def layer_args(*, x, topk_ids, router_weights, w13, w2, out, workspace, w13_scales=None, w2_scales=None,
+               w13_zeros=None, w2_zeros=None, w13_global=None, w2_global=None, w_format="none", group_size=0,
+               activation="silu", shared_out=None, residual=None, status=None, io_dtype="bf16",
+               weight_dtype="fp32") -> MoeLayerArgs:
+    """Fills a MoeLayerArgs from tensors.  E, H and I come from w2's shape
+    [E, H, I] (16-bit weights) or [E, H, I / 2] (4-bit codes)."""
+    T, H = x.shape
+    k = topk_ids.shape[-1]
+    E, h2, i2 = w2.shape
+    fmt = W_FORMAT[w_format]
+    inner = i2 if fmt == 0 else 2 * i2
+    if h2 != H:
+        raise ValueError(f"w2 has rows for H = {h2}; x has H = {H}")
+    xp, xs = _rows(x, T, H, 2, "x")
+    n2 = E * H * inner
+    s2, z2 = _scale_bytes(w_format, group_size, n2)
+    rows = T * H * 2
+    return MoeLayerArgs(
+        T, H, inner, E, k, xp, xs, _sized(topk_ids, T * k * 4, "topk_ids"),
+        _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2), "router_weights"),
+        _sized(w13, n2 * 4 if fmt == 0 else n2, "w13"), _sized(w13_scales, 2 * s2, "w13_scales"),
+        _sized(w13_zeros, 2 * z2, "w13_zeros"), _sized(w13_global, 4 * E, "w13_global"),
+        _sized(w2, n2 * 2 if fmt == 0 else n2 // 2, "w2"), _sized(w2_scales, s2, "w2_scales"),
+        _sized(w2_zeros, z2, "w2_zeros"), _sized(w2_global, 4 * E, "w2_global"),
+        _sized(shared_out, rows, "shared_out"), _sized(residual, rows, "residual"), _sized(out, rows, "out"),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _sized(status, 4, "status"),
+        fmt, group_size, ACTIVATION[activation], IO_DTYPE[io_dtype], WEIGHT_DTYPE[weight_dtype])
+
+
+def moe_layer(stream=None, **kw) -> None:
+    """Enqueues a whole expert layer for up to 64 tokens; keyword arguments as
+    in layer_args() (or args=, a MoeLayerArgs)."""
+    args = kw.pop("args", None) or layer_args(**kw)
+    _check(lib().moe_layer(C.byref(args), _stream(stream)), "moe_layer")
