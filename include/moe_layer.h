@@ -23,7 +23,8 @@ extern "C" {
 /* Limits of the few-token products (validated on the host). */
 #define MOE_FEW_TOKENS 64          /* rows of x of a linear, tokens of a layer */
 #define MOE_LAYER_MAX_EXPERTS 1024
-#define MOE_FEW_MAX_DIM 65536      /* K and N of a linear, H and I of a layer */
+#define MOE_FEW_MAX_DIM 65536      /* N of a linear, I of a layer */
+#define MOE_FEW_MAX_K 32768        /* K of a linear, H of a layer */
 
 /* How a weight matrix [rows, K] is held.  4-bit codes are packed two to a
  * byte, element 2i of a row in the low nibble of byte i, rows contiguous. */

@@ -123,6 +123,8 @@ SYMBOLS = {
 def lib() -> C.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -184,6 +186,22 @@ def _stream(stream):
         import torch
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
+
+
+_raw_stream = None  # torch's getter of a device's current stream as an integer
+
+
+def _stream_of(stream, t):
+    """_stream() for the few-token operators, whose kernels take a few
+    microseconds: the current stream of t's device without a Stream object."""
+    global _raw_stream
+    if stream is not None:
+        return getattr(stream, "cuda_stream", stream)
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(t.get_device())
 
 
 def _check(st: int, what: str):
@@ -361,7 +379,7 @@ def moe_select_experts(logits, topk_ids, router_weights, *, scoring="softmax", r
                                     1 if renormalize else 0, scale, _sized(topk_ids, T * k * 4, "topk_ids"),
                                     _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2),
                                            "router_weights"),
-                                    WEIGHT_DTYPE[weight_dtype], _stream(stream)),
+                                    WEIGHT_DTYPE[weight_dtype], _stream_of(stream, logits)),
            "moe_select_experts")
 
 
@@ -381,7 +399,7 @@ def linear_w4_args(x, w, w_scales, out, *, w_format="nvfp4", group_size=0, zeros
 def moe_linear_w4(x, w, w_scales, out, *, stream=None, **kw) -> None:
     """out [M, N] = x [M, K] W^T with W in 4 bits; M <= 64.  Keyword arguments
     as in linear_w4_args()."""
-    _check(lib().moe_linear_w4(C.byref(linear_w4_args(x, w, w_scales, out, **kw)), _stream(stream)),
+    _check(lib().moe_linear_w4(C.byref(linear_w4_args(x, w, w_scales, out, **kw)), _stream_of(stream, x)),
            "moe_linear_w4")
 
 
@@ -423,5 +441,8 @@ def layer_args(*, x, topk_ids, router_weights, w13, w2, out, workspace, w13_scal
 def moe_layer(stream=None, **kw) -> None:
     """Enqueues a whole expert layer for up to 64 tokens; keyword arguments as
     in layer_args() (or args=, a MoeLayerArgs)."""
-    args = kw.pop("args", None) or layer_args(**kw)
-    _check(lib().moe_layer(C.byref(args), _stream(stream)), "moe_layer")
+    args = kw.pop("args", None)
+    if args is not None:
+        _check(lib().moe_layer(C.byref(args), _stream(stream)), "moe_layer")
+    else:
+        _check(lib().moe_layer(C.byref(layer_args(**kw)), _stream_of(stream, kw["x"])), "moe_layer")

@@ -1,26 +1,40 @@
 // skinny.cuh -- products of a weight matrix with a few columns, the inner
 // loop of the 4-bit linear and of the few-token expert layer.
 //
-//   D[n, c] = sum_k W[n, k] X[c, k],   c < 8 NT columns (tokens)
+//   D[n, c] = sum_k W[n, k] X[c, k],   c < 8 columns (tokens)
 //
-// One warp computes 16 rows of W by 8 NT columns over a range of k with
+// One warp computes 16 rows of W by 8 columns over a range of k with
 // mma.sync m16n8k16: W is the 16-row operand, the tokens are the 8-column one,
 // and the sums stay in fp32.  The products are bound by the stream of W (a
-// weight is used for a handful of tokens), so the weights go from global
-// memory straight into the registers that the matrix instruction reads; no
-// shared memory and no barrier stands in between.
+// weight is used for a handful of tokens), so what counts is the bytes that
+// are in flight and the instructions spent on each weight.
 //
-// The order of k inside a step is free as long as both operands agree on it.
-// A lane (g = lane / 4, t = lane % 4) therefore loads consecutive elements of
-// the rows g and g + 8 with one wide load each, and the same elements of
-// column g, and feeds them to the instruction's k slots in that order:
-//   16-bit weights   8 elements a lane (16 bytes), a step of 32 k, 2 instructions
-//   4-bit weights   16 elements a lane (8 bytes), a step of 64 k, 4 instructions
+// In flight: a CTA has a ring of slots in shared memory.  A slot holds one
+// panel, 128 bytes of each of 16 rows for every warp of a group or two, and a
+// producer warp fills slots with tensor copies (TMA), as far ahead as the ring goes,
+// across the ends of row blocks.  The warps of a group share out the k of a
+// panel; several groups take different row blocks, so that enough warps are
+// there to hide each other's latencies.  (Tensor copies of 8 rows x 128 bytes x
+// strips reach 6.3 TB/s whatever the panel's width; a bulk copy for each row
+// costs about 80 cycles, 3.7 TB/s with rows of 1 KB.)
+//
+// Instructions: the columns are laid out in the order in which the matrix
+// instruction takes them, once for many rows.  Integers are widened to the
+// type of the columns, with one or-and and a half or three quarters of a shift
+// for two.  e2m1 codes take one conversion for two of them to fp16, and five
+// operations to bf16.  For bf16 columns that are used for many rows, the columns
+// are therefore held as fp16 times a power of two, chosen for each column and
+// each strip of k (256 elements) so that the largest magnitude lies in
+// [2^14, 2^15): every element down to 2^-29 of the largest keeps all its bits,
+// and a smaller one is off by at most 2^-40 of the largest, far below the
+// rounding of the fp32 sum that it goes into.
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>  // CUtensorMap only; no libcuda symbol is linked
 #include <cuda_runtime.h>
 
+#include "common.h"
 #include "ptx.cuh"
 
 namespace nqg {
@@ -38,9 +52,21 @@ struct WeightView {
 
 // ------------------------------------------------------------ instructions
 
-template <bool BF16>
+// d = a b + (FIRST ? 0 : d)
+template <bool BF16, bool FIRST = false>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
+    if constexpr (FIRST) {
+        if constexpr (BF16)
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+        else
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+        return;
+    }
     if constexpr (BF16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -51,29 +77,28 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Loads of weights: read once, so they do not displace the tokens in L1.
-__device__ __forceinline__ uint4 ldg_stream16(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ uint2 ldg_stream8(const void *p)
-{
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
-
 // Loads of columns: written by the kernel before, so they take the coherent path.
 __device__ __forceinline__ uint4 load_column(const void *p)
 {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
+}
+
+// A constant that the compiler does not see.
+__device__ __forceinline__ uint32_t opaque(uint32_t v)
+{
+    uint32_t r;
+    asm("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t c)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "n"(MASK), "r"(c));
+    return r;
 }
 
 template <bool BF16>
@@ -98,6 +123,13 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b)
     return r;
 }
 
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ float widen16(uint16_t v)
 {
@@ -119,99 +151,183 @@ __device__ __forceinline__ uint16_t narrow16(float f)
     return r;
 }
 
-// An e4m3 byte's value in fp16 (exact: 4 significant bits, exponents -9 to 8).
-__device__ __forceinline__ uint16_t e4m3_to_f16(uint32_t code)
-{
-    uint32_t r;
-    const uint16_t c = static_cast<uint16_t>(code);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
-    return static_cast<uint16_t>(r);
-}
-
 // ---------------------------------------------------------- weight formats
 //
-// A format loads one lane's slice of a row and turns it into the row's
-// operand registers, pairs[2 m] and pairs[2 m + 1] for instruction m, after
-// which scale_after (int4) multiplies the instruction's sums.
+// A strip is 128 bytes of each of 16 rows, what one warp takes of a panel; it
+// goes through it in kSteps steps of kMma instructions.  The order of k inside
+// a strip is free as long as both operands agree on it: in step u, lane
+// (g = lane / 4, t = lane % 4) takes kLane consecutive elements of the rows g
+// and g + 8 and of column g, from element at(u, t) of the strip on.
+//
+// Rows of a strip lie 128 bytes apart with their 16-byte chunks exchanged as
+// the 128-byte swizzle of the tensor copies does it: chunk i of row g is at
+// position i ^ g.  A lane's slices are chosen so that 8 lanes of two rows meet
+// all banks (16 lanes of 4 rows meet half of them with int4's 8-byte slices).
+//
+//   Slice    one lane's bytes of a row for all steps of the strip
+//   Scales   what it needs of the row's scales
+//   operand  p[2 i], p[2 i + 1]: the row's operand registers of instruction i
 
-template <int FMT, bool BF16>
+constexpr int kStripBytes = 128;
+
+// Consumer warps of a CTA: with the producer's 24, for 80 registers a thread,
+// or 20, for 96 (int4, which would spill).
+template <int FMT>
+constexpr int kMaxConsumers = FMT == kWInt4 ? 19 : 23;
+
+constexpr int kColumns = 8;
+
+// NATIVE: operands of the columns' type; otherwise nvfp4's are fp16.
+template <int FMT, bool BF16, bool NATIVE = false>
 struct Format;
 
-template <bool BF16>
-struct Format<kW16, BF16> {
-    static constexpr int kLane = 8;       // elements of a row that a lane holds in a step
-    static constexpr int kMma = 2;        // instructions in a step
-    static constexpr bool kSplit = false; // pairs are elements (j, j + 4) of 8, not (2 j, 2 j + 1)
-    static constexpr bool kAfter = false;
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds8(uint32_t at)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds4(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ uint16_t lds2(uint32_t at)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds1(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+
+// Where a slot's scales lie, from the start of the slot, and how.
+struct ScalePlace {
+    uint32_t at, pitch;        // scales of a row
+    uint32_t zero_at, zero_pitch;  // zero points, pitch 0: none
+};
+
+// How the slots of a ring are laid out.  A slot: its tiles, each rows 0 to 7 of
+// every strip of the panel, 1 KB each, then rows 8 to 15, then the scales; and
+// then columns, if any.
+struct SlotPlan {
+    int32_t warps;      // of a group
+    int32_t strips;     // of a panel: warp j takes strips j, j + warps, ...
+    int32_t tiles;      // of 16 rows in a slot
+    int32_t half;       // bytes of the strips of 8 rows
+    int32_t tile;       // bytes of a tile with its scales
+    ScalePlace scale;   // from the start of a tile
+    int32_t columns_at;
+    int32_t bytes;      // of a slot, a multiple of 1024
+    int32_t depth;      // slots of a group's ring
+};
+
+template <bool BF16, bool NATIVE>
+struct Format<kW16, BF16, NATIVE> {
     static constexpr float kPost = 1.0f;  // the sums are to be multiplied by this
+    static constexpr bool kHalf = !BF16;  // the operands are fp16
+    static constexpr int kStripK = 64, kSteps = 2, kLane = 8, kMma = 2;
+    static constexpr bool kSplit = false;  // columns: pairs are elements (j, j + 4) of 8, not (2 j, 2 j + 1)
+    static constexpr bool kAfter = false;  // scales multiply the sums of a step, not the operands
+    struct Scales {};
     struct Slice {
-        uint4 v;
+        uint4 v[2];
     };
-    struct Row {
-        const uint8_t *w;
-    };
-    __device__ static Row row(const WeightView &W, int64_t r)
+    __host__ __device__ static int row_bytes(int K) { return K * 2; }
+    __device__ static int at(int u, int t) { return 16 * t + 8 * u; }
+    __device__ static uint32_t scale_at(const ScalePlace &, int, int, int) { return 0; }
+    __device__ static void load_scales(Scales (&)[2], uint32_t, const SlotPlan &, const WeightView &, int, int, int) {}
+    __device__ static void load(Slice &s, uint32_t tile)  // tile: of the lane's row, at lane_at()
     {
-        return {W.w + r * W.K * 2};
+        s.v[0] = lds16(tile);
+        s.v[1] = lds16(tile ^ 16);
     }
-    __device__ static void load(Slice &s, const WeightView &, const Row &row, int k)
+    __device__ static uint32_t lane_at(int g, int t) { return g * kStripBytes + ((2 * t) ^ g) * 16; }
+    // Clears the elements from `left` of the strip on.
+    __device__ static void clear(Slice &s, Scales &, int left, int t)
     {
-        s.v = ldg_stream16(row.w + static_cast<int64_t>(k) * 2);
+        if (16 * t >= left)
+            s.v[0] = make_uint4(0, 0, 0, 0);
+        if (16 * t + 8 >= left)
+            s.v[1] = make_uint4(0, 0, 0, 0);
     }
-    __device__ static void none(Slice &s) { s.v = make_uint4(0, 0, 0, 0); }
-    __device__ static void pairs(const Slice &s, uint32_t (&p)[4])
+    __device__ static void operand(const Slice &s, const Scales &, int u, uint32_t (&p)[4])
     {
-        p[0] = s.v.x;
-        p[1] = s.v.y;
-        p[2] = s.v.z;
-        p[3] = s.v.w;
+        p[0] = s.v[u].x;
+        p[1] = s.v[u].y;
+        p[2] = s.v[u].z;
+        p[3] = s.v[u].w;
     }
 };
 
 // NVFP4: a weight is e2m1 x e4m3.  The product has at most 2 + 4 significant
-// bits, so it is exact in bf16 and fp16 and the scale is multiplied into the
-// operand: one instruction for two weights.
-template <bool BF16>
-struct Format<kWNvfp4, BF16> {
-    static constexpr int kLane = 16;
-    static constexpr int kMma = 4;
-    static constexpr bool kSplit = BF16;
+// bits and lies between 2^-10 and 2688, so it is exact in fp16 and the scale is
+// multiplied into the operand: one instruction for two weights.  Lane t takes
+// the elements 64 t to 64 t + 63 of a strip, so that the four scales that it
+// needs of a row are one word.
+template <bool BF16, bool NATIVE>
+struct Format<kWNvfp4, BF16, NATIVE> {
+    static constexpr bool kHalf = !(BF16 && NATIVE);
+    // bf16: a code's bits s, eem moved to bits 15 and 8..6 are the bf16 number
+    // value x 2^-126 (the subnormals included); the scale carries 2^100 of it
+    // back, which keeps it finite, and the sums the other 2^26.
+    static constexpr float kPost = kHalf ? 1.0f : 0x1p26f;
+    static constexpr int kStripK = 256, kSteps = 4, kLane = 16, kMma = 4;
+    static constexpr bool kSplit = !kHalf;
     static constexpr bool kAfter = false;
-    // bf16: an e2m1 code's bits s, eem moved to bits 15 and 8..6 are the bf16
-    // number value x 2^-126 (the subnormals included); the scale carries 2^100
-    // of it back, which keeps it finite, and the sums the other 2^26.
-    static constexpr float kPost = BF16 ? 0x1p26f : 1.0f;
+    struct Scales {
+        uint32_t codes;
+    };
     struct Slice {
-        uint2 v;
-        uint32_t scale;
+        uint4 v[2];
     };
-    struct Row {
-        const uint8_t *w, *s;
-    };
-    __device__ static Row row(const WeightView &W, int64_t r)
+    __host__ __device__ static int row_bytes(int K) { return K / 2; }
+    __device__ static int at(int u, int t) { return 64 * t + 16 * u; }
+    // Of row g and the panel's strip j, from the slot on; row g + 8 lies 8 rows further.
+    __device__ static uint32_t scale_at(const ScalePlace &pl, int g, int j, int t) { return pl.at + g * pl.pitch + 16 * j + 4 * t; }
+    __device__ static void load_scales(Scales (&s)[2], uint32_t at, const SlotPlan &plan, const WeightView &, int, int i, int)
     {
-        return {W.w + r * (W.K / 2), W.scales + r * (W.K / 16)};
+        s[0].codes = lds4(at + 16 * i);
+        s[1].codes = lds4(at + 16 * i + 8 * plan.scale.pitch);
     }
-    __device__ static void load(Slice &s, const WeightView &, const Row &row, int k)
+    __device__ static void load(Slice &s, uint32_t tile)  // tile: of the lane's row, at lane_at()
     {
-        s.v = ldg_stream8(row.w + (k >> 1));
-        s.scale = __ldg(row.s + (k >> 4));
+        s.v[0] = lds16(tile);
+        s.v[1] = lds16(tile ^ 16);
     }
-    __device__ static void none(Slice &s)
+    __device__ static uint32_t lane_at(int g, int t) { return g * kStripBytes + ((2 * t) ^ g) * 16; }
+    __device__ static void clear(Slice &s, Scales &sc, int left, int t)
     {
-        s.v = make_uint2(0, 0);
-        s.scale = 0;
+        const int groups = min(max((left - 64 * t) / 16, 0), 4);  // of this lane's four
+        sc.codes &= groups == 4 ? 0xFFFFFFFFu : (1u << (8 * groups)) - 1;
+        if (groups < 1)
+            s.v[0].x = s.v[0].y = 0;
+        if (groups < 2)
+            s.v[0].z = s.v[0].w = 0;
+        if (groups < 3)
+            s.v[1].x = s.v[1].y = 0;
+        if (groups < 4)
+            s.v[1].z = s.v[1].w = 0;
     }
     __device__ static void eight(uint32_t w, uint32_t scale, uint32_t *p)
     {
-        if constexpr (BF16) {
-            constexpr uint32_t kSign = 0x80008000u, kMag = 0x01C001C0u;
-            p[0] = mul2<true>(((w << 12) & kSign) | ((w << 6) & kMag), scale);
-            p[1] = mul2<true>(((w << 8) & kSign) | ((w << 2) & kMag), scale);
-            p[2] = mul2<true>(((w << 4) & kSign) | ((w >> 2) & kMag), scale);
-            p[3] = mul2<true>((w & kSign) | ((w >> 6) & kMag), scale);
-        } else {
-            uint32_t h[4];
+        uint32_t h[4];
+        if constexpr (kHalf) {
             asm("{ .reg .b8 b0, b1, b2, b3;\n"
                 "  mov.b32 {b0, b1, b2, b3}, %4;\n"
                 "  cvt.rn.f16x2.e2m1x2 %0, b0;\n"
@@ -220,170 +336,736 @@ struct Format<kWNvfp4, BF16> {
                 "  cvt.rn.f16x2.e2m1x2 %3, b3; }"
                 : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
                 : "r"(w));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                p[j] = mul2<false>(h[j], scale);
+        } else {  // the sum of two shifted copies is one multiplication, on the other pipe
+            const uint32_t v = w >> 8;
+            h[0] = ((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+            h[1] = ((w & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
+            h[2] = ((v & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
+            h[3] = ((v & 0x00F000F0u) * 0x0104u) & 0x81C081C0u;
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            p[j] = mul2<!kHalf>(h[j], scale);
     }
-    __device__ static void pairs(const Slice &s, uint32_t (&p)[8])
+    __device__ static void operand(const Slice &s, const Scales &sc, int u, uint32_t (&p)[8])
     {
-        uint32_t scale = e4m3_to_f16(s.scale);
-        if constexpr (BF16)
-            scale = narrow16<true>(widen16<false>(static_cast<uint16_t>(scale)) * 0x1p100f);
-        scale |= scale << 16;
-        eight(s.v.x, scale, p);
-        eight(s.v.y, scale, p + 4);
+        uint32_t two;  // the scales of steps 2 (u / 2) and the next
+        const uint16_t c = static_cast<uint16_t>(sc.codes >> (16 * (u >> 1)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(c));
+        uint32_t scale = __byte_perm(two, two, u & 1 ? 0x3232 : 0x1010);
+        if constexpr (!kHalf) {
+            const float f = widen16<false>(static_cast<uint16_t>(scale)) * 0x1p100f;
+            scale = f32x2_to_bf16x2(f, f);
+        }
+        eight(u & 1 ? s.v[u >> 1].z : s.v[u >> 1].x, scale, p);
+        eight(u & 1 ? s.v[u >> 1].w : s.v[u >> 1].y, scale, p + 4);
     }
 };
 
-// 4-bit integers: (code - zero) has at most 5 bits and is exact in bf16 and
-// fp16.  Times a 16-bit scale it would not be, so the scale multiplies the
-// fp32 sums of a step, all of whose k lie in one group (group % 64 == 0).
-// A nibble or-ed into the mantissa of 128 (bf16) or 1024 (fp16) is that
-// number plus the code.
-template <bool BF16>
-struct Format<kWInt4, BF16> {
-    static constexpr int kLane = 16;
-    static constexpr int kMma = 4;
+// 4-bit integers: code - zero has at most 5 bits and is exact in bf16 and fp16.
+// Times a 16-bit scale it would not be, so the scale multiplies the fp32 sums of
+// a step, all of whose k lie in one group (group % 64 == 0): lane t takes the
+// elements 16 t to 16 t + 15 of the step's 64.
+// A code in bits 3..0 of the mantissa of 128 (bf16) or 1024 (fp16) makes that
+// number plus the code, and in fp16 one in bits 7..4 makes 1024 + 16 code; either
+// less the zero point is one exact instruction.
+template <bool BF16, bool NATIVE>
+struct Format<kWInt4, BF16, NATIVE> {
+    static constexpr bool kHalf = !BF16;
+    static constexpr float kPost = 1.0f;
+    static constexpr int kStripK = 256, kSteps = 4, kLane = 16, kMma = 4;
     static constexpr bool kSplit = true;
     static constexpr bool kAfter = true;
-    static constexpr float kPost = 1.0f;
-    static constexpr uint32_t kMagic = BF16 ? 0x43004300u : 0x64006400u;
-    struct Slice {
-        uint2 v;
-        uint32_t zero;
-        uint16_t scale;
+    struct Scales {
+        uint32_t scale[2];  // two steps' in a word
+        uint32_t zero;      // a byte for each step
     };
-    struct Row {
-        const uint8_t *w, *s, *z;
+    struct Slice {  // read step by step
+        uint32_t at;
     };
-    __device__ static Row row(const WeightView &W, int64_t r)
+    __host__ __device__ static int row_bytes(int K) { return K / 2; }
+    __device__ static int at(int u, int t) { return 64 * u + 16 * t; }
+    // the row alone: scales and zero points have pitches of their own
+    __device__ static uint32_t scale_at(const ScalePlace &, int g, int, int) { return g; }
+    // strip: of the row, i of the panel; from: the panel's first element.  A strip starts with a
+    // group, or inside one of 512 and more.  What is read for steps past the end
+    // is cleared later.
+    __device__ static void load_scales(Scales (&s)[2], uint32_t at, const SlotPlan &plan, const WeightView &W, int strip, int, int from)
     {
-        const int64_t groups = W.K >> W.group_shift;
-        return {W.w + r * (W.K / 2), W.scales + r * groups * 2, W.zeros ? W.zeros + r * groups : nullptr};
-    }
-    __device__ static void load(Slice &s, const WeightView &W, const Row &row, int k)
-    {
-        s.v = ldg_stream8(row.w + (k >> 1));
-        const int grp = k >> W.group_shift;
-        s.scale = __ldg(reinterpret_cast<const uint16_t *>(row.s) + grp);
-        s.zero = row.z ? __ldg(row.z + grp) : 8u;
-    }
-    __device__ static void none(Slice &s)
-    {
-        s.v = make_uint2(0, 0);
-        s.zero = 0;
-        s.scale = 0;
-    }
-    __device__ static void pairs(const Slice &s, uint32_t (&p)[8])
-    {
-        const uint32_t zero = kMagic | (s.zero & 15u) * 0x00010001u;
+        const int shift = W.group_shift, first = ((strip * kStripK) >> shift) - (from >> shift);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            p[j] = sub2<BF16>(((s.v.x >> (4 * j)) & 0x000F000Fu) | kMagic, zero);
-            p[4 + j] = sub2<BF16>(((s.v.y >> (4 * j)) & 0x000F000Fu) | kMagic, zero);
-        }
-    }
-    __device__ static float scale_after(const Slice &s) { return widen16<BF16>(s.scale); }
-};
-
-// ------------------------------------------------------------- the product
-
-// A lane's slice of a column: kLane consecutive 16-bit elements.
-template <int N>
-struct ColumnSlice {
-    uint4 v[N / 8];
-};
-
-template <class F>
-__device__ __forceinline__ void column_pairs(const ColumnSlice<F::kLane> &c, uint32_t (&b)[F::kLane / 2])
-{
-#pragma unroll
-    for (int h = 0; h < F::kLane / 8; ++h) {
-        const uint4 v = c.v[h];
-        if constexpr (F::kSplit) {
-            b[4 * h + 0] = __byte_perm(v.x, v.z, 0x5410);
-            b[4 * h + 1] = __byte_perm(v.x, v.z, 0x7632);
-            b[4 * h + 2] = __byte_perm(v.y, v.w, 0x5410);
-            b[4 * h + 3] = __byte_perm(v.y, v.w, 0x7632);
-        } else {
-            b[4 * h + 0] = v.x;
-            b[4 * h + 1] = v.y;
-            b[4 * h + 2] = v.z;
-            b[4 * h + 3] = v.w;
-        }
-    }
-}
-
-// acc[nt] += W[rows of this lane, k0..k1) x columns, for the tiles of columns
-// nt < tiles (the same for every lane).  `lo` and `hi` are rows g and g + 8,
-// col[nt] the lane's column g of tile nt; a row or column past the end points
-// at any valid one and its sums are ignored.  k0 is a multiple of the step and
-// k1 of a lane's slice; past k1 the slices are zero.
-template <class F, bool BF16, int NT, int U>
-__device__ __forceinline__ void skinny_product(float (&acc)[NT][4], const WeightView &W, const typename F::Row &lo,
-                                               const typename F::Row &hi, const uint16_t *const (&col)[NT], int tiles,
-                                               int k0, int k1, int lane)
-{
-    constexpr int kStep = 4 * F::kLane;
-    const int own = (lane & 3) * F::kLane;
-    for (int k = k0 + own; k < k1 + own; k += U * kStep) {
-        typename F::Slice a[U][2];
-        ColumnSlice<F::kLane> b[U][NT];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int ku = k + u * kStep;
-            if (ku < k1) {
-                F::load(a[u][0], W, lo, ku);
-                F::load(a[u][1], W, hi, ku);
+        for (int h = 0; h < 2; ++h) {
+            const int r = (at & 7) + 8 * h;  // tiles are 1024-byte aligned
+            const uint32_t a = (at & ~7u) + plan.scale.at + 2 * first + r * plan.scale.pitch;
+            const uint32_t z = (at & ~7u) + plan.scale.zero_at + first + r * plan.scale.zero_pitch;
+            s[h].zero = 0x08080808u;
+            if (shift == 6) {  // four groups
+                const uint2 v = lds8(a);
+                s[h].scale[0] = v.x;
+                s[h].scale[1] = v.y;
+                if (plan.scale.zero_pitch)
+                    s[h].zero = lds4(z);
+            } else if (shift == 7) {
+                const uint32_t v = lds4(a);
+                s[h].scale[0] = __byte_perm(v, v, 0x1010);
+                s[h].scale[1] = __byte_perm(v, v, 0x3232);
+                if (plan.scale.zero_pitch)
+                    s[h].zero = __byte_perm(lds2(z), 0, 0x1100);
             } else {
-                F::none(a[u][0]);
-                F::none(a[u][1]);
+                const uint32_t v = lds2(a);
+                s[h].scale[0] = s[h].scale[1] = __byte_perm(v, v, 0x1010);
+                if (plan.scale.zero_pitch)
+                    s[h].zero = __byte_perm(lds1(z), 0, 0x0000);
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < F::kLane / 8; ++i)
-                    b[u][nt].v[i] = nt < tiles && ku < k1 ? load_column(col[nt] + ku + 8 * i)
-                                                          : make_uint4(0, 0, 0, 0);
+            s[h].zero &= 0x0F0F0F0Fu;
         }
+    }
+    __device__ static void load(Slice &s, uint32_t tile) { s.at = tile; }
+    __device__ static uint32_t lane_at(int g, int t) { return g * kStripBytes + ((t >> 1) ^ g) * 16 + (t & 1) * 8; }
+    // Past the end the columns are zero, and codes are finite whatever they are.
+    __device__ static void clear(Slice &, Scales &sc, int left, int)
+    {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            uint32_t p[2][F::kLane / 2];
-            F::pairs(a[u][0], p[0]);
-            F::pairs(a[u][1], p[1]);
+        for (int u = 0; u < 4; ++u)
+            if (64 * u >= left)
+                sc.scale[u >> 1] &= u & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+    __device__ static void operand(const Slice &s, const Scales &sc, int u, uint32_t (&p)[8])
+    {
+        // in a register, so that and and or are one instruction
+        const uint32_t base = opaque(BF16 ? 0x43004300u : 0x64006400u);
+        const uint32_t less = __byte_perm(sc.zero, 0, 0x4040 + 0x0101 * u) | base;  // 128 or 1024, + zero
+        const uint2 w8 = lds8(s.at ^ (32 * u));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (nt >= tiles)
-                    continue;
-                uint32_t q[F::kLane / 2];
-                column_pairs<F>(b[u][nt], q);
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
-                float(&d)[4] = F::kAfter ? part : acc[nt];
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w = h ? w8.y : w8.x;
+            if constexpr (BF16) {
 #pragma unroll
-                for (int m = 0; m < F::kMma; ++m) {
-                    const uint32_t frag[4] = {p[0][2 * m], p[1][2 * m], p[0][2 * m + 1], p[1][2 * m + 1]};
-                    mma16816<BF16>(d, frag, q[2 * m], q[2 * m + 1]);
+                for (int i = 0; i < 4; ++i)
+                    p[4 * h + i] = sub2<true>(and_or<0x000F000Fu>(w >> (4 * i), base), less);
+            } else {
+                constexpr uint32_t kSixteenth = 0x2C002C00u;
+                const uint32_t less16 = sub2<false>(0x63806380u, less);  // 960 - 1024 - zero
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t v = b ? w >> 8 : w;
+                    p[4 * h + 2 * b] = sub2<false>(and_or<0x000F000Fu>(v, base), less);
+                    p[4 * h + 2 * b + 1] = fma_f16x2(and_or<0x00F000F0u>(v, base), kSixteenth, less16);
                 }
-                if constexpr (F::kAfter) {
-                    const float slo = F::scale_after(a[u][0]), shi = F::scale_after(a[u][1]);
-                    acc[nt][0] = fmaf(slo, part[0], acc[nt][0]);
-                    acc[nt][1] = fmaf(slo, part[1], acc[nt][1]);
-                    acc[nt][2] = fmaf(shi, part[2], acc[nt][2]);
-                    acc[nt][3] = fmaf(shi, part[3], acc[nt][3]);
+            }
+        }
+    }
+    __device__ static float scale_after(const Scales &s, int u) { return widen16<BF16>(static_cast<uint16_t>((u & 2 ? s.scale[1] : s.scale[0]) >> (16 * (u & 1)))); }
+};
+
+template <class F>
+__host__ __device__ inline int strips_of(int K)
+{
+    return (K + F::kStripK - 1) / F::kStripK;
+}
+
+// sums = (FRESH) or += 16 rows of a strip x n columns.  tile: the lane's
+// row g of the strip, at lane_at(); row g + 8 lies `half` bytes further.
+// column: the lane's, at column_at(); scales: of the two rows; left: elements of
+// the strip that the matrix has.  A row or column past the end is any valid one
+// or zero, and its sums are ignored.
+template <class F, bool BF16, bool FRESH>
+__device__ __forceinline__ void strip_product(float (&sums)[4], uint32_t tile, uint32_t half, uint32_t column, uint32_t swap,
+                                              typename F::Scales (&sc)[2], int left, int t)
+{
+    typename F::Slice a, b;
+    F::load(a, tile);
+    F::load(b, tile + half);
+    if (left < F::kStripK) {
+        F::clear(a, sc[0], left, t);
+        F::clear(b, sc[1], left, t);
+    }
+    const uint32_t even = column + swap, odd = column - swap;
+    constexpr int kAtOnce = F::kAfter ? 2 : F::kSteps;  // fewer registers where the scales take some
+#pragma unroll kAtOnce
+    for (int u = 0; u < F::kSteps; ++u) {
+        uint32_t p[F::kLane / 2], q[F::kLane / 2], c[F::kLane / 2];
+#pragma unroll
+        for (int h = 0; h < F::kLane / 8; ++h) {
+            const int i = u * (F::kLane / 8) + h;
+            const uint4 v = lds16((i & 1 ? odd : even) + i * 64);
+            c[4 * h] = v.x;
+            c[4 * h + 1] = v.y;
+            c[4 * h + 2] = v.z;
+            c[4 * h + 3] = v.w;
+        }
+        F::operand(a, sc[0], u, p);
+        F::operand(b, sc[1], u, q);
+        float part[4];
+        float(&d)[4] = F::kAfter ? part : sums;
+#pragma unroll
+        for (int m = 0; m < F::kMma; ++m) {
+            const uint32_t frag[4] = {p[2 * m], q[2 * m], p[2 * m + 1], q[2 * m + 1]};
+            if (m == 0 && (F::kAfter || (FRESH && u == 0)))
+                mma16816<!F::kHalf, true>(d, frag, c[2 * m], c[2 * m + 1]);
+            else
+                mma16816<!F::kHalf>(d, frag, c[2 * m], c[2 * m + 1]);
+        }
+        if constexpr (F::kAfter) {
+            const float slo = F::scale_after(sc[0], u), shi = F::scale_after(sc[1], u);
+            const bool first = FRESH && u == 0;
+            sums[0] = first ? slo * part[0] : fmaf(slo, part[0], sums[0]);
+            sums[1] = first ? slo * part[1] : fmaf(slo, part[1], sums[1]);
+            sums[2] = first ? shi * part[2] : fmaf(shi, part[2], sums[2]);
+            sums[3] = first ? shi * part[3] : fmaf(shi, part[3], sums[3]);
+        }
+    }
+}
+
+// ------------------------------------------------------------- the columns
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Eight bf16 values times `by` as fp16.
+__device__ __forceinline__ uint4 scale_to_f16(uint4 v, float by)
+{
+    const auto two = [by](uint32_t w) {
+        float lo, hi;
+        bf16x2_to_f32(w, lo, hi);
+        return f32x2_to_f16x2(lo * by, hi * by);
+    };
+    return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+}
+
+// The largest finite magnitude of two bf16 values, as its bits, and `most`.
+__device__ __forceinline__ uint32_t largest_bf16(uint32_t w, uint32_t most)
+{
+    const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
+    most = lo < 0x7F80u ? max(most, lo) : most;
+    return hi < 0x7F80u ? max(most, hi) : most;
+}
+
+__device__ __forceinline__ uint32_t largest_bf16(uint4 v, uint32_t most)
+{
+    return largest_bf16(v.x, largest_bf16(v.y, largest_bf16(v.z, largest_bf16(v.w, most))));
+}
+
+// The exponent s for which a largest magnitude with bits `most` times 2^s lies
+// in [2^14, 2^15), as far as 2^s and 2^-s are normal floats.
+__device__ __forceinline__ int column_exponent(uint32_t most)
+{
+    return most ? min(14 + 127 - static_cast<int>(most >> 7), 126) : 0;
+}
+
+// Shared memory of `n` columns of `strips` strips.
+template <class F>
+__host__ __device__ constexpr int column_bytes(int n, int strips)
+{
+    return n * strips * F::kStripK * 2;
+}
+
+// Where a lane's column lies in a strip: in pieces of 64 bytes for the four
+// lanes of a column, odd columns' pieces exchanged in pairs, so that two columns
+// meet all banks.  `swap`: what is added for even pieces and taken off for odd.
+// odd: column 0 counts as odd; size: bytes from column to column.
+template <class F>
+__device__ __forceinline__ uint32_t column_at(int n, int lane, uint32_t &swap, int odd = 0, uint32_t size = F::kStripK * 2)
+{
+    const int c = min(lane >> 2, n - 1);
+    swap = ((c + odd) & 1) * 64;
+    return c * size + (lane & 3) * 16;
+}
+
+// Where the i-th eight consecutive elements of a strip lie in its column, in
+// bytes; odd: of an odd column.
+template <class F>
+__host__ __device__ __forceinline__ int piece_at(int i, int odd)
+{
+    // element k of a strip is lane tt's in step u, at(u, tt) + (0, 8)
+    const int k = 8 * i;
+    int u, tt, half;
+    if constexpr (F::kLane == 8) {
+        u = (k >> 3) & 1;
+        tt = k >> 4;
+        half = 0;
+    } else {
+        half = (k >> 3) & 1;
+        u = F::kAfter ? k >> 6 : (k >> 4) & 3;
+        tt = F::kAfter ? (k >> 4) & 3 : k >> 6;
+    }
+    return ((u * (F::kLane / 8) + half) ^ odd) * 64 + tt * 16;
+}
+
+// Where element r of such eight lies, in elements.
+template <class F>
+__device__ __forceinline__ int element_at(int r)
+{
+    return F::kSplit ? 2 * (r & 3) + (r >> 2) : r;
+}
+
+// Whether columns are held times a power of two.
+template <class F, bool BF16>
+constexpr bool kScaled = BF16 && F::kHalf;
+
+// Lays out the strips first, first + step, ... of columns [0, n) of K elements,
+// zero past K; strip s comes to columns + s * column_bytes(n, 1).  column(c):
+// where column c lies in global memory.  factors[8 s + c]: what the sums of the
+// strip's column c have to be multiplied by, a power of two over `divisor`
+// (kScaled).  One warp: it copies all its strips as they are, at once, and then
+// rearranges each in place.
+template <class F, bool BF16, class Column>
+__device__ __forceinline__ void lay_out_strips(uint32_t columns, float *factors, Column column, int n, int first, int step,
+                                               int K, float divisor, int lane)
+{
+    constexpr int kPieces = F::kStripK / 8;  // of a strip's column, 8 elements each
+    constexpr int kAtOnce = 32 / kPieces;    // columns
+    const int strips = strips_of<F>(K), i = lane % kPieces;
+    for (int s = first; s < strips; s += step) {
+        const int k = s * F::kStripK + 8 * i;
+        const uint32_t to = columns + s * column_bytes<F>(n, 1) + 16 * lane;
+        for (int c = lane / kPieces; c < n; c += kAtOnce)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (c - lane / kPieces) * (F::kStripK * 2)),
+                         "l"(column(c) + (k < K ? k : 0)), "r"(k < K ? 16 : 0)
+                         : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    for (int s = first; s < strips; s += step) {
+        const uint32_t strip = columns + s * column_bytes<F>(n, 1);
+        for (int c0 = 0; c0 < n; c0 += kAtOnce) {
+            const int c = c0 + lane / kPieces;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (c < n)
+                v = lds16(strip + c0 * (F::kStripK * 2) + 16 * lane);
+            if constexpr (kScaled<F, BF16>) {  // a column is 32 lanes' pieces
+                const int e = column_exponent(__reduce_max_sync(0xFFFFFFFFu, largest_bf16(v, 0)));
+                v = scale_to_f16(v, pow2(e));
+                if (lane == 0)
+                    factors[s * kColumns + c] = pow2(-e) / divisor;
+            }
+            __syncwarp();
+            if constexpr (F::kSplit)
+                v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                               __byte_perm(v.y, v.w, 0x7632));
+            if (c < n)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(strip + c * (F::kStripK * 2) + piece_at<F>(i, c & 1)),
+                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
+        }
+    }
+    __syncwarp();
+}
+
+// A global scale g divides the sums in two places.  g >= 1 comes with the
+// columns' factors, which are far from overflow there although the sums times
+// a factor alone may not be; g < 1 comes last, where an overflow is the result's.
+__device__ __forceinline__ float early(float g) { return g >= 1.0f ? g : 1.0f; }
+__device__ __forceinline__ float late(float g) { return g >= 1.0f ? 1.0f : g; }
+
+// A warp's sums to shared memory, [8 columns][16 rows].
+__device__ __forceinline__ void store_sums(float *to, const float (&acc)[4], int lane)
+{
+    const int g = lane >> 2, t = lane & 3;
+    to[2 * t * 16 + g] = acc[0];
+    to[(2 * t + 1) * 16 + g] = acc[1];
+    to[2 * t * 16 + g + 8] = acc[2];
+    to[(2 * t + 1) * 16 + g + 8] = acc[3];
+}
+
+// ----------------------------------------------------------------- the ring
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+// The tensor copies of a matrix.
+struct WeightMaps {
+    CUtensorMap panels;  // [row][strip of the whole strips][128 bytes]: 8 rows x a panel's strips
+    CUtensorMap strips;  // [row][byte]: 8 rows x 128 bytes, zero past the end of a row
+    CUtensorMap scales;  // [row][byte of scales]: 8 rows x a panel's
+    CUtensorMap zeros;   // int4: likewise
+    int32_t tensor;        // rows are multiples of 16 bytes: the copies above; 0: 8-byte copies
+    int32_t whole;         // whole strips of a row
+    int32_t scale_tensor;  // the scales (and zero points, if any) of a panel are multiples of 16 bytes
+    int32_t by_hand;       // lanes' own copies come with every slot
+    uint32_t scale_bytes;  // of a panel's tensor copies of scales and zero points
+};
+
+// A position in a ring.  Every group of consumers has a ring of its own: a slot
+// that went from one group to another would let a group mistake the phase
+// before the other's for the one that it waits for.
+struct RingAt {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int depth)
+    {
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+constexpr int kMaxGroups = 8;
+
+// Barriers of a slot: full, then empty, 8 bytes each.
+constexpr int kBarrierBytes = 16;
+
+__device__ __forceinline__ void tensor_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+                     "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tensor_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+                     "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+
+// Copies `bytes` from src(r) for r < 16 to dst + r * pitch, by one warp, two
+// lanes a row: in asynchronous pieces of 16, 8 or 4 bytes, as the alignment of
+// every row allows (`align`: all addresses and `bytes` or-ed together), or
+// else byte by byte at once.
+template <class Source>
+__device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, Source src, int bytes, uintptr_t align, int lane)
+{
+    const int r = lane >> 1, odd = lane & 1;
+    const uint8_t *from = src(r);
+    const uint32_t to = dst + r * pitch;
+    if (align % 16 == 0) {
+        for (int b = 16 * odd; b < bytes; b += 32)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + b), "l"(from + b) : "memory");
+    } else if (align % 8 == 0) {
+        for (int b = 8 * odd; b < bytes; b += 16)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + b), "l"(from + b) : "memory");
+    } else if (align % 4 == 0) {
+        for (int b = 4 * odd; b < bytes; b += 8)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + b), "l"(from + b) : "memory");
+    } else {
+#pragma unroll 4
+        for (int b = odd; b < bytes; b += 2) {
+            const uint32_t v = __ldg(from + b);
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + b), "r"(v) : "memory");
+        }
+    }
+}
+
+// Arrivals that make a slot full: one with the tensor copies' bytes, and every
+// lane's when its own copies have landed, if the producer's lanes make any.
+__host__ __device__ inline int fill_arrivals(const WeightMaps &maps) { return maps.by_hand ? 33 : 1; }
+
+// The tensor copies into one slot of panel `panel` of the rows from lo on and
+// of those from hi on, 8 each, and of the tiles 16 rows further; `more` bytes
+// come by other copies.  One thread.
+template <class F, int FMT>
+__device__ __forceinline__ void fill_by_tensor(uint32_t slot, uint32_t full, const SlotPlan &plan, const WeightView &W,
+                                               const WeightMaps &maps, int panel, int lo, int hi, uint32_t more)
+{
+    const int strip = panel * plan.strips;
+    const bool by_panel = strip + plan.strips <= maps.whole || maps.whole * kStripBytes == F::row_bytes(W.K);
+    const int here = by_panel ? plan.strips : min(plan.strips, (F::row_bytes(W.K) + kStripBytes - 1) / kStripBytes - strip);
+    mbar_arrive_expect_tx(full, plan.tiles * ((maps.tensor ? 2048 * here : 0) + maps.scale_bytes) + more);
+    for (int tile = 0; tile < plan.tiles; ++tile, slot += plan.tile, lo += 16, hi += 16) {
+        if (maps.tensor) {
+            if (by_panel) {
+                tensor_3d(slot, &maps.panels, 0, lo, strip, full);
+                tensor_3d(slot + plan.half, &maps.panels, 0, hi, strip, full);
+            } else {
+                for (int i = 0; i < here; ++i) {
+                    tensor_2d(slot + i * 1024, &maps.strips, (strip + i) * kStripBytes, lo, full);
+                    tensor_2d(slot + plan.half + i * 1024, &maps.strips, (strip + i) * kStripBytes, hi, full);
                 }
+            }
+        }
+        if (FMT != kW16 && maps.scale_tensor) {
+            const int x = panel * plan.scale.pitch;
+            tensor_2d(slot + plan.scale.at, &maps.scales, x, lo, full);
+            tensor_2d(slot + plan.scale.at + 8 * plan.scale.pitch, &maps.scales, x, hi, full);
+            if (FMT == kWInt4 && plan.scale.zero_pitch) {
+                const int z = panel * plan.scale.zero_pitch;
+                tensor_2d(slot + plan.scale.zero_at, &maps.zeros, z, lo, full);
+                tensor_2d(slot + plan.scale.zero_at + 8 * plan.scale.zero_pitch, &maps.zeros, z, hi, full);
             }
         }
     }
 }
 
-// A product's sum times kPost and divided by the global scale g.  For g >= 1
-// the quotient is taken first: a sum near the largest float may not survive
-// kPost alone.  For g < 1 that would mean that the result overflows too.
-template <class F>
-__device__ __forceinline__ float descale(float sum, float g)
+// What tensor copies cannot bring, by the lanes of one warp; rows from `rows`
+// on are past the end of the matrix, and the last row stands in for them.
+template <class F, int FMT>
+__device__ __forceinline__ void fill_by_hand(uint32_t slot, uint32_t full, const SlotPlan &plan, const WeightView &W,
+                                             const WeightMaps &maps, int panel, int lo, int hi, int rows, int lane)
 {
-    return g >= 1.0f ? sum * (F::kPost / g) : sum * F::kPost / g;
+    const int strip = panel * plan.strips;
+    for (int tile = 0; tile < plan.tiles; ++tile, slot += plan.tile, lo += 16, hi += 16) {
+        const auto row = [&](int r) { return static_cast<int64_t>(min((r & 8 ? hi : lo) + (r & 7), rows - 1)); };
+        if (!maps.tensor) {
+            const int row_bytes = F::row_bytes(W.K), r = lane >> 1, bytes = min(plan.strips * kStripBytes, row_bytes - strip * kStripBytes);
+            const uint8_t *from = W.w + row(r) * row_bytes + strip * kStripBytes;
+            const uint32_t to = slot + (r >> 3) * plan.half + (r & 7) * kStripBytes;
+            for (int b = 8 * (lane & 1); b < bytes; b += 16)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + b / kStripBytes * 1024 +
+                                                                              (((b % kStripBytes) >> 4 ^ (r & 7)) << 4) + (b & 8)),
+                             "l"(from + b)
+                             : "memory");
+        }
+        if (FMT != kW16 && !maps.scale_tensor) {
+            const int shift = FMT == kWNvfp4 ? 4 : W.group_shift, size = FMT == kWNvfp4 ? 1 : 2;
+            const int groups = W.K >> shift, k0 = strip * F::kStripK, k1 = min(k0 + plan.strips * F::kStripK, W.K);
+            const int g0 = k0 >> shift, n = ((k1 - 1) >> shift) + 1 - g0;
+            copy_rows(slot + plan.scale.at, plan.scale.pitch, [&](int r) { return W.scales + (row(r) * groups + g0) * size; },
+                      size * n, reinterpret_cast<uintptr_t>(W.scales) | size * groups | size * g0 | size * n, lane);
+            if (FMT == kWInt4 && plan.scale.zero_pitch)
+                copy_rows(slot + plan.scale.zero_at, plan.scale.zero_pitch, [&](int r) { return W.zeros + row(r) * groups + g0; },
+                          n, reinterpret_cast<uintptr_t>(W.zeros) | groups | g0 | n, lane);
+        }
+    }
+    // what was copied at once is visible to whoever sees the arrival; the asynchronous copies arrive by themselves
+    __threadfence_block();
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p;\n"
+                 "  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 "  selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
+// The producer warp's work.  Lane g keeps group g's ring filled from items,
+// which are the lane's own:
+//   bool next(panel, lo, hi)     the panel and the rows of the next slot, or false at the end
+//   uint32_t column_bytes()      what the slot also holds, by bulk copies of columns(slot, bar)
+// The lanes go side by side, so that the producer's instructions are shared by
+// the groups' slots, but none waits for another: groups meet at barriers, and a
+// group may need more slots before it gets there while another's ring is full.
+// Copies by hand take the whole warp and go group by group.  Weights may be
+// read from the start; columns (COLUMNS) and, if !COLUMNS, everything only after
+// the kernel before: the caller has waited for it unless COLUMNS.
+// `limit`: slots that lane 0 fills at most.
+template <class F, int FMT, bool COLUMNS, class Items>
+__device__ __forceinline__ void produce(Items items, int groups, uint32_t slots, uint32_t bars, const SlotPlan &plan,
+                                        const WeightView &W, const WeightMaps &maps, int rows, int64_t limit, int lane)
+{
+    RingAt at;
+    const uint32_t ring = slots + lane * plan.depth * plan.bytes, ring_bars = bars + lane * plan.depth * kBarrierBytes;
+    int panel = 0, lo = 0, hi = 0;
+    bool more = lane < groups && !(lane == 0 && limit <= 0);
+    if constexpr (COLUMNS) {
+        if (maps.by_hand) {
+            grid_dependency_wait();
+            more = more && items.next(panel, lo, hi);
+        } else {
+            // the weights of the rings' slots first, and their columns when these are there
+            Items columns = items;
+            int primed = 0;
+            while (more && (more = items.next(panel, lo, hi)) && primed < plan.depth) {
+                fill_by_tensor<F, FMT>(ring + primed * plan.bytes, ring_bars + primed * kBarrierBytes, plan, W, maps, panel, lo, hi,
+                                       items.column_bytes());
+                ++primed;
+            }
+            __syncwarp();
+            grid_dependency_wait();
+            for (int i = 0; i < primed; ++i) {
+                int x, y, z;
+                columns.next(x, y, z);
+                columns.columns(ring + i * plan.bytes, ring_bars + i * kBarrierBytes);
+                at.next(plan.depth);
+            }
+        }
+    } else {
+        more = more && items.next(panel, lo, hi);
+    }
+    uint64_t since = 0;  // when the last slot was filled, or 0: just now
+    while (__any_sync(0xFFFFFFFFu, more)) {
+        const uint32_t bar = ring_bars + at.slot * kBarrierBytes, slot = ring + at.slot * plan.bytes;
+        const bool ready = more && mbar_test(bar + 8, at.phase ^ 1);
+        uint32_t filled = __ballot_sync(0xFFFFFFFFu, ready);
+        if (!filled) {
+            const uint64_t now = globaltimer_ns();
+            if (since == 0)
+                since = now;
+            else if (now - since > kWaitLimitNs)
+                break;
+            __nanosleep(32);
+            continue;
+        }
+        since = 0;
+        if (ready) {
+            uint32_t bytes = 0;
+            if constexpr (COLUMNS)
+                bytes = items.column_bytes();
+            fill_by_tensor<F, FMT>(slot, bar, plan, W, maps, panel, lo, hi, bytes);
+            if constexpr (COLUMNS)
+                items.columns(slot, bar);
+        }
+        if (maps.by_hand)
+            for (; filled; filled &= filled - 1) {
+                const int g = __ffs(filled) - 1;
+                fill_by_hand<F, FMT>(__shfl_sync(0xFFFFFFFFu, slot, g), __shfl_sync(0xFFFFFFFFu, bar, g), plan, W, maps,
+                                     __shfl_sync(0xFFFFFFFFu, panel, g), __shfl_sync(0xFFFFFFFFu, lo, g),
+                                     __shfl_sync(0xFFFFFFFFu, hi, g), rows, lane);
+            }
+        if (ready) {
+            at.next(plan.depth);
+            more = !(lane == 0 && --limit <= 0) && items.next(panel, lo, hi);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Waits of the consumers.  Once one has run out (after two seconds, which no
+// healthy launch comes near) the warp goes through the rest of its work
+// without waiting, so that barriers still match, and the results are marked.
+struct Patience {
+    volatile int32_t *failed;  // shared memory
+    bool gone = false;
+    __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity)
+    {
+        if (!gone && !mbar_wait_bounded(bar, parity, kWaitLimitNs)) {
+            gone = true;
+            *failed = 1;
+        }
+    }
+};
+
+// A consumer warp at its group's ring: it takes strips j, j + warps, ... of
+// every panel for one of the slot's tiles.
+template <class F, int FMT, bool BF16>
+struct Consumer {
+    const SlotPlan &plan;
+    const WeightView &W;
+    Patience patience;
+    uint32_t slot, bar;           // addresses of the next slot and its barriers
+    int at = 0;                   // its place in the ring
+    uint32_t phase = 0;
+    uint32_t tile_at, scale_at;   // the lane's in the panel's first strip, from a slot on
+    int j, t;
+
+    __device__ Consumer(const SlotPlan &p, const WeightView &w, volatile int32_t *failed, uint32_t ring, uint32_t ring_bars, int tile,
+                        int j_, int lane)
+        : plan(p), W(w), patience{failed}, slot(ring), bar(ring_bars), j(j_), t(lane & 3)
+    {
+        tile_at = tile * p.tile + F::lane_at(lane >> 2, t);
+        scale_at = tile * p.tile + F::scale_at(p.scale, lane >> 2, 0, t);
+    }
+
+    __device__ __forceinline__ void wait() { patience.wait(bar, phase); }
+
+    // The next slot, which holds panel `panel` and has been waited for: sums +=
+    // its strips of this warp x columns.  column, swap: from column_at, in the
+    // panel's first strip, strip_size bytes from strip to strip; factors: of the
+    // panel's first strip's columns (SCALED), by which a strip's sums are
+    // multiplied.  Gives the slot back.
+    template <bool SCALED>
+    __device__ __forceinline__ void take(float (&sums)[4], int panel, uint32_t column, uint32_t strip_size, uint32_t swap,
+                                         uint32_t factors)
+    {
+        const int first = panel * plan.strips, from = first * F::kStripK;
+#pragma unroll 1
+        for (int i = j; i < plan.strips; i += plan.warps) {
+            const int left = W.K - (first + i) * F::kStripK;
+            if (left <= 0)
+                break;
+            typename F::Scales sc[2];
+            F::load_scales(sc, slot + scale_at, plan, W, first + i, i, from);
+            const uint32_t tile = slot + tile_at + i * 1024, col = column + i * strip_size;
+            if constexpr (SCALED) {
+                float part[4];
+                strip_product<F, BF16, true>(part, tile, plan.half, col, swap, sc, left, t);
+                const uint2 f = lds8(factors + i * (kColumns * 4) + 8 * t);
+                sums[0] = fmaf(part[0], __uint_as_float(f.x), sums[0]);
+                sums[1] = fmaf(part[1], __uint_as_float(f.y), sums[1]);
+                sums[2] = fmaf(part[2], __uint_as_float(f.x), sums[2]);
+                sums[3] = fmaf(part[3], __uint_as_float(f.y), sums[3]);
+            } else {
+                strip_product<F, BF16, false>(sums, tile, plan.half, col, swap, sc, left, t);
+            }
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive(bar + 8);
+        slot += plan.bytes;
+        bar += kBarrierBytes;
+        if (++at == plan.depth) {
+            slot -= at * plan.bytes;
+            bar -= at * kBarrierBytes;
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// -------------------------------------------------------------- host side
+
+constexpr size_t kSmemPerCta = 227 * 1024;
+
+// Warps that split `strips` strips: at most `most`, and as few as leave the
+// busiest warp no more strips than that.
+inline int split_warps(int strips, int most)
+{
+    const int each = (strips + most - 1) / most;
+    return (strips + each - 1) / each;
+}
+
+// Bytes of one row's scales or zero points (`size` bytes a group) in a panel,
+// if tensor copies can bring them: whole groups, multiples of 16 bytes; or 0.
+inline int tensor_scale_bytes(int strip_k, int strips, int K, int shift, int size, const void *at)
+{
+    const int k = strips * strip_k;
+    if ((k & ((1 << shift) - 1)) != 0 || !aligned16(at))
+        return 0;
+    const int bytes = (k >> shift) * size;
+    return bytes % 16 == 0 && bytes <= 256 && ((K >> shift) * size) % 16 == 0 ? bytes : 0;
+}
+
+// A slot with `strips` strips of `tiles` tiles of 16 rows, for `warps` warps
+// each, and `more` bytes of columns, and the kind of copies that fill it.
+template <class F, int FMT>
+SlotPlan slot_plan(int warps, int strips, int tiles, int more, const WeightView &W, WeightMaps &maps)
+{
+    SlotPlan s{};
+    s.warps = warps;
+    s.strips = strips;
+    s.tiles = tiles;
+    s.half = strips * 1024;
+    maps.tensor = F::row_bytes(W.K) % 16 == 0;
+    int at = 2 * s.half;
+    if (FMT != kW16) {
+        const int shift = FMT == kWNvfp4 ? 4 : W.group_shift, size = FMT == kWNvfp4 ? 1 : 2;
+        const int bytes = tensor_scale_bytes(F::kStripK, strips, W.K, shift, size, W.scales);
+        const int zeros = W.zeros ? tensor_scale_bytes(F::kStripK, strips, W.K, shift, 1, W.zeros) : 0;
+        maps.scale_tensor = bytes > 0 && (!W.zeros || zeros > 0);
+        maps.scale_bytes = maps.scale_tensor ? 16 * (bytes + zeros) : 0;
+        // by hand: a panel may start inside a group; an odd multiple of 16 spreads 8 rows over all banks
+        const int groups = ((strips * F::kStripK) >> shift) + 2;
+        s.scale.at = at;
+        s.scale.pitch = maps.scale_tensor ? bytes : (size * groups + 15) / 16 * 16 | 16;
+        at = (at + 16 * s.scale.pitch + 127) / 128 * 128;
+        if (W.zeros) {
+            s.scale.zero_at = at;
+            s.scale.zero_pitch = maps.scale_tensor ? zeros : (groups + 15) / 16 * 16 | 16;
+            at += 16 * s.scale.zero_pitch;
+        }
+    }
+    maps.by_hand = !maps.tensor || (FMT != kW16 && !maps.scale_tensor);
+    s.tile = (at + 1023) / 1024 * 1024;
+    s.columns_at = tiles * s.tile;
+    s.bytes = (s.columns_at + more + 1023) / 1024 * 1024;
+    return s;
+}
+
+// Encodes the tensor copies that slot_plan chose for W's `rows` rows (weight_maps.cu).
+moe_status make_maps(WeightMaps &m, const SlotPlan &plan, const WeightView &W, int row_bytes, int64_t rows, int scale_row,
+                     int zero_row);
+
+// The same for a format; scale_row, zero_row: bytes of a row's scales and zero points.
+template <class F, int FMT>
+moe_status make_maps(WeightMaps &m, const SlotPlan &plan, const WeightView &W, int64_t rows)
+{
+    const int groups = FMT == kWNvfp4 ? W.K / 16 : FMT == kWInt4 ? W.K >> W.group_shift : 0;
+    return make_maps(m, plan, W, F::row_bytes(W.K), rows, FMT == kWInt4 ? 2 * groups : groups, W.zeros ? groups : 0);
 }
 
 } // namespace nqg

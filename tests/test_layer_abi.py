@@ -21,7 +21,7 @@ def test_argument_layouts(L):
     assert L.moe_layer_args_size() == C.sizeof(nqg.MoeLayerArgs) == 192
 
 
-@pytest.mark.parametrize("T,k,I,want", [(1, 8, 2048, 32768), (0, 1, 8, 0), (3, 1, 8, 256), (64, 32, 65536, 1 << 28)])
+@pytest.mark.parametrize("T,k,I,want", [(1, 8, 2048, 32768), (0, 1, 8, 0), (3, 1, 8, 1536), (64, 32, 65536, 1 << 28)])
 def test_workspace_size(L, T, k, I, want):
     assert nqg.moe_layer_workspace_size(T, k, I) == want
 
