@@ -114,6 +114,17 @@ def test_select_many_tokens():
     assert torch.allclose(w, torch.softmax(top.values, 1).cpu(), rtol=1e-5, atol=1e-7)
 
 
+@pytest.mark.parametrize("dt", ["fp32", "bf16", "fp16"])
+def test_select_large_batch_with_equal_values(dt):
+    T, E, k = 5000, 200, 8
+    x = torch.randint(0, 12, (T, E), generator=_gen(4)).float() - 6
+    x[::7, ::3] = -math.inf
+    ids, w = _select(x.to(DT[dt]).to(DEV), k, dt)
+    top, want = torch.sort(x, dim=1, descending=True, stable=True)
+    assert torch.equal(ids.long(), want[:, :k])
+    assert torch.allclose(w, torch.softmax(top[:, :k], 1), rtol=1e-5, atol=0)
+
+
 def test_select_empty_batch():
     nqg.moe_select_experts(torch.empty((0, 8), device=DEV), torch.empty((0, 2), device=DEV, dtype=torch.int32),
                            torch.empty((0, 2), device=DEV))
