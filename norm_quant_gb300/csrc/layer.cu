@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) gate_up_kern
             }
         };
         const int end = min(slabs, slab0 + left);
-        produce<F, FMT, false>(Items{L.expert, a, slab0 + lane, end, 0, left - (end - slab0), lane, groups, panels, slabs, p.I},
+        produce<F, FMT, false, false>(Items{L.expert, a, slab0 + lane, end, 0, left - (end - slab0), lane, groups, panels, slabs, p.I},
                         groups, slots, bars, plan, p.W13, p.maps13, p.E * 2 * p.I,
                         blockIdx.x == 0 && p.stall >= 0 ? p.stall : INT64_MAX, lane);
         return;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) down_kernel(
     };
     if (warp == consumers) {  // the producer
         if (L.parts > 0)
-            produce<F, FMT, true>(Items{p, L, 0, lane, first_block, last_block, strips, 0, 0}, groups, slots, bars, plan,
+            produce<F, FMT, true, true>(Items{p, L, 0, lane, first_block, last_block, strips, 0, 0}, groups, slots, bars, plan,
                                   p.W2, p.maps2, p.E * p.H, INT64_MAX, lane);
         return;
     }
@@ -504,7 +504,7 @@ moe_status launch_layer(LayerParams &p, moe_stream_t stream)
     int least = 3;
     for (int m = strips >= 2 * warps ? 2 : 1; m > 0; --m) {
         p.gate_up_panels = (strips + m * warps - 1) / (m * warps);
-        p.gate_up = slot_plan<F, FMT>(warps, m * warps, 1, 0, p.W13, p.maps13);
+        p.gate_up = slot_plan<F, FMT>(warps, m * warps, 1, true, 0, p.W13, p.maps13);
         p.gate_up_groups = most_groups < kMaxGroups ? static_cast<int>(most_groups) : kMaxGroups;
         if (m > 1 && gate_bytes(most, p.gate_up_groups < 2 ? 3 : 2) > kSmemPerCta)
             continue;
@@ -538,7 +538,7 @@ moe_status launch_layer(LayerParams &p, moe_stream_t stream)
     };
     for (int tiles = per_cta < 3 ? per_cta : 3;; --tiles) {
         const int down_warps = panel_strips * tiles > 12 ? (panel_strips + 1) / 2 : panel_strips;
-        p.down = slot_plan<F2, FMT>(down_warps, panel_strips, tiles, column_bytes<F2>(p.down_most, panel_strips), p.W2, p.maps2);
+        p.down = slot_plan<F2, FMT>(down_warps, panel_strips, tiles, false, column_bytes<F2>(p.down_most, panel_strips), p.W2, p.maps2);
         p.down_groups = kMaxConsumers<FMT> / (down_warps * tiles) < kMaxGroups ? kMaxConsumers<FMT> / (down_warps * tiles) : kMaxGroups;
         while (p.down_groups > 1 && down_bytes(2) > kSmemPerCta)
             --p.down_groups;

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) linear_w4_ke
                 return true;
             }
         };
-        produce<F, FMT, false>(Items{first + lane, 0, 0, first + lane, last, p.groups, p.panels, (p.M + p.round - 1) / p.round}, p.groups,
+        produce<F, FMT, false, false>(Items{first + lane, 0, 0, first + lane, last, p.groups, p.panels, (p.M + p.round - 1) / p.round}, p.groups,
                         slots, bars, p.plan, p.W, p.maps, p.N,
                         blockIdx.x == 0 && p.stall >= 0 ? p.stall : INT64_MAX, lane);
         return;
@@ -167,7 +167,7 @@ moe_status launch_linear(LinearParams &p, moe_stream_t stream)
     int least = 3;
     for (int m = strips >= 2 * warps ? 2 : 1; m > 0; --m) {
         p.panels = (strips + m * warps - 1) / (m * warps);
-        p.plan = slot_plan<F, FMT>(warps, m * warps, 1, 0, p.W, p.maps);
+        p.plan = slot_plan<F, FMT>(warps, m * warps, 1, false, 0, p.W, p.maps);
         p.groups = most_groups < kMaxGroups ? most_groups : kMaxGroups;
         if (m > 1 && bytes(p.round, p.groups < 2 ? 3 : 2) > kSmemPerCta)
             continue;
@@ -194,6 +194,194 @@ moe_status launch_linear(LinearParams &p, moe_stream_t stream)
     if (st != MOE_OK)
         return st;
     return PdlLaunch(static_cast<unsigned>(blocks < sms ? blocks : sms), 32 * (warps * p.groups + 1), smem, stream).run(kern, p);
+}
+
+// More than 8 rows of x.  A CTA takes the blocks of 16 rows that fall to it as
+// the tiles of a slot, in passes of up to 4.  The columns come with the weights, as they lie in memory, since they
+// do not fit in shared memory for all of k; they are read once for all tiles of
+// a pass.  A consumer warp takes strip j of every panel, or half of its steps, for
+// one tile and all columns, so that a weight is widened once.  A weight is used for 9 to 64
+// columns here, and with 32 and more the matrix instruction is the bound: 47
+// cycles of an SM a strip (4096 weights) and 8 columns, against 100 that the
+// strip's bytes take.
+constexpr int kWideWarps = 15;  // consumers; with the producer 16, for 128 registers each
+
+// Warps that share a strip's steps: with more columns, shared memory holds fewer strips.
+template <int NT>
+constexpr int kShares = NT == 2 ? 1 : 2;
+
+struct WideParams {
+    WeightMaps maps;
+    CUtensorMap x;
+    WeightView W;
+    SlotPlan plan;
+    uint16_t *out;
+    int64_t out_stride;
+    int32_t M, N, panels;
+    float divisor;
+    int64_t stall;
+};
+
+__host__ __device__ inline uint32_t wide_sums_at(const SlotPlan &s)
+{
+    return (s.depth * (s.bytes + kBarrierBytes) + 4 + 15) / 16 * 16;
+}
+
+template <int FMT, bool BF16, int NT>
+__global__ void __launch_bounds__(32 * (kWideWarps + 1), 1) linear_w4_wide_kernel(const __grid_constant__ WideParams p)
+{
+    using F = Format<FMT, BF16, true, true>;
+    constexpr int kRows = 8 * NT;  // of the columns' boxes
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const SlotPlan &plan = p.plan;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = plan.strips * kShares<NT>,
+              consumers = warps * plan.tiles;
+    const uint32_t slots = smem_u32(smem), bars = slots + plan.depth * plan.bytes;
+    volatile int32_t *failed = reinterpret_cast<volatile int32_t *>(smem + plan.depth * (plan.bytes + kBarrierBytes));
+    float *red = reinterpret_cast<float *>(smem + wide_sums_at(plan));  // [tiles][warps][columns][16]
+    const int all = (p.N + 15) / 16;
+    const int first = static_cast<int>(static_cast<int64_t>(all) * blockIdx.x / gridDim.x);
+    const int last = static_cast<int>(static_cast<int64_t>(all) * (blockIdx.x + 1) / gridDim.x);
+    if (tid == 0) {
+        for (int i = 0; i < plan.depth; ++i) {
+            mbar_init(bars + i * kBarrierBytes, fill_arrivals(p.maps));
+            mbar_init(bars + i * kBarrierBytes + 8, consumers);
+        }
+        *failed = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (warp == consumers) {  // the producer
+        struct Items {
+            const WideParams &p;
+            int b, panel, last, now;
+            __device__ bool next(int &at, int &lo, int &hi)
+            {
+                if (panel == p.panels) {
+                    panel = 0;
+                    b += p.plan.tiles;
+                }
+                if (b >= last)
+                    return false;
+                at = now = panel++;
+                lo = 16 * b;
+                hi = lo + 8;
+                return true;
+            }
+            // runs of 64 elements; what lies past the end of a row is zero
+            __device__ uint32_t column_bytes() const { return 4 * p.plan.strips * kRows * kStripBytes; }
+            __device__ void columns(uint32_t slot, uint32_t bar) const
+            {
+                const int chunk = 4 * now * p.plan.strips;
+                if (p.W.K % 64 == 0)
+                    tensor_3d(slot + p.plan.columns_at, &p.x, 0, 0, chunk, bar);
+                else
+                    for (int i = 0; i < 4 * p.plan.strips; ++i)
+                        tensor_2d(slot + p.plan.columns_at + i * kRows * kStripBytes, &p.x, (chunk + i) * kStripBytes, 0, bar);
+            }
+        };
+        produce<F, FMT, true, false>(Items{p, first, 0, last, 0}, 1, slots, bars, plan, p.W, p.maps, p.N,
+                                     blockIdx.x == 0 && p.stall >= 0 ? p.stall : INT64_MAX, lane);
+        return;
+    }
+    const int tile = warp / warps, j = (warp - tile * warps) / kShares<NT>, share = warp % kShares<NT>, t = lane & 3;
+    Consumer<F, FMT, BF16> consumer(plan, p.W, failed, slots, bars, tile, j, lane);
+    const uint32_t column = plan.columns_at + j * 4 * kRows * kStripBytes + wide_column_at(lane);
+    for (int b0 = first; b0 < last; b0 += plan.tiles) {
+        float acc[NT][4] = {};
+        for (int panel = 0; panel < p.panels; ++panel) {
+            const int strip = panel * plan.strips + j, left = p.W.K - strip * F::kStripK;
+            consumer.wait();
+            if (left > 0) {
+                typename F::Scales sc[2];
+                F::load_scales(sc, consumer.slot + consumer.scale_at, plan, p.W, strip, j, panel * plan.strips * F::kStripK);
+                wide_product<F, BF16, NT, kShares<NT>>(acc, consumer.slot + consumer.tile_at + j * plan.strip, plan.half, consumer.slot + column, kRows,
+                                          sc, left, share, t);
+            }
+            consumer.give_back();
+        }
+        float *mine = red + warp * kRows * 16;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            store_sums(mine + nt * 128, acc[nt], lane);
+        named_barrier_sync(1, 32 * consumers);
+        for (int i = tid; i < 16 * p.M * plan.tiles; i += 32 * consumers) {
+            const int r = i & 15, c = (i >> 4) % p.M, q = (i >> 4) / p.M, n = 16 * (b0 + q) + r;
+            if (b0 + q >= last || n >= p.N)
+                continue;
+            float s = 0.0f;
+            for (int w = 0; w < warps; ++w)
+                s += red[(q * warps + w) * kRows * 16 + c * 16 + r];
+            if (*failed)
+                s = __int_as_float(0x7FC00000);
+            if (FMT == kWNvfp4)
+                s = s * (F::kPost / early(p.divisor)) / late(p.divisor);
+            p.out[c * p.out_stride + n] = narrow16<BF16>(s);
+        }
+        named_barrier_sync(1, 32 * consumers);  // the sums have been read
+    }
+}
+
+template <int FMT, bool BF16, int NT>
+moe_status launch_wide(const LinearParams &a, moe_stream_t stream)
+{
+    using F = Format<FMT, BF16, true, true>;
+    constexpr int kRows = 8 * NT;
+    static SmemLimit limit;
+    const int sms = sm_count(), strips = strips_of<F>(a.W.K), blocks = (a.N + 15) / 16;
+    if (sms <= 0)
+        return MOE_ERR_CUDA;
+    WideParams p{};
+    p.W = a.W;
+    p.out = a.out;
+    p.out_stride = a.out_stride;
+    p.M = a.M;
+    p.N = a.N;
+    p.divisor = a.divisor;
+    p.stall = a.stall;
+    const auto bytes = [&](int depth) {
+        SlotPlan s = p.plan;
+        s.depth = depth;
+        return static_cast<size_t>(wide_sums_at(s)) + static_cast<size_t>(s.tiles) * s.strips * kShares<NT> * kRows * 64;
+    };
+    const int per_cta = (blocks + sms - 1) / sms;
+    // equal passes of at most 4 tiles
+    const int passes = (per_cta + 3) / 4, tiles = (per_cta + passes - 1) / passes;
+    for (int w = split_warps(strips, kWideWarps / (tiles * kShares<NT>));; --w) {
+        p.plan = slot_plan<F, FMT>(w, w, tiles, false, w * 4 * kRows * kStripBytes, p.W, p.maps);
+        if (bytes(2) <= kSmemPerCta)
+            break;
+        if (w == 1)
+            return MOE_ERR_UNSUPPORTED;
+    }
+    p.panels = (strips + p.plan.strips - 1) / p.plan.strips;
+    p.plan.depth = 2;
+    while (p.plan.depth < 8 && bytes(p.plan.depth + 1) <= kSmemPerCta)
+        ++p.plan.depth;
+    const size_t smem = bytes(p.plan.depth);
+    int dev = 0;
+    const auto kern = linear_w4_wide_kernel<FMT, BF16, NT>;
+    if (cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limit) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    moe_status st = make_maps<F, FMT>(p.maps, p.plan, p.W, p.N);
+    if (st == MOE_OK)
+        st = make_column_map(p.x, a.x, 2 * p.W.K, p.M, 2 * a.x_stride, kRows, 4 * p.plan.strips);
+    if (st != MOE_OK)
+        return st;
+    return PdlLaunch(static_cast<unsigned>(blocks < sms ? blocks : sms), 32 * (p.plan.strips * kShares<NT> * tiles + 1), smem, stream).run(kern, p);
+}
+
+template <int FMT, bool BF16>
+moe_status launch(LinearParams &p, moe_stream_t stream)
+{
+    return p.M <= kColumns ? launch_linear<FMT, BF16>(p, stream)
+           : p.M <= 16     ? launch_wide<FMT, BF16, 2>(p, stream)
+           : p.M <= 32     ? launch_wide<FMT, BF16, 4>(p, stream)
+                           : launch_wide<FMT, BF16, 8>(p, stream);
 }
 
 } // namespace
@@ -235,6 +423,6 @@ extern "C" moe_status moe_linear_w4(const moe_linear_w4_args *a, moe_stream_t st
     p.stall = debug_stall_slots();
     const bool bf16 = a->io_dtype == MOE_IO_BF16;
     if (int4)
-        return bf16 ? launch_linear<kWInt4, true>(p, stream) : launch_linear<kWInt4, false>(p, stream);
-    return bf16 ? launch_linear<kWNvfp4, true>(p, stream) : launch_linear<kWNvfp4, false>(p, stream);
+        return bf16 ? launch<kWInt4, true>(p, stream) : launch<kWInt4, false>(p, stream);
+    return bf16 ? launch<kWNvfp4, true>(p, stream) : launch<kWNvfp4, false>(p, stream);
 }

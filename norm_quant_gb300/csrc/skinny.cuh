@@ -177,8 +177,10 @@ constexpr int kMaxConsumers = FMT == kWInt4 ? 19 : 23;
 
 constexpr int kColumns = 8;
 
-// NATIVE: operands of the columns' type; otherwise nvfp4's are fp16.
-template <int FMT, bool BF16, bool NATIVE = false>
+// NATIVE: operands of the columns' type; otherwise nvfp4's are fp16.  STEPS:
+// nvfp4's lanes take 64 elements a step between them, as int4's do, so that
+// columns can be read as they lie in memory.
+template <int FMT, bool BF16, bool NATIVE = false, bool STEPS = false>
 struct Format;
 
 __device__ __forceinline__ uint4 lds16(uint32_t at)
@@ -222,23 +224,25 @@ struct ScalePlace {
     uint32_t zero_at, zero_pitch;  // zero points, pitch 0: none
 };
 
-// How the slots of a ring are laid out.  A slot: its tiles, each rows 0 to 7 of
-// every strip of the panel, 1 KB each, then rows 8 to 15, then the scales; and
-// then columns, if any.
+// How the slots of a ring are laid out.  A slot: for every strip of the panel
+// 128 bytes of each row, in blocks of `block` consecutive rows of the matrix;
+// then the scales of all rows; and then columns, if any.  Either the slot's
+// 16-row tiles are one block, or there are two blocks of 8 rows for one tile.
 struct SlotPlan {
-    int32_t warps;      // of a group
+    int32_t warps;      // of a group for each tile
     int32_t strips;     // of a panel: warp j takes strips j, j + warps, ...
     int32_t tiles;      // of 16 rows in a slot
-    int32_t half;       // bytes of the strips of 8 rows
-    int32_t tile;       // bytes of a tile with its scales
-    ScalePlace scale;   // from the start of a tile
+    int32_t block;      // rows: 16 tiles, or 8
+    int32_t strip;      // bytes from strip to strip of a block
+    int32_t half;       // bytes from rows 0 to 7 of a tile to rows 8 to 15
+    ScalePlace scale;   // from the start of a slot
     int32_t columns_at;
     int32_t bytes;      // of a slot, a multiple of 1024
     int32_t depth;      // slots of a group's ring
 };
 
 template <bool BF16, bool NATIVE>
-struct Format<kW16, BF16, NATIVE> {
+struct Format<kW16, BF16, NATIVE, false> {
     static constexpr float kPost = 1.0f;  // the sums are to be multiplied by this
     static constexpr bool kHalf = !BF16;  // the operands are fp16
     static constexpr int kStripK = 64, kSteps = 2, kLane = 8, kMma = 2;
@@ -250,7 +254,7 @@ struct Format<kW16, BF16, NATIVE> {
     };
     __host__ __device__ static int row_bytes(int K) { return K * 2; }
     __device__ static int at(int u, int t) { return 16 * t + 8 * u; }
-    __device__ static uint32_t scale_at(const ScalePlace &, int, int, int) { return 0; }
+    __device__ static uint32_t scale_at(const ScalePlace &, int, int) { return 0; }
     __device__ static void load_scales(Scales (&)[2], uint32_t, const SlotPlan &, const WeightView &, int, int, int) {}
     __device__ static void load(Slice &s, uint32_t tile)  // tile: of the lane's row, at lane_at()
     {
@@ -281,7 +285,7 @@ struct Format<kW16, BF16, NATIVE> {
 // the elements 64 t to 64 t + 63 of a strip, so that the four scales that it
 // needs of a row are one word.
 template <bool BF16, bool NATIVE>
-struct Format<kWNvfp4, BF16, NATIVE> {
+struct Format<kWNvfp4, BF16, NATIVE, false> {
     static constexpr bool kHalf = !(BF16 && NATIVE);
     // bf16: a code's bits s, eem moved to bits 15 and 8..6 are the bf16 number
     // value x 2^-126 (the subnormals included); the scale carries 2^100 of it
@@ -298,8 +302,8 @@ struct Format<kWNvfp4, BF16, NATIVE> {
     };
     __host__ __device__ static int row_bytes(int K) { return K / 2; }
     __device__ static int at(int u, int t) { return 64 * t + 16 * u; }
-    // Of row g and the panel's strip j, from the slot on; row g + 8 lies 8 rows further.
-    __device__ static uint32_t scale_at(const ScalePlace &pl, int g, int j, int t) { return pl.at + g * pl.pitch + 16 * j + 4 * t; }
+    // Of row r of the slot, from its start on; row r + 8 lies 8 rows further.
+    __device__ static uint32_t scale_at(const ScalePlace &pl, int r, int t) { return pl.at + r * pl.pitch + 4 * t; }
     __device__ static void load_scales(Scales (&s)[2], uint32_t at, const SlotPlan &plan, const WeightView &, int, int i, int)
     {
         s[0].codes = lds4(at + 16 * i);
@@ -323,6 +327,14 @@ struct Format<kWNvfp4, BF16, NATIVE> {
             s.v[1].x = s.v[1].y = 0;
         if (groups < 4)
             s.v[1].z = s.v[1].w = 0;
+    }
+    // The factor of the operands, from the scale twice in fp16.
+    __device__ static uint32_t operand_scale(uint32_t twice)
+    {
+        if constexpr (kHalf)
+            return twice;
+        const float f = widen16<false>(static_cast<uint16_t>(twice)) * 0x1p100f;
+        return f32x2_to_bf16x2(f, f);
     }
     __device__ static void eight(uint32_t w, uint32_t scale, uint32_t *p)
     {
@@ -352,13 +364,53 @@ struct Format<kWNvfp4, BF16, NATIVE> {
         uint32_t two;  // the scales of steps 2 (u / 2) and the next
         const uint16_t c = static_cast<uint16_t>(sc.codes >> (16 * (u >> 1)));
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(c));
-        uint32_t scale = __byte_perm(two, two, u & 1 ? 0x3232 : 0x1010);
-        if constexpr (!kHalf) {
-            const float f = widen16<false>(static_cast<uint16_t>(scale)) * 0x1p100f;
-            scale = f32x2_to_bf16x2(f, f);
-        }
+        const uint32_t scale = operand_scale(__byte_perm(two, two, u & 1 ? 0x3232 : 0x1010));
         eight(u & 1 ? s.v[u >> 1].z : s.v[u >> 1].x, scale, p);
         eight(u & 1 ? s.v[u >> 1].w : s.v[u >> 1].y, scale, p + 4);
+    }
+};
+
+template <bool BF16>
+struct Format<kWNvfp4, BF16, true, true> : Format<kWNvfp4, BF16, true, false> {
+    using Base = Format<kWNvfp4, BF16, true, false>;
+    struct Scales {
+        uint32_t codes[4];  // of the four groups of each step; lane t's is byte t
+    };
+    struct Slice {  // read step by step
+        uint32_t at;
+    };
+    __device__ static uint32_t scale_at(const ScalePlace &pl, int r, int) { return pl.at + r * pl.pitch; }
+    __device__ static void load_scales(Scales (&s)[2], uint32_t at, const SlotPlan &plan, const WeightView &, int, int i, int)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 v = lds16(at + 16 * i + 8 * h * plan.scale.pitch);
+            s[h].codes[0] = v.x;
+            s[h].codes[1] = v.y;
+            s[h].codes[2] = v.z;
+            s[h].codes[3] = v.w;
+        }
+    }
+    __device__ static void load(Slice &s, uint32_t tile) { s.at = tile; }
+    __device__ static uint32_t lane_at(int g, int t) { return g * kStripBytes + ((t >> 1) ^ g) * 16 + (t & 1) * 8; }
+    // Past the end the columns are zero, and codes are finite whatever they are.
+    __device__ static void clear(Slice &, Scales &sc, int left, int t)
+    {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (64 * u + 16 * t >= left)
+                sc.codes[u] = 0;
+    }
+    __device__ static void operand(const Slice &s, const Scales &sc, int u, uint32_t (&p)[8])
+    {
+        uint32_t two;
+        const uint32_t word = u & 2 ? (u & 1 ? sc.codes[3] : sc.codes[2]) : (u & 1 ? sc.codes[1] : sc.codes[0]);
+        const uint16_t c = static_cast<uint16_t>((word >> (8 * (threadIdx.x & 3))) & 0xFFu);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(c));
+        const uint32_t scale = Base::operand_scale(__byte_perm(two, two, 0x1010));
+        const uint2 w = lds8(s.at ^ (32 * u));
+        Base::eight(w.x, scale, p);
+        Base::eight(w.y, scale, p + 4);
     }
 };
 
@@ -369,8 +421,8 @@ struct Format<kWNvfp4, BF16, NATIVE> {
 // A code in bits 3..0 of the mantissa of 128 (bf16) or 1024 (fp16) makes that
 // number plus the code, and in fp16 one in bits 7..4 makes 1024 + 16 code; either
 // less the zero point is one exact instruction.
-template <bool BF16, bool NATIVE>
-struct Format<kWInt4, BF16, NATIVE> {
+template <bool BF16, bool NATIVE, bool STEPS>
+struct Format<kWInt4, BF16, NATIVE, STEPS> {
     static constexpr bool kHalf = !BF16;
     static constexpr float kPost = 1.0f;
     static constexpr int kStripK = 256, kSteps = 4, kLane = 16, kMma = 4;
@@ -386,7 +438,7 @@ struct Format<kWInt4, BF16, NATIVE> {
     __host__ __device__ static int row_bytes(int K) { return K / 2; }
     __device__ static int at(int u, int t) { return 64 * u + 16 * t; }
     // the row alone: scales and zero points have pitches of their own
-    __device__ static uint32_t scale_at(const ScalePlace &, int g, int, int) { return g; }
+    __device__ static uint32_t scale_at(const ScalePlace &, int r, int) { return r; }
     // strip: of the row, i of the panel; from: the panel's first element.  A strip starts with a
     // group, or inside one of 512 and more.  What is read for steps past the end
     // is cleared later.
@@ -395,9 +447,9 @@ struct Format<kWInt4, BF16, NATIVE> {
         const int shift = W.group_shift, first = ((strip * kStripK) >> shift) - (from >> shift);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = (at & 7) + 8 * h;  // tiles are 1024-byte aligned
-            const uint32_t a = (at & ~7u) + plan.scale.at + 2 * first + r * plan.scale.pitch;
-            const uint32_t z = (at & ~7u) + plan.scale.zero_at + first + r * plan.scale.zero_pitch;
+            const int r = (at & 127) + 8 * h;  // slots are 1024-byte aligned
+            const uint32_t a = (at & ~127u) + plan.scale.at + 2 * first + r * plan.scale.pitch;
+            const uint32_t z = (at & ~127u) + plan.scale.zero_at + first + r * plan.scale.zero_pitch;
             s[h].zero = 0x08080808u;
             if (shift == 6) {  // four groups
                 const uint2 v = lds8(a);
@@ -515,6 +567,73 @@ __device__ __forceinline__ void strip_product(float (&sums)[4], uint32_t tile, u
             sums[3] = first ? shi * part[3] : fmaf(shi, part[3], sums[3]);
         }
     }
+}
+
+// sums[nt] += 16 rows of a strip x the columns 8 nt to 8 nt + 7 for nt < NT, for
+// columns that lie as tensor copies bring them: 128 bytes of each of `rows`
+// rows, swizzled, for every 64 elements.  columns: the lane's, at wide_column_at().
+// The warp takes the share-th of SHARES equal shares of the strip's steps.
+template <class F, bool BF16, int NT, int SHARES>
+__device__ __forceinline__ void wide_product(float (&sums)[NT][4], uint32_t tile, uint32_t half, uint32_t columns, uint32_t rows,
+                                             typename F::Scales (&sc)[2], int left, int share, int t)
+{
+    typename F::Slice a, b;
+    F::load(a, tile);
+    F::load(b, tile + half);
+    if (left < F::kStripK) {
+        F::clear(a, sc[0], left, t);
+        F::clear(b, sc[1], left, t);
+    }
+#pragma unroll
+    for (int i = 0; i < F::kSteps / SHARES; ++i) {
+        const int u = SHARES == 1 ? i : share * (F::kSteps / SHARES) + i;
+        uint32_t p[8], q[8];
+        F::operand(a, sc[0], u, p);
+        F::operand(b, sc[1], u, q);
+        const uint32_t at = columns + u * rows * kStripBytes;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            uint32_t c[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 v = lds16((at ^ (16 * h)) + nt * 8 * kStripBytes);
+                if constexpr (F::kSplit) {
+                    c[4 * h] = __byte_perm(v.x, v.z, 0x5410);
+                    c[4 * h + 1] = __byte_perm(v.x, v.z, 0x7632);
+                    c[4 * h + 2] = __byte_perm(v.y, v.w, 0x5410);
+                    c[4 * h + 3] = __byte_perm(v.y, v.w, 0x7632);
+                } else {
+                    c[4 * h] = v.x;
+                    c[4 * h + 1] = v.y;
+                    c[4 * h + 2] = v.z;
+                    c[4 * h + 3] = v.w;
+                }
+            }
+            float part[4];
+            float(&d)[4] = F::kAfter ? part : sums[nt];
+#pragma unroll
+            for (int m = 0; m < F::kMma; ++m) {
+                const uint32_t frag[4] = {p[2 * m], q[2 * m], p[2 * m + 1], q[2 * m + 1]};
+                if (m == 0 && F::kAfter)
+                    mma16816<!F::kHalf, true>(d, frag, c[2 * m], c[2 * m + 1]);
+                else
+                    mma16816<!F::kHalf>(d, frag, c[2 * m], c[2 * m + 1]);
+            }
+            if constexpr (F::kAfter) {
+                const float slo = F::scale_after(sc[0], u), shi = F::scale_after(sc[1], u);
+                sums[nt][0] = fmaf(slo, part[0], sums[nt][0]);
+                sums[nt][1] = fmaf(slo, part[1], sums[nt][1]);
+                sums[nt][2] = fmaf(shi, part[2], sums[nt][2]);
+                sums[nt][3] = fmaf(shi, part[3], sums[nt][3]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t wide_column_at(int lane)
+{
+    const int g = lane >> 2, t = lane & 3;
+    return g * kStripBytes + ((2 * t) ^ g) * 16;
 }
 
 // ------------------------------------------------------------- the columns
@@ -673,9 +792,9 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // The tensor copies of a matrix.
 struct WeightMaps {
-    CUtensorMap panels;  // [row][strip of the whole strips][128 bytes]: 8 rows x a panel's strips
-    CUtensorMap strips;  // [row][byte]: 8 rows x 128 bytes, zero past the end of a row
-    CUtensorMap scales;  // [row][byte of scales]: 8 rows x a panel's
+    CUtensorMap panels;  // [row][strip of the whole strips][128 bytes]: a block's rows x a panel's strips
+    CUtensorMap strips;  // [row][byte]: a block's rows x 128 bytes, zero past the end of a row
+    CUtensorMap scales;  // [row][byte of scales]: a block's rows x a panel's
     CUtensorMap zeros;   // int4: likewise
     int32_t tensor;        // rows are multiples of 16 bytes: the copies above; 0: 8-byte copies
     int32_t whole;         // whole strips of a row
@@ -718,30 +837,32 @@ __device__ __forceinline__ void tensor_3d(uint32_t dst, const CUtensorMap *map, 
                  : "memory");
 }
 
-// Copies `bytes` from src(r) for r < 16 to dst + r * pitch, by one warp, two
-// lanes a row: in asynchronous pieces of 16, 8 or 4 bytes, as the alignment of
-// every row allows (`align`: all addresses and `bytes` or-ed together), or
-// else byte by byte at once.
+// Copies `bytes` from src(r) for r < rows (a multiple of 16) to dst + r * pitch,
+// by one warp, two lanes a row: in asynchronous pieces of 16, 8 or 4 bytes, as
+// the alignment of every row allows (`align`: all addresses and `bytes` or-ed
+// together), or else byte by byte at once.
 template <class Source>
-__device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, Source src, int bytes, uintptr_t align, int lane)
+__device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, int rows, Source src, int bytes, uintptr_t align, int lane)
 {
-    const int r = lane >> 1, odd = lane & 1;
-    const uint8_t *from = src(r);
-    const uint32_t to = dst + r * pitch;
-    if (align % 16 == 0) {
-        for (int b = 16 * odd; b < bytes; b += 32)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + b), "l"(from + b) : "memory");
-    } else if (align % 8 == 0) {
-        for (int b = 8 * odd; b < bytes; b += 16)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + b), "l"(from + b) : "memory");
-    } else if (align % 4 == 0) {
-        for (int b = 4 * odd; b < bytes; b += 8)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + b), "l"(from + b) : "memory");
-    } else {
+    const int odd = lane & 1;
+    for (int r = lane >> 1; r < rows; r += 16) {
+        const uint8_t *from = src(r);
+        const uint32_t to = dst + r * pitch;
+        if (align % 16 == 0) {
+            for (int b = 16 * odd; b < bytes; b += 32)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + b), "l"(from + b) : "memory");
+        } else if (align % 8 == 0) {
+            for (int b = 8 * odd; b < bytes; b += 16)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + b), "l"(from + b) : "memory");
+        } else if (align % 4 == 0) {
+            for (int b = 4 * odd; b < bytes; b += 8)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + b), "l"(from + b) : "memory");
+        } else {
 #pragma unroll 4
-        for (int b = odd; b < bytes; b += 2) {
-            const uint32_t v = __ldg(from + b);
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + b), "r"(v) : "memory");
+            for (int b = odd; b < bytes; b += 2) {
+                const uint32_t v = __ldg(from + b);
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + b), "r"(v) : "memory");
+            }
         }
     }
 }
@@ -750,38 +871,32 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, Source src, i
 // lane's when its own copies have landed, if the producer's lanes make any.
 __host__ __device__ inline int fill_arrivals(const WeightMaps &maps) { return maps.by_hand ? 33 : 1; }
 
-// The tensor copies into one slot of panel `panel` of the rows from lo on and
-// of those from hi on, 8 each, and of the tiles 16 rows further; `more` bytes
-// come by other copies.  One thread.
+// The tensor copies into one slot of panel `panel` of the rows from lo on and,
+// where a tile is two blocks, from hi on; `more` bytes come by other copies.
+// One thread.
 template <class F, int FMT>
 __device__ __forceinline__ void fill_by_tensor(uint32_t slot, uint32_t full, const SlotPlan &plan, const WeightView &W,
                                                const WeightMaps &maps, int panel, int lo, int hi, uint32_t more)
 {
-    const int strip = panel * plan.strips;
+    const int strip = panel * plan.strips, blocks = 16 * plan.tiles / plan.block;
     const bool by_panel = strip + plan.strips <= maps.whole || maps.whole * kStripBytes == F::row_bytes(W.K);
     const int here = by_panel ? plan.strips : min(plan.strips, (F::row_bytes(W.K) + kStripBytes - 1) / kStripBytes - strip);
-    mbar_arrive_expect_tx(full, plan.tiles * ((maps.tensor ? 2048 * here : 0) + maps.scale_bytes) + more);
-    for (int tile = 0; tile < plan.tiles; ++tile, slot += plan.tile, lo += 16, hi += 16) {
+    mbar_arrive_expect_tx(full, (maps.tensor ? 16 * plan.tiles * kStripBytes * here : 0) + maps.scale_bytes + more);
+    for (int b = 0; b < blocks; ++b) {
+        const int row = b ? hi : lo;
+        const uint32_t to = slot + b * plan.half;
         if (maps.tensor) {
-            if (by_panel) {
-                tensor_3d(slot, &maps.panels, 0, lo, strip, full);
-                tensor_3d(slot + plan.half, &maps.panels, 0, hi, strip, full);
-            } else {
-                for (int i = 0; i < here; ++i) {
-                    tensor_2d(slot + i * 1024, &maps.strips, (strip + i) * kStripBytes, lo, full);
-                    tensor_2d(slot + plan.half + i * 1024, &maps.strips, (strip + i) * kStripBytes, hi, full);
-                }
-            }
+            if (by_panel)
+                tensor_3d(to, &maps.panels, 0, row, strip, full);
+            else
+                for (int i = 0; i < here; ++i)
+                    tensor_2d(to + i * plan.strip, &maps.strips, (strip + i) * kStripBytes, row, full);
         }
         if (FMT != kW16 && maps.scale_tensor) {
-            const int x = panel * plan.scale.pitch;
-            tensor_2d(slot + plan.scale.at, &maps.scales, x, lo, full);
-            tensor_2d(slot + plan.scale.at + 8 * plan.scale.pitch, &maps.scales, x, hi, full);
-            if (FMT == kWInt4 && plan.scale.zero_pitch) {
-                const int z = panel * plan.scale.zero_pitch;
-                tensor_2d(slot + plan.scale.zero_at, &maps.zeros, z, lo, full);
-                tensor_2d(slot + plan.scale.zero_at + 8 * plan.scale.zero_pitch, &maps.zeros, z, hi, full);
-            }
+            tensor_2d(slot + plan.scale.at + b * 8 * plan.scale.pitch, &maps.scales, panel * plan.scale.pitch, row, full);
+            if (FMT == kWInt4 && plan.scale.zero_pitch)
+                tensor_2d(slot + plan.scale.zero_at + b * 8 * plan.scale.zero_pitch, &maps.zeros, panel * plan.scale.zero_pitch,
+                          row, full);
         }
     }
 }
@@ -792,29 +907,31 @@ template <class F, int FMT>
 __device__ __forceinline__ void fill_by_hand(uint32_t slot, uint32_t full, const SlotPlan &plan, const WeightView &W,
                                              const WeightMaps &maps, int panel, int lo, int hi, int rows, int lane)
 {
-    const int strip = panel * plan.strips;
-    for (int tile = 0; tile < plan.tiles; ++tile, slot += plan.tile, lo += 16, hi += 16) {
-        const auto row = [&](int r) { return static_cast<int64_t>(min((r & 8 ? hi : lo) + (r & 7), rows - 1)); };
-        if (!maps.tensor) {
-            const int row_bytes = F::row_bytes(W.K), r = lane >> 1, bytes = min(plan.strips * kStripBytes, row_bytes - strip * kStripBytes);
+    const int strip = panel * plan.strips, all = 16 * plan.tiles;
+    const bool pair = plan.block < all;
+    const auto row = [&](int r) { return static_cast<int64_t>(min(pair ? (r & 8 ? hi : lo) + (r & 7) : lo + r, rows - 1)); };
+    if (!maps.tensor) {
+        const int row_bytes = F::row_bytes(W.K), bytes = min(plan.strips * kStripBytes, row_bytes - strip * kStripBytes);
+        for (int r = lane >> 1; r < all; r += 16) {
             const uint8_t *from = W.w + row(r) * row_bytes + strip * kStripBytes;
-            const uint32_t to = slot + (r >> 3) * plan.half + (r & 7) * kStripBytes;
+            const uint32_t to = slot + (pair ? (r >> 3) * plan.half + (r & 7) * kStripBytes : r * kStripBytes);
             for (int b = 8 * (lane & 1); b < bytes; b += 16)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + b / kStripBytes * 1024 +
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + b / kStripBytes * plan.strip +
                                                                               (((b % kStripBytes) >> 4 ^ (r & 7)) << 4) + (b & 8)),
                              "l"(from + b)
                              : "memory");
         }
-        if (FMT != kW16 && !maps.scale_tensor) {
-            const int shift = FMT == kWNvfp4 ? 4 : W.group_shift, size = FMT == kWNvfp4 ? 1 : 2;
-            const int groups = W.K >> shift, k0 = strip * F::kStripK, k1 = min(k0 + plan.strips * F::kStripK, W.K);
-            const int g0 = k0 >> shift, n = ((k1 - 1) >> shift) + 1 - g0;
-            copy_rows(slot + plan.scale.at, plan.scale.pitch, [&](int r) { return W.scales + (row(r) * groups + g0) * size; },
-                      size * n, reinterpret_cast<uintptr_t>(W.scales) | size * groups | size * g0 | size * n, lane);
-            if (FMT == kWInt4 && plan.scale.zero_pitch)
-                copy_rows(slot + plan.scale.zero_at, plan.scale.zero_pitch, [&](int r) { return W.zeros + row(r) * groups + g0; },
-                          n, reinterpret_cast<uintptr_t>(W.zeros) | groups | g0 | n, lane);
-        }
+    }
+    if (FMT != kW16 && !maps.scale_tensor) {
+        const int shift = FMT == kWNvfp4 ? 4 : W.group_shift, size = FMT == kWNvfp4 ? 1 : 2;
+        const int groups = W.K >> shift, k0 = strip * F::kStripK, k1 = min(k0 + plan.strips * F::kStripK, W.K);
+        const int g0 = k0 >> shift, n = ((k1 - 1) >> shift) + 1 - g0;
+        copy_rows(slot + plan.scale.at, plan.scale.pitch, all, [&](int r) { return W.scales + (row(r) * groups + g0) * size; },
+                  size * n, reinterpret_cast<uintptr_t>(W.scales) | size * groups | size * g0 | size * n, lane);
+        if (FMT == kWInt4 && plan.scale.zero_pitch)
+            copy_rows(slot + plan.scale.zero_at, plan.scale.zero_pitch, all,
+                      [&](int r) { return W.zeros + row(r) * groups + g0; }, n,
+                      reinterpret_cast<uintptr_t>(W.zeros) | groups | g0 | n, lane);
     }
     // what was copied at once is visible to whoever sees the arrival; the asynchronous copies arrive by themselves
     __threadfence_block();
@@ -840,11 +957,11 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 // The lanes go side by side, so that the producer's instructions are shared by
 // the groups' slots, but none waits for another: groups meet at barriers, and a
 // group may need more slots before it gets there while another's ring is full.
-// Copies by hand take the whole warp and go group by group.  Weights may be
-// read from the start; columns (COLUMNS) and, if !COLUMNS, everything only after
-// the kernel before: the caller has waited for it unless COLUMNS.
+// Copies by hand take the whole warp and go group by group.  EARLY: weights may
+// be read before the kernel before has ended, which is then waited for here;
+// otherwise the caller has waited.
 // `limit`: slots that lane 0 fills at most.
-template <class F, int FMT, bool COLUMNS, class Items>
+template <class F, int FMT, bool COLUMNS, bool EARLY, class Items>
 __device__ __forceinline__ void produce(Items items, int groups, uint32_t slots, uint32_t bars, const SlotPlan &plan,
                                         const WeightView &W, const WeightMaps &maps, int rows, int64_t limit, int lane)
 {
@@ -852,7 +969,7 @@ __device__ __forceinline__ void produce(Items items, int groups, uint32_t slots,
     const uint32_t ring = slots + lane * plan.depth * plan.bytes, ring_bars = bars + lane * plan.depth * kBarrierBytes;
     int panel = 0, lo = 0, hi = 0;
     bool more = lane < groups && !(lane == 0 && limit <= 0);
-    if constexpr (COLUMNS) {
+    if constexpr (EARLY) {
         if (maps.by_hand) {
             grid_dependency_wait();
             more = more && items.next(panel, lo, hi);
@@ -947,11 +1064,26 @@ struct Consumer {
                         int j_, int lane)
         : plan(p), W(w), patience{failed}, slot(ring), bar(ring_bars), j(j_), t(lane & 3)
     {
-        tile_at = tile * p.tile + F::lane_at(lane >> 2, t);
-        scale_at = tile * p.tile + F::scale_at(p.scale, lane >> 2, 0, t);
+        tile_at = tile * 16 * kStripBytes + F::lane_at(lane >> 2, t);
+        scale_at = F::scale_at(p.scale, tile * 16 + (lane >> 2), t);
     }
 
     __device__ __forceinline__ void wait() { patience.wait(bar, phase); }
+
+    __device__ __forceinline__ void give_back()
+    {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive(bar + 8);
+        slot += plan.bytes;
+        bar += kBarrierBytes;
+        if (++at == plan.depth) {
+            slot -= at * plan.bytes;
+            bar -= at * kBarrierBytes;
+            at = 0;
+            phase ^= 1;
+        }
+    }
 
     // The next slot, which holds panel `panel` and has been waited for: sums +=
     // its strips of this warp x columns.  column, swap: from column_at, in the
@@ -970,7 +1102,7 @@ struct Consumer {
                 break;
             typename F::Scales sc[2];
             F::load_scales(sc, slot + scale_at, plan, W, first + i, i, from);
-            const uint32_t tile = slot + tile_at + i * 1024, col = column + i * strip_size;
+            const uint32_t tile = slot + tile_at + i * plan.strip, col = column + i * strip_size;
             if constexpr (SCALED) {
                 float part[4];
                 strip_product<F, BF16, true>(part, tile, plan.half, col, swap, sc, left, t);
@@ -983,17 +1115,7 @@ struct Consumer {
                 strip_product<F, BF16, false>(sums, tile, plan.half, col, swap, sc, left, t);
             }
         }
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0)
-            mbar_arrive(bar + 8);
-        slot += plan.bytes;
-        bar += kBarrierBytes;
-        if (++at == plan.depth) {
-            slot -= at * plan.bytes;
-            bar -= at * kBarrierBytes;
-            at = 0;
-            phase ^= 1;
-        }
+        give_back();
     }
 };
 
@@ -1021,40 +1143,47 @@ inline int tensor_scale_bytes(int strip_k, int strips, int K, int shift, int siz
 }
 
 // A slot with `strips` strips of `tiles` tiles of 16 rows, for `warps` warps
-// each, and `more` bytes of columns, and the kind of copies that fill it.
+// each, and `more` bytes of columns, and the kind of copies that fill it.  pair:
+// the tile's halves are apart in the matrix.
 template <class F, int FMT>
-SlotPlan slot_plan(int warps, int strips, int tiles, int more, const WeightView &W, WeightMaps &maps)
+SlotPlan slot_plan(int warps, int strips, int tiles, bool pair, int more, const WeightView &W, WeightMaps &maps)
 {
     SlotPlan s{};
+    const int rows = 16 * tiles;
     s.warps = warps;
     s.strips = strips;
     s.tiles = tiles;
-    s.half = strips * 1024;
+    s.block = pair ? 8 : rows;
+    s.strip = s.block * kStripBytes;
+    s.half = pair ? strips * s.strip : 8 * kStripBytes;
     maps.tensor = F::row_bytes(W.K) % 16 == 0;
-    int at = 2 * s.half;
+    int at = rows * strips * kStripBytes;
     if (FMT != kW16) {
         const int shift = FMT == kWNvfp4 ? 4 : W.group_shift, size = FMT == kWNvfp4 ? 1 : 2;
         const int bytes = tensor_scale_bytes(F::kStripK, strips, W.K, shift, size, W.scales);
         const int zeros = W.zeros ? tensor_scale_bytes(F::kStripK, strips, W.K, shift, 1, W.zeros) : 0;
         maps.scale_tensor = bytes > 0 && (!W.zeros || zeros > 0);
-        maps.scale_bytes = maps.scale_tensor ? 16 * (bytes + zeros) : 0;
+        maps.scale_bytes = maps.scale_tensor ? rows * (bytes + zeros) : 0;
         // by hand: a panel may start inside a group; an odd multiple of 16 spreads 8 rows over all banks
         const int groups = ((strips * F::kStripK) >> shift) + 2;
         s.scale.at = at;
         s.scale.pitch = maps.scale_tensor ? bytes : (size * groups + 15) / 16 * 16 | 16;
-        at = (at + 16 * s.scale.pitch + 127) / 128 * 128;
+        at = (at + rows * s.scale.pitch + 127) / 128 * 128;
         if (W.zeros) {
             s.scale.zero_at = at;
             s.scale.zero_pitch = maps.scale_tensor ? zeros : (groups + 15) / 16 * 16 | 16;
-            at += 16 * s.scale.zero_pitch;
+            at += rows * s.scale.zero_pitch;
         }
     }
     maps.by_hand = !maps.tensor || (FMT != kW16 && !maps.scale_tensor);
-    s.tile = (at + 1023) / 1024 * 1024;
-    s.columns_at = tiles * s.tile;
+    s.columns_at = (at + 1023) / 1024 * 1024;
     s.bytes = (s.columns_at + more + 1023) / 1024 * 1024;
     return s;
 }
+
+// The tensor copies of 128 bytes of each of `box` rows of a matrix [rows, row_bytes], rows `pitch` bytes apart, for
+// `chunks` runs of 128 bytes at once where a row is a whole number of them (a 3-dimensional map), or else one.
+moe_status make_column_map(CUtensorMap &map, const void *at, int row_bytes, int rows, int64_t pitch, int box, int chunks);
 
 // Encodes the tensor copies that slot_plan chose for W's `rows` rows (weight_maps.cu).
 moe_status make_maps(WeightMaps &m, const SlotPlan &plan, const WeightView &W, int row_bytes, int64_t rows, int scale_row,

@@ -50,19 +50,19 @@ moe_status make_maps(WeightMaps &m, const SlotPlan &plan, const WeightView &W, i
     const cuuint64_t n = static_cast<cuuint64_t>(rows), pitch = static_cast<cuuint64_t>(row_bytes);
     if (m.tensor && m.whole > 0) {
         const cuuint64_t size[3] = {kStripBytes, n, static_cast<cuuint64_t>(m.whole)}, stride[2] = {pitch, kStripBytes};
-        const cuuint32_t box[3] = {kStripBytes, 8, static_cast<cuuint32_t>(plan.strips)};
+        const cuuint32_t box[3] = {kStripBytes, static_cast<cuuint32_t>(plan.block), static_cast<cuuint32_t>(plan.strips)};
         if (!encode(m.panels, W.w, 3, size, stride, box, CU_TENSOR_MAP_SWIZZLE_128B))
             return MOE_ERR_CUDA;
     }
     if (m.tensor && row_bytes % kStripBytes != 0) {
         const cuuint64_t size[2] = {pitch, n}, stride[1] = {pitch};
-        const cuuint32_t box[2] = {kStripBytes, 8};
+        const cuuint32_t box[2] = {kStripBytes, static_cast<cuuint32_t>(plan.block)};
         if (!encode(m.strips, W.w, 2, size, stride, box, CU_TENSOR_MAP_SWIZZLE_128B))
             return MOE_ERR_CUDA;
     }
     const auto scales = [&](CUtensorMap &map, const void *at, int row, int panel) {
         const cuuint64_t size[2] = {static_cast<cuuint64_t>(row), n}, stride[1] = {static_cast<cuuint64_t>(row)};
-        const cuuint32_t box[2] = {static_cast<cuuint32_t>(panel), 8};
+        const cuuint32_t box[2] = {static_cast<cuuint32_t>(panel), static_cast<cuuint32_t>(plan.block)};
         return encode(map, at, 2, size, stride, box, CU_TENSOR_MAP_SWIZZLE_NONE);
     };
     if (m.scale_tensor && !scales(m.scales, W.scales, scale_row, plan.scale.pitch))
@@ -70,6 +70,19 @@ moe_status make_maps(WeightMaps &m, const SlotPlan &plan, const WeightView &W, i
     if (m.scale_tensor && zero_row && !scales(m.zeros, W.zeros, zero_row, plan.scale.zero_pitch))
         return MOE_ERR_CUDA;
     return MOE_OK;
+}
+
+moe_status make_column_map(CUtensorMap &map, const void *at, int row_bytes, int rows, int64_t pitch, int box, int chunks)
+{
+    if (!encoder())
+        return MOE_ERR_CUDA;
+    const cuuint64_t n = static_cast<cuuint64_t>(rows), p = static_cast<cuuint64_t>(pitch), bytes = static_cast<cuuint64_t>(row_bytes);
+    const cuuint64_t size3[3] = {kStripBytes, n, bytes / kStripBytes}, stride3[2] = {p, kStripBytes};
+    const cuuint64_t size2[2] = {bytes, n};
+    const cuuint32_t boxes[3] = {kStripBytes, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(chunks)};
+    const bool ok = row_bytes % kStripBytes == 0 ? encode(map, at, 3, size3, stride3, boxes, CU_TENSOR_MAP_SWIZZLE_128B)
+                                                 : encode(map, at, 2, size2, stride3, boxes, CU_TENSOR_MAP_SWIZZLE_128B);
+    return ok ? MOE_OK : MOE_ERR_CUDA;
 }
 
 } // namespace nqg
