@@ -801,6 +801,8 @@ struct WeightMaps {
     int32_t scale_tensor;  // the scales (and zero points, if any) of a panel are multiples of 16 bytes
     int32_t by_hand;       // lanes' own copies come with every slot
     uint32_t scale_bytes;  // of a panel's tensor copies of scales and zero points
+    int32_t plain;         // tensor copies alone, and a row is whole strips
+    uint32_t bytes;        // of a slot's tensor copies then
 };
 
 // A position in a ring.  Every group of consumers has a ring of its own: a slot
@@ -878,7 +880,28 @@ template <class F, int FMT>
 __device__ __forceinline__ void fill_by_tensor(uint32_t slot, uint32_t full, const SlotPlan &plan, const WeightView &W,
                                                const WeightMaps &maps, int panel, int lo, int hi, uint32_t more)
 {
-    const int strip = panel * plan.strips, blocks = 16 * plan.tiles / plan.block;
+    const int strip = panel * plan.strips;
+    if (maps.plain) {  // the usual case, in as few instructions as it takes: the producer is one warp
+        const bool pair = plan.half > 8 * kStripBytes;
+        mbar_arrive_expect_tx(full, maps.bytes + more);
+        tensor_3d(slot, &maps.panels, 0, lo, strip, full);
+        if (pair)
+            tensor_3d(slot + plan.half, &maps.panels, 0, hi, strip, full);
+        if constexpr (FMT != kW16) {
+            const uint32_t to = slot + plan.scale.at;
+            tensor_2d(to, &maps.scales, panel * plan.scale.pitch, lo, full);
+            if (pair)
+                tensor_2d(to + 8 * plan.scale.pitch, &maps.scales, panel * plan.scale.pitch, hi, full);
+            if (FMT == kWInt4 && plan.scale.zero_pitch) {
+                const uint32_t z = slot + plan.scale.zero_at;
+                tensor_2d(z, &maps.zeros, panel * plan.scale.zero_pitch, lo, full);
+                if (pair)
+                    tensor_2d(z + 8 * plan.scale.zero_pitch, &maps.zeros, panel * plan.scale.zero_pitch, hi, full);
+            }
+        }
+        return;
+    }
+    const int blocks = 16 * plan.tiles / plan.block;
     const bool by_panel = strip + plan.strips <= maps.whole || maps.whole * kStripBytes == F::row_bytes(W.K);
     const int here = by_panel ? plan.strips : min(plan.strips, (F::row_bytes(W.K) + kStripBytes - 1) / kStripBytes - strip);
     mbar_arrive_expect_tx(full, (maps.tensor ? 16 * plan.tiles * kStripBytes * here : 0) + maps.scale_bytes + more);
@@ -1155,9 +1178,9 @@ SlotPlan slot_plan(int warps, int strips, int tiles, bool pair, int more, const 
     s.tiles = tiles;
     s.block = pair ? 8 : rows;
     s.strip = s.block * kStripBytes;
-    s.half = pair ? strips * s.strip : 8 * kStripBytes;
+    s.half = pair ? (strips * s.strip > 8 * kStripBytes ? strips * s.strip : 2 * s.strip) : 8 * kStripBytes;
     maps.tensor = F::row_bytes(W.K) % 16 == 0;
-    int at = rows * strips * kStripBytes;
+    int at = pair ? 2 * s.half : rows * strips * kStripBytes;
     if (FMT != kW16) {
         const int shift = FMT == kWNvfp4 ? 4 : W.group_shift, size = FMT == kWNvfp4 ? 1 : 2;
         const int bytes = tensor_scale_bytes(F::kStripK, strips, W.K, shift, size, W.scales);
@@ -1176,6 +1199,8 @@ SlotPlan slot_plan(int warps, int strips, int tiles, bool pair, int more, const 
         }
     }
     maps.by_hand = !maps.tensor || (FMT != kW16 && !maps.scale_tensor);
+    maps.plain = !maps.by_hand && F::row_bytes(W.K) % kStripBytes == 0;
+    maps.bytes = rows * strips * kStripBytes + maps.scale_bytes;
     s.columns_at = (at + 1023) / 1024 * 1024;
     s.bytes = (s.columns_at + more + 1023) / 1024 * 1024;
     return s;
