@@ -161,7 +161,7 @@ __device__ __forceinline__ float activate(float g, bool gelu)
 {
     if (gelu)
         return 0.5f * g * (1.0f + tanhf(0.7978845608f * (g + 0.044715f * g * g * g)));
-    return g / (1.0f + expf(-g));
+    return __fdividef(g, 1.0f + expf(-g));  // the quotient of a huge divisor, 0 here, is below 2^-119
 }
 
 __device__ __forceinline__ float not_a_number() { return __int_as_float(0x7FC00000); }
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) gate_up_kern
         const int end = min(slabs, slab0 + left), first = L.first[a], n = L.first[a + 1] - first;
         left -= end - slab0;
         const float div = FMT == kWNvfp4 && p.w13_global ? p.w13_global[L.expert[a]] : 1.0f;
-        const float once = kScaled<F, BF16> ? 1.0f : early(div);  // otherwise the columns' factors hold it
+        const float back = 1.0f / (kScaled<F, BF16> ? 1.0f : early(div));  // otherwise the columns' factors hold it
         if (later)
             named_barrier_sync(1, 32 * consumers);  // the columns before have been read
         lay_out_strips<F, BF16>(columns, factors, [&](int c) { return p.x + L.token[first + c] * p.x_stride; }, n, warp, consumers,
@@ -302,10 +302,18 @@ __global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) gate_up_kern
                         gate += sum[w * 128];
                         up += sum[w * 128 + 8];
                     }
+                    if constexpr (FMT == kWNvfp4) {
+                        gate *= back;
+                        up *= back;
+                        if (div < 1.0f) {
+                            gate /= div;
+                            up /= div;
+                        }
+                    }
                     if (*failed)
                         gate = not_a_number();
                     act_piece<FMT, BF16>(p, first + c, slab)[element_at<Format<FMT, BF16, true>>(r)] = narrow16<BF16>(
-                        activate(gate / once / late(div), p.gelu) * (up / once / late(div)) * L.weight[first + c]);
+                        activate(gate, p.gelu) * up * L.weight[first + c]);
                 }
                 if (slab == slabs - 1) {  // zeros from I to the end of the last strip
                     const int more = strips_of<Format<FMT, BF16, true>>(p.I) * (Format<FMT, BF16, true>::kStripK / 8) - slabs;

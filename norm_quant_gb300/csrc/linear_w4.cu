@@ -1,11 +1,16 @@
 // linear_w4.cu -- out[m, n] = sum_k x[m, k] W[n, k] for a few rows x and a
 // matrix W in 4 bits (NVFP4, or integers with group scales).
 //
-// One CTA an SM; CTAs take equal, consecutive shares of the blocks of 16 rows.
-// The consumer warps form groups: the warps of a group split k and add their
-// fp32 sums in the order of the warps, and the groups take different blocks.
-// The columns are laid out once for all of them.  Columns that do not fit at
-// once are taken in rounds, for which the weights come from L2.
+// Two kernels.  In both a CTA, one an SM, takes an equal, consecutive share of
+// the blocks of 16 rows of W, and warps that split k add their fp32 sums in the
+// order of the warps, so that a result does not depend on timing.
+//
+// The wide one streams columns (rows of x) with the weights, and takes the
+// blocks of a CTA together, so that the columns are read once for up to 4.
+// The resident one holds the columns in shared memory for the whole of k, as
+// fp16 times a power of two.  It is there for bf16 columns and NVFP4 alone: e2m1
+// codes widen to fp16 in one conversion for two but to bf16 in five operations, and
+// with a column or two the widening is what a CTA's time goes into.
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -26,7 +31,6 @@ struct LinearParams {
     uint16_t *out;
     int64_t x_stride, out_stride;
     int32_t M, N, panels, groups;
-    int32_t round;  // columns at a time
     float divisor;
     int64_t stall;  // test hook: CTA 0 fills no more than this many slots (-1: off)
 };
@@ -46,10 +50,11 @@ __host__ __device__ inline uint32_t columns_at(const SlotPlan &s, int groups, in
     return sums_at(s, groups, panels) + groups * s.warps * 1024;
 }
 
-template <int FMT, bool BF16>
-__global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) linear_w4_kernel(const __grid_constant__ LinearParams p)
+__global__ void __launch_bounds__(32 * (kMaxConsumers<kWNvfp4> + 1), 1)
+    linear_w4_resident_kernel(const __grid_constant__ LinearParams p)
 {
-    using F = Format<FMT, BF16>;
+    using F = Format<kWNvfp4, true>;
+    static_assert(kScaled<F, true>);
     extern __shared__ __align__(1024) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = p.plan.warps, depth = p.plan.depth;
     const int consumers = warps * p.groups;
@@ -73,18 +78,14 @@ __global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) linear_w4_ke
     allow_dependent_launch();
     if (warp == consumers) {  // the producer
         struct Items {  // the slots of one group
-            int b, panel, round, start, last, step, panels, rounds;
+            int b, panel, last, step, panels;
             __device__ bool next(int &at, int &lo, int &hi)
             {
                 if (panel == panels) {
                     panel = 0;
                     b += step;
-                    if (b >= last) {
-                        b = start;
-                        ++round;
-                    }
                 }
-                if (round >= rounds || b >= last)
+                if (b >= last)
                     return false;
                 at = panel++;
                 lo = 16 * b;
@@ -92,123 +93,124 @@ __global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) linear_w4_ke
                 return true;
             }
         };
-        produce<F, FMT, false, false>(Items{first + lane, 0, 0, first + lane, last, p.groups, p.panels, (p.M + p.round - 1) / p.round}, p.groups,
-                        slots, bars, p.plan, p.W, p.maps, p.N,
-                        blockIdx.x == 0 && p.stall >= 0 ? p.stall : INT64_MAX, lane);
+        produce<F, kWNvfp4, false, false>(Items{first + lane, 0, last, p.groups, p.panels}, p.groups, slots, bars, p.plan, p.W,
+                                          p.maps, p.N, blockIdx.x == 0 && p.stall >= 0 ? p.stall : INT64_MAX, lane);
         return;
     }
     const int group = warp / warps, j = warp - group * warps;
-    Consumer<F, FMT, BF16> consumer(p.plan, p.W, failed, slots + group * depth * p.plan.bytes,
-                                    bars + group * depth * kBarrierBytes, 0, j, lane);
+    Consumer<F, kWNvfp4, true> consumer(p.plan, p.W, failed, slots + group * depth * p.plan.bytes,
+                                        bars + group * depth * kBarrierBytes, 0, j, lane);
     const uint32_t columns = slots + columns_at(p.plan, p.groups, p.panels);
     float *red = reinterpret_cast<float *>(smem + sums_at(p.plan, p.groups, p.panels)) + group * warps * 256;  // [2][warps][8 columns][16 rows]
+    lay_out_strips<F, true>(columns, factors, [&](int c) { return p.x + c * p.x_stride; }, p.M, warp, consumers, p.W.K,
+                            early(p.divisor), lane);
+    named_barrier_sync(1, 32 * consumers);
+    uint32_t swap;
+    const uint32_t column = columns + column_at<F>(p.M, lane, swap), size = column_bytes<F>(p.M, 1);
     int turn = 0;
-    for (int m0 = 0; m0 < p.M; m0 += p.round) {
-        const int n = min(p.round, p.M - m0);
-        if (m0 > 0)
-            named_barrier_sync(1, 32 * consumers);  // the columns before have been read
-        lay_out_strips<F, BF16>(columns, factors, [&](int c) { return p.x + (m0 + c) * p.x_stride; }, n, warp, consumers, p.W.K,
-                                early(p.divisor), lane);
-        named_barrier_sync(1, 32 * consumers);
-        uint32_t swap;
-        const uint32_t column = columns + column_at<F>(n, lane, swap), size = column_bytes<F>(n, 1);
-        for (int b = first + group; b < last; b += p.groups) {
-            float acc[4] = {};
-            for (int panel = 0; panel < p.panels; ++panel) {
-                consumer.wait();
-                consumer.template take<kScaled<F, BF16>>(acc, panel, column + panel * p.plan.strips * size, size, swap,
-                                                         smem_u32(factors + panel * p.plan.strips * kColumns));
+    for (int b = first + group; b < last; b += p.groups, ++turn) {
+        float acc[4] = {};
+        for (int panel = 0; panel < p.panels; ++panel) {
+            consumer.wait();
+            consumer.template take<true>(acc, panel, column + panel * p.plan.strips * size, size, swap,
+                                         smem_u32(factors + panel * p.plan.strips * kColumns));
+        }
+        float *set = red + (turn & 1) * warps * 128;
+        store_sums(set + j * 128, acc, lane);
+        named_barrier_sync(2 + group, 32 * warps);
+        // the other set is written next, and this one only after another barrier
+        if (j == turn % warps) {
+            const int n0 = 16 * b;
+            for (int i = lane; i < 16 * p.M; i += 32) {
+                float s = 0.0f;
+                for (int w = 0; w < warps; ++w)
+                    s += set[w * 128 + i];
+                if (*failed)
+                    s = __int_as_float(0x7FC00000);
+                s /= late(p.divisor);  // the columns' factors hold the early part
+                if (n0 + (i & 15) < p.N)
+                    p.out[(i >> 4) * p.out_stride + n0 + (i & 15)] = narrow16<true>(s);
             }
-            float *set = red + (turn & 1) * warps * 128;
-            store_sums(set + j * 128, acc, lane);
-            named_barrier_sync(2 + group, 32 * warps);
-            // the other set is written next, and this one only after another barrier
-            if (j == turn % warps) {
-                const int n0 = 16 * b;
-                for (int i = lane; i < 16 * n; i += 32) {
-                    float s = 0.0f;
-                    for (int w = 0; w < warps; ++w)
-                        s += set[w * 128 + i];
-                    if (*failed)
-                        s = __int_as_float(0x7FC00000);
-                    if (FMT == kWNvfp4)  // scaled columns' factors hold the early part
-                        s = s / (kScaled<F, BF16> ? 1.0f : early(p.divisor)) / late(p.divisor);
-                    if (n0 + (i & 15) < p.N)
-                        p.out[(m0 + (i >> 4)) * p.out_stride + n0 + (i & 15)] = narrow16<BF16>(s);
-                }
-            }
-            ++turn;
         }
     }
 }
 
-template <int FMT, bool BF16>
-moe_status launch_linear(LinearParams &p, moe_stream_t stream)
+// What a launch of that kernel takes, or false where the columns do not fit
+// beside three slots (two for each of several groups).
+bool plan_resident(LinearParams &p, int sms, size_t &smem)
 {
-    using F = Format<FMT, BF16>;
-    static SmemLimit limit;
-    const int sms = sm_count(), strips = strips_of<F>(p.W.K), blocks = (p.N + 15) / 16;
-    if (sms <= 0)
-        return MOE_ERR_CUDA;
+    using F = Format<kWNvfp4, true>;
+    const int strips = strips_of<F>(p.W.K), blocks = (p.N + 15) / 16, each = (blocks + sms - 1) / sms;
     // Few blocks: one group of as many warps as split k.  More: groups of up to 8, as many as there are warps.
-    const int each = (blocks + sms - 1) / sms;
     const int warps = split_warps(strips, each < 2 ? 16 : 8);
-    const auto bytes = [&](int round, int depth) {
+    const auto bytes = [&](int depth) {
         SlotPlan s = p.plan;
         s.depth = depth;
-        return static_cast<size_t>(columns_at(s, p.groups, p.panels)) + column_bytes<F>(round, s.strips * p.panels);
+        return static_cast<size_t>(columns_at(s, p.groups, p.panels)) + column_bytes<F>(p.M, s.strips * p.panels);
     };
-    // As many groups as let all columns (up to 8) fit beside two slots a group,
-    // three of a single one, since a second round would read the weights again;
-    // with one group, as many columns as fit.  Two strips a warp in a slot where
-    // that fits too.  What is left holds more slots.
-    const int most_groups = kMaxConsumers<FMT> / warps < each ? kMaxConsumers<FMT> / warps : each;
-    p.round = p.M < kColumns ? p.M : kColumns;
-    int least = 3;
+    const auto least = [&] { return p.groups < 2 ? 3 : 2; };
+    int most = kMaxConsumers<kWNvfp4> / warps;
+    most = most < each ? most : each;
+    most = most < kMaxGroups ? most : kMaxGroups;
+    // Two strips a warp in a slot where that fits for all groups, else one, and as
+    // many groups as fit; what is left holds more slots.
     for (int m = strips >= 2 * warps ? 2 : 1; m > 0; --m) {
         p.panels = (strips + m * warps - 1) / (m * warps);
-        p.plan = slot_plan<F, FMT>(warps, m * warps, 1, false, 0, p.W, p.maps);
-        p.groups = most_groups < kMaxGroups ? most_groups : kMaxGroups;
-        if (m > 1 && bytes(p.round, p.groups < 2 ? 3 : 2) > kSmemPerCta)
-            continue;
-        while (p.groups > 1 && bytes(p.round, 2) > kSmemPerCta)
-            --p.groups;
-        least = p.groups < 2 ? 3 : 2;
-        break;
+        p.plan = slot_plan<F, kWNvfp4>(warps, m * warps, 1, false, 0, p.W, p.maps);
+        for (p.groups = most; p.groups > 0; --p.groups) {
+            if (bytes(least()) > kSmemPerCta) {
+                if (m > 1)
+                    break;
+                continue;
+            }
+            p.plan.depth = least();
+            while (p.plan.depth * p.groups < 16 && bytes(p.plan.depth + 1) <= kSmemPerCta)
+                ++p.plan.depth;
+            smem = bytes(p.plan.depth);
+            return true;
+        }
     }
-    while (p.round > 0 && bytes(p.round, least) > kSmemPerCta)
-        --p.round;
-    if (p.round < 1)
-        return MOE_ERR_UNSUPPORTED;
-    p.plan.depth = least;
-    while (p.plan.depth * p.groups < 16 && bytes(p.round, p.plan.depth + 1) <= kSmemPerCta)
-        ++p.plan.depth;
-    const size_t smem = bytes(p.round, p.plan.depth);
+    return false;
+}
+
+moe_status launch_resident(LinearParams &p, int sms, size_t smem, moe_stream_t stream)
+{
+    static SmemLimit limit;
+    const int blocks = (p.N + 15) / 16;
     int dev = 0;
-    const auto kern = linear_w4_kernel<FMT, BF16>;
-    if (cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limit) != cudaSuccess) {
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        ensure_dynamic_smem(linear_w4_resident_kernel, dev, static_cast<int>(smem), limit) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
-    const moe_status st = make_maps<F, FMT>(p.maps, p.plan, p.W, p.N);
+    const moe_status st = make_maps<Format<kWNvfp4, true>, kWNvfp4>(p.maps, p.plan, p.W, p.N);
     if (st != MOE_OK)
         return st;
-    return PdlLaunch(static_cast<unsigned>(blocks < sms ? blocks : sms), 32 * (warps * p.groups + 1), smem, stream).run(kern, p);
+    return PdlLaunch(static_cast<unsigned>(blocks < sms ? blocks : sms), 32 * (p.plan.warps * p.groups + 1), smem, stream)
+        .run(linear_w4_resident_kernel, p);
 }
 
-// More than 8 rows of x.  A CTA takes the blocks of 16 rows that fall to it as
-// the tiles of a slot, in passes of up to 4.  The columns come with the weights, as they lie in memory, since they
-// do not fit in shared memory for all of k; they are read once for all tiles of
-// a pass.  A consumer warp takes strip j of every panel, or half of its steps, for
-// one tile and all columns, so that a weight is widened once.  A weight is used for 9 to 64
-// columns here, and with 32 and more the matrix instruction is the bound: 47
-// cycles of an SM a strip (4096 weights) and 8 columns, against 100 that the
-// strip's bytes take.
-constexpr int kWideWarps = 15;  // consumers; with the producer 16, for 128 registers each
+// The wide kernel.  A CTA takes its blocks of 16 rows as the tiles of a slot,
+// in passes of up to 4.  The columns come with the weights, as they lie in
+// memory, and are read once for all tiles of a pass.  A consumer warp takes strip j
+// of every panel, or half of its steps, for one tile and all columns (1, 2, 4 or 8 times
+// 8), so that a weight is widened once.  With 32 columns and more the matrix
+// instruction is the bound: 47 cycles of an SM a strip (4096 weights) and 8
+// columns, against 100 that the strip's bytes take; below that it is the issue
+// of the instructions that widen and lay out, 270 a strip.
+// N = 16384, K = 7168: fp16 columns and NVFP4, M = 1 to 8, 17.3 us, 3.8 TB/s of
+// weights; integers, group 128, 22 us.  N = K = 7168, M = 32: 17.1 us; M = 64, integers:
+// 29.5 us, 223 Tflop/s.
+//
+// Consumers: with the producer 24 warps, for 80 registers each, or 16, for 128.
+// With 23 instead of 15 consumers and 8 columns N = 16384 takes 17.4 instead of
+// 18.6 us, N = 7168 8.0 instead of 7.8.
+template <int NT>
+constexpr int kWideWarps = NT == 1 ? 23 : 15;
 
 // Warps that share a strip's steps: with more columns, shared memory holds fewer strips.
 template <int NT>
-constexpr int kShares = NT == 2 ? 1 : 2;
+constexpr int kShares = NT <= 2 ? 1 : 2;
 
 struct WideParams {
     WeightMaps maps;
@@ -228,7 +230,7 @@ __host__ __device__ inline uint32_t wide_sums_at(const SlotPlan &s)
 }
 
 template <int FMT, bool BF16, int NT>
-__global__ void __launch_bounds__(32 * (kWideWarps + 1), 1) linear_w4_wide_kernel(const __grid_constant__ WideParams p)
+__global__ void __launch_bounds__(32 * (kWideWarps<NT> + 1), 1) linear_w4_wide_kernel(const __grid_constant__ WideParams p)
 {
     using F = Format<FMT, BF16, true, true>;
     constexpr int kRows = 8 * NT;  // of the columns' boxes
@@ -349,7 +351,7 @@ moe_status launch_wide(const LinearParams &a, moe_stream_t stream)
     const int per_cta = (blocks + sms - 1) / sms;
     // equal passes of at most 4 tiles
     const int passes = (per_cta + 3) / 4, tiles = (per_cta + passes - 1) / passes;
-    for (int w = split_warps(strips, kWideWarps / (tiles * kShares<NT>));; --w) {
+    for (int w = split_warps(strips, kWideWarps<NT> / (tiles * kShares<NT>));; --w) {
         p.plan = slot_plan<F, FMT>(w, w, tiles, false, w * 4 * kRows * kStripBytes, p.W, p.maps);
         if (bytes(2) <= kSmemPerCta)
             break;
@@ -378,10 +380,23 @@ moe_status launch_wide(const LinearParams &a, moe_stream_t stream)
 template <int FMT, bool BF16>
 moe_status launch(LinearParams &p, moe_stream_t stream)
 {
-    return p.M <= kColumns ? launch_linear<FMT, BF16>(p, stream)
-           : p.M <= 16     ? launch_wide<FMT, BF16, 2>(p, stream)
-           : p.M <= 32     ? launch_wide<FMT, BF16, 4>(p, stream)
-                           : launch_wide<FMT, BF16, 8>(p, stream);
+    if constexpr (FMT == kWNvfp4 && BF16) {
+        const int sms = sm_count();
+        size_t smem;
+        if (sms <= 0)
+            return MOE_ERR_CUDA;
+        // Both kernels timed with K = 7168, us, resident against wide: N = 16384,
+        // M = 1: 18.3 / 23.9, 4: 21.1 / 23.9, 6: 23.6 / 24.0, 8: 27.7 / 24.0; N = 7168, M = 1:
+        // 8.6 / 10.8, 2: 9.4 / 10.5, 3: 10.5 / 10.6, 6: 15.2 / 10.4; N = 2048, M = 1: 4.8 / 5.9,
+        // 3: 6.9 / 5.6.  With little k there is not enough to do to lay columns out:
+        // N = 7000, K = 2048, M = 1: 5.1 / 4.8; N = K = 4096, M = 1: 5.8 / 6.1.
+        if (p.M <= 6 && p.M <= 1 + p.N / 4096 && p.W.K >= 4096 && plan_resident(p, sms, smem))
+            return launch_resident(p, sms, smem, stream);
+    }
+    return p.M <= 8    ? launch_wide<FMT, BF16, 1>(p, stream)
+           : p.M <= 16 ? launch_wide<FMT, BF16, 2>(p, stream)
+           : p.M <= 32 ? launch_wide<FMT, BF16, 4>(p, stream)
+                       : launch_wide<FMT, BF16, 8>(p, stream);
 }
 
 } // namespace

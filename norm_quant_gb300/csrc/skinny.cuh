@@ -157,7 +157,8 @@ __device__ __forceinline__ uint16_t narrow16(float f)
 // goes through it in kSteps steps of kMma instructions.  The order of k inside
 // a strip is free as long as both operands agree on it: in step u, lane
 // (g = lane / 4, t = lane % 4) takes kLane consecutive elements of the rows g
-// and g + 8 and of column g, from element at(u, t) of the strip on.
+// and g + 8 and of column g, from element 16 t + 8 u of the strip on with
+// 16-bit weights, 64 t + 16 u with NVFP4, and 64 u + 16 t with integers and STEPS.
 //
 // Rows of a strip lie 128 bytes apart with their 16-byte chunks exchanged as
 // the 128-byte swizzle of the tensor copies does it: chunk i of row g is at
@@ -220,8 +221,9 @@ __device__ __forceinline__ uint32_t lds1(uint32_t at)
 
 // Where a slot's scales lie, from the start of the slot, and how.
 struct ScalePlace {
-    uint32_t at, pitch;        // scales of a row
+    uint32_t at, pitch;            // scales of a row
     uint32_t zero_at, zero_pitch;  // zero points, pitch 0: none
+    int32_t down, zero_down;       // int4: a row's scales start at a group that is a multiple of down + 1
 };
 
 // How the slots of a ring are laid out.  A slot: for every strip of the panel
@@ -253,7 +255,6 @@ struct Format<kW16, BF16, NATIVE, false> {
         uint4 v[2];
     };
     __host__ __device__ static int row_bytes(int K) { return K * 2; }
-    __device__ static int at(int u, int t) { return 16 * t + 8 * u; }
     __device__ static uint32_t scale_at(const ScalePlace &, int, int) { return 0; }
     __device__ static void load_scales(Scales (&)[2], uint32_t, const SlotPlan &, const WeightView &, int, int, int) {}
     __device__ static void load(Slice &s, uint32_t tile)  // tile: of the lane's row, at lane_at()
@@ -301,7 +302,6 @@ struct Format<kWNvfp4, BF16, NATIVE, false> {
         uint4 v[2];
     };
     __host__ __device__ static int row_bytes(int K) { return K / 2; }
-    __device__ static int at(int u, int t) { return 64 * t + 16 * u; }
     // Of row r of the slot, from its start on; row r + 8 lies 8 rows further.
     __device__ static uint32_t scale_at(const ScalePlace &pl, int r, int t) { return pl.at + r * pl.pitch + 4 * t; }
     __device__ static void load_scales(Scales (&s)[2], uint32_t at, const SlotPlan &plan, const WeightView &, int, int i, int)
@@ -436,7 +436,6 @@ struct Format<kWInt4, BF16, NATIVE, STEPS> {
         uint32_t at;
     };
     __host__ __device__ static int row_bytes(int K) { return K / 2; }
-    __device__ static int at(int u, int t) { return 64 * u + 16 * t; }
     // the row alone: scales and zero points have pitches of their own
     __device__ static uint32_t scale_at(const ScalePlace &, int r, int) { return r; }
     // strip: of the row, i of the panel; from: the panel's first element.  A strip starts with a
@@ -444,12 +443,13 @@ struct Format<kWInt4, BF16, NATIVE, STEPS> {
     // is cleared later.
     __device__ static void load_scales(Scales (&s)[2], uint32_t at, const SlotPlan &plan, const WeightView &W, int strip, int, int from)
     {
-        const int shift = W.group_shift, first = ((strip * kStripK) >> shift) - (from >> shift);
+        const int shift = W.group_shift, group = (strip * kStripK) >> shift;
+        const int first = group - ((from >> shift) & ~plan.scale.down), zero = group - ((from >> shift) & ~plan.scale.zero_down);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = (at & 127) + 8 * h;  // slots are 1024-byte aligned
             const uint32_t a = (at & ~127u) + plan.scale.at + 2 * first + r * plan.scale.pitch;
-            const uint32_t z = (at & ~127u) + plan.scale.zero_at + first + r * plan.scale.zero_pitch;
+            const uint32_t z = (at & ~127u) + plan.scale.zero_at + zero + r * plan.scale.zero_pitch;
             s[h].zero = 0x08080808u;
             if (shift == 6) {  // four groups
                 const uint2 v = lds8(a);
@@ -695,7 +695,7 @@ __device__ __forceinline__ uint32_t column_at(int n, int lane, uint32_t &swap, i
 template <class F>
 __host__ __device__ __forceinline__ int piece_at(int i, int odd)
 {
-    // element k of a strip is lane tt's in step u, at(u, tt) + (0, 8)
+    // element k of a strip is lane tt's in step u
     const int k = 8 * i;
     int u, tt, half;
     if constexpr (F::kLane == 8) {
@@ -873,6 +873,20 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int pitch, int rows, Sou
 // lane's when its own copies have landed, if the producer's lanes make any.
 __host__ __device__ inline int fill_arrivals(const WeightMaps &maps) { return maps.by_hand ? 33 : 1; }
 
+// Where the tensor copies of scales and zero points of a panel that starts with
+// strip `strip` begin in a row, in bytes: a multiple of 16.
+template <class F, int FMT>
+__device__ __forceinline__ int scale_x(const SlotPlan &plan, const WeightView &W, int strip)
+{
+    return FMT == kWNvfp4 ? 16 * strip : 2 * (((strip * F::kStripK) >> W.group_shift) & ~plan.scale.down);
+}
+
+template <class F>
+__device__ __forceinline__ int zero_x(const SlotPlan &plan, const WeightView &W, int strip)
+{
+    return ((strip * F::kStripK) >> W.group_shift) & ~plan.scale.zero_down;
+}
+
 // The tensor copies into one slot of panel `panel` of the rows from lo on and,
 // where a tile is two blocks, from hi on; `more` bytes come by other copies.
 // One thread.
@@ -889,14 +903,16 @@ __device__ __forceinline__ void fill_by_tensor(uint32_t slot, uint32_t full, con
             tensor_3d(slot + plan.half, &maps.panels, 0, hi, strip, full);
         if constexpr (FMT != kW16) {
             const uint32_t to = slot + plan.scale.at;
-            tensor_2d(to, &maps.scales, panel * plan.scale.pitch, lo, full);
+            const int x = scale_x<F, FMT>(plan, W, strip);
+            tensor_2d(to, &maps.scales, x, lo, full);
             if (pair)
-                tensor_2d(to + 8 * plan.scale.pitch, &maps.scales, panel * plan.scale.pitch, hi, full);
+                tensor_2d(to + 8 * plan.scale.pitch, &maps.scales, x, hi, full);
             if (FMT == kWInt4 && plan.scale.zero_pitch) {
                 const uint32_t z = slot + plan.scale.zero_at;
-                tensor_2d(z, &maps.zeros, panel * plan.scale.zero_pitch, lo, full);
+                const int zx = zero_x<F>(plan, W, strip);
+                tensor_2d(z, &maps.zeros, zx, lo, full);
                 if (pair)
-                    tensor_2d(z + 8 * plan.scale.zero_pitch, &maps.zeros, panel * plan.scale.zero_pitch, hi, full);
+                    tensor_2d(z + 8 * plan.scale.zero_pitch, &maps.zeros, zx, hi, full);
             }
         }
         return;
@@ -916,10 +932,10 @@ __device__ __forceinline__ void fill_by_tensor(uint32_t slot, uint32_t full, con
                     tensor_2d(to + i * plan.strip, &maps.strips, (strip + i) * kStripBytes, row, full);
         }
         if (FMT != kW16 && maps.scale_tensor) {
-            tensor_2d(slot + plan.scale.at + b * 8 * plan.scale.pitch, &maps.scales, panel * plan.scale.pitch, row, full);
+            tensor_2d(slot + plan.scale.at + b * 8 * plan.scale.pitch, &maps.scales, scale_x<F, FMT>(plan, W, strip), row, full);
             if (FMT == kWInt4 && plan.scale.zero_pitch)
-                tensor_2d(slot + plan.scale.zero_at + b * 8 * plan.scale.zero_pitch, &maps.zeros, panel * plan.scale.zero_pitch,
-                          row, full);
+                tensor_2d(slot + plan.scale.zero_at + b * 8 * plan.scale.zero_pitch, &maps.zeros, zero_x<F>(plan, W, strip), row,
+                          full);
         }
     }
 }
@@ -1154,15 +1170,18 @@ inline int split_warps(int strips, int most)
     return (strips + each - 1) / each;
 }
 
-// Bytes of one row's scales or zero points (`size` bytes a group) in a panel,
-// if tensor copies can bring them: whole groups, multiples of 16 bytes; or 0.
+// Bytes of the box that brings one row's scales or zero points (`size` bytes a
+// group) of a panel, from a multiple of 16 bytes on, by tensor copies; or 0 where
+// rows do not allow them.
 inline int tensor_scale_bytes(int strip_k, int strips, int K, int shift, int size, const void *at)
 {
-    const int k = strips * strip_k;
-    if ((k & ((1 << shift) - 1)) != 0 || !aligned16(at))
+    if (!aligned16(at) || ((K >> shift) * size) % 16 != 0)
         return 0;
-    const int bytes = (k >> shift) * size;
-    return bytes % 16 == 0 && bytes <= 256 && ((K >> shift) * size) % 16 == 0 ? bytes : 0;
+    const int bytes = ((strips * strip_k + (1 << shift) - 1) >> shift) * size;
+    // what the panels start with is a multiple of the panel's bytes, or anything where groups are cut
+    const bool whole = (strips * strip_k) % (1 << shift) == 0 && bytes % 16 == 0;
+    const int box = whole ? bytes : (bytes + size + 15 + 15) / 16 * 16;
+    return box <= 256 ? box : 0;
 }
 
 // A slot with `strips` strips of `tiles` tiles of 16 rows, for `warps` warps
@@ -1191,6 +1210,8 @@ SlotPlan slot_plan(int warps, int strips, int tiles, bool pair, int more, const 
         const int groups = ((strips * F::kStripK) >> shift) + 2;
         s.scale.at = at;
         s.scale.pitch = maps.scale_tensor ? bytes : (size * groups + 15) / 16 * 16 | 16;
+        s.scale.down = maps.scale_tensor ? 7 : 0;
+        s.scale.zero_down = maps.scale_tensor ? 15 : 0;
         at = (at + rows * s.scale.pitch + 127) / 128 * 128;
         if (W.zeros) {
             s.scale.zero_at = at;

@@ -76,7 +76,9 @@ moe_status make_column_map(CUtensorMap &map, const void *at, int row_bytes, int 
 {
     if (!encoder())
         return MOE_ERR_CUDA;
-    const cuuint64_t n = static_cast<cuuint64_t>(rows), p = static_cast<cuuint64_t>(pitch), bytes = static_cast<cuuint64_t>(row_bytes);
+    const cuuint64_t n = static_cast<cuuint64_t>(rows), bytes = static_cast<cuuint64_t>(row_bytes);
+    // the pitch of a single row is its caller's business, and may pass what a map takes
+    const cuuint64_t p = rows > 1 ? static_cast<cuuint64_t>(pitch) : (bytes + 15) / 16 * 16;
     const cuuint64_t size3[3] = {kStripBytes, n, bytes / kStripBytes}, stride3[2] = {p, kStripBytes};
     const cuuint64_t size2[2] = {bytes, n};
     const cuuint32_t boxes[3] = {kStripBytes, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(chunks)};

@@ -171,6 +171,40 @@ def test_linear_matches_definition(M, N, K, fmt, group, zeros, io):
     _check_linear(M, N, K, fmt, group, zeros, io)
 
 
+# bf16 and NVFP4 with a few rows and much k take a kernel of their own
+@pytest.mark.parametrize("M,N,K", [(1, 1, 4096), (1, 33, 4112), (2, 4099, 4112), (3, 8193, 4096), (4, 12301, 4096),
+                                   (1, 40, 32768), (2, 4100, 32752)])
+def test_linear_few_rows_much_k(M, N, K):
+    _check_linear(M, N, K, "nvfp4", 16, False, "bf16")
+
+
+def test_linear_few_rows_much_k_non_finite_and_large():
+    gen = _gen(11)
+    W = ref.Weights(gen, (), 8200, 4096, "nvfp4")
+    x = torch.randn((3, 4096), generator=gen).to(torch.bfloat16)
+    x[0] *= 2.0 ** 100
+    x[0, 5] = 2.0 ** 120
+    x[2] *= 2.0 ** -100
+    want, tol = ref.linear(x, W.value, "bf16")
+    clean = _linear(x, W, "bf16")
+    assert (clean.double() - want).abs().le(tol).all()
+    x[1, 100] = math.nan
+    x[2, 3] = math.inf
+    W.scales[17, 5] = 0x7F
+    got = _linear(x, W, "bf16")
+    keep = [n for n in range(8200) if n != 17]
+    assert torch.equal(got[0, keep], clean[0, keep]) and got[:, 17].isnan().all()
+    assert got[1].isnan().all() and not got[2].isfinite().any()
+
+
+@pytest.mark.parametrize("K,group", [(1280, 64), (1152, 64), (7168, 128), (1792, 128), (10240, 512), (16384, 1024)])
+@pytest.mark.parametrize("M", [2, 12])
+def test_linear_int4_panels_that_start_inside_a_scale_vector(M, K, group):
+    for zeros in (False, True):
+        _check_linear(M, 50, K, "int4", group, zeros, "bf16")
+        _check_linear(M, 2500, K, "int4", group, zeros, "fp16")
+
+
 @pytest.mark.parametrize("K", [16, 32, 48, 80, 1040, 2064])
 def test_linear_nvfp4_rows_that_end_inside_a_step(K):
     for io in ("bf16", "fp16"):
