@@ -208,6 +208,10 @@ moe_status launch_resident(LinearParams &p, int sms, size_t smem, moe_stream_t s
 template <int NT>
 constexpr int kWideWarps = NT == 1 ? 23 : 15;
 
+// With 16 columns and fewer their permutations cost less than neighbours.
+template <int NT>
+constexpr int kWideSteps = NT > 2 ? kPairs : kApart;
+
 // Warps that share a strip's steps: with more columns, shared memory holds fewer strips.
 template <int NT>
 constexpr int kShares = NT <= 2 ? 1 : 2;
@@ -232,7 +236,7 @@ __host__ __device__ inline uint32_t wide_sums_at(const SlotPlan &s)
 template <int FMT, bool BF16, int NT>
 __global__ void __launch_bounds__(32 * (kWideWarps<NT> + 1), 1) linear_w4_wide_kernel(const __grid_constant__ WideParams p)
 {
-    using F = Format<FMT, BF16, true, true>;
+    using F = Format<FMT, BF16, true, kWideSteps<NT>>;
     constexpr int kRows = 8 * NT;  // of the columns' boxes
     extern __shared__ __align__(1024) uint8_t smem[];
     const SlotPlan &plan = p.plan;
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(32 * (kWideWarps<NT> + 1), 1) linear_w4_wide_k
 template <int FMT, bool BF16, int NT>
 moe_status launch_wide(const LinearParams &a, moe_stream_t stream)
 {
-    using F = Format<FMT, BF16, true, true>;
+    using F = Format<FMT, BF16, true, kWideSteps<NT>>;
     constexpr int kRows = 8 * NT;
     static SmemLimit limit;
     const int sms = sm_count(), strips = strips_of<F>(a.W.K), blocks = (a.N + 15) / 16;

@@ -179,9 +179,14 @@ constexpr int kMaxConsumers = FMT == kWInt4 ? 19 : 23;
 constexpr int kColumns = 8;
 
 // NATIVE: operands of the columns' type; otherwise nvfp4's are fp16.  STEPS:
-// nvfp4's lanes take 64 elements a step between them, as int4's do, so that
-// columns can be read as they lie in memory.
-template <int FMT, bool BF16, bool NATIVE = false, bool STEPS = false>
+// for columns that are read as they lie in memory.  nvfp4's lanes take 64
+// elements a step between them, as int4's do; and what widens two codes at a time
+// takes neighbours (kPairs), or codes 16 bits apart (kApart), which leaves it to the
+// columns to be paired the same way.  Neighbours take 2 to 4 operations more for 8 codes, and spare
+// each 8 columns 8 permutations for 32 codes.
+enum : int { kLaidOut, kApart, kPairs };
+
+template <int FMT, bool BF16, bool NATIVE = false, int STEPS = kLaidOut>
 struct Format;
 
 __device__ __forceinline__ uint4 lds16(uint32_t at)
@@ -244,7 +249,7 @@ struct SlotPlan {
 };
 
 template <bool BF16, bool NATIVE>
-struct Format<kW16, BF16, NATIVE, false> {
+struct Format<kW16, BF16, NATIVE, kLaidOut> {
     static constexpr float kPost = 1.0f;  // the sums are to be multiplied by this
     static constexpr bool kHalf = !BF16;  // the operands are fp16
     static constexpr int kStripK = 64, kSteps = 2, kLane = 8, kMma = 2;
@@ -286,7 +291,7 @@ struct Format<kW16, BF16, NATIVE, false> {
 // the elements 64 t to 64 t + 63 of a strip, so that the four scales that it
 // needs of a row are one word.
 template <bool BF16, bool NATIVE>
-struct Format<kWNvfp4, BF16, NATIVE, false> {
+struct Format<kWNvfp4, BF16, NATIVE, kLaidOut> {
     static constexpr bool kHalf = !(BF16 && NATIVE);
     // bf16: a code's bits s, eem moved to bits 15 and 8..6 are the bf16 number
     // value x 2^-126 (the subnormals included); the scale carries 2^100 of it
@@ -336,6 +341,7 @@ struct Format<kWNvfp4, BF16, NATIVE, false> {
         const float f = widen16<false>(static_cast<uint16_t>(twice)) * 0x1p100f;
         return f32x2_to_bf16x2(f, f);
     }
+    template <bool PAIRS = false>
     __device__ static void eight(uint32_t w, uint32_t scale, uint32_t *p)
     {
         uint32_t h[4];
@@ -348,6 +354,11 @@ struct Format<kWNvfp4, BF16, NATIVE, false> {
                 "  cvt.rn.f16x2.e2m1x2 %3, b3; }"
                 : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
                 : "r"(w));
+        } else if constexpr (PAIRS) {
+            const uint32_t v = w >> 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                h[j] = ((__byte_perm(w, v, 0x0400 + 0x0101 * j) & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
         } else {  // the sum of two shifted copies is one multiplication, on the other pipe
             const uint32_t v = w >> 8;
             h[0] = ((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u;
@@ -370,9 +381,10 @@ struct Format<kWNvfp4, BF16, NATIVE, false> {
     }
 };
 
-template <bool BF16>
-struct Format<kWNvfp4, BF16, true, true> : Format<kWNvfp4, BF16, true, false> {
-    using Base = Format<kWNvfp4, BF16, true, false>;
+template <bool BF16, int STEPS>
+struct Nvfp4Steps : Format<kWNvfp4, BF16, true, kLaidOut> {
+    using Base = Format<kWNvfp4, BF16, true, kLaidOut>;
+    static constexpr bool kSplit = Base::kSplit && STEPS == kApart;
     struct Scales {
         uint32_t codes[4];  // of the four groups of each step; lane t's is byte t
     };
@@ -409,10 +421,15 @@ struct Format<kWNvfp4, BF16, true, true> : Format<kWNvfp4, BF16, true, false> {
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(c));
         const uint32_t scale = Base::operand_scale(__byte_perm(two, two, 0x1010));
         const uint2 w = lds8(s.at ^ (32 * u));
-        Base::eight(w.x, scale, p);
-        Base::eight(w.y, scale, p + 4);
+        Base::template eight<STEPS == kPairs>(w.x, scale, p);
+        Base::template eight<STEPS == kPairs>(w.y, scale, p + 4);
     }
 };
+
+template <bool BF16>
+struct Format<kWNvfp4, BF16, true, kApart> : Nvfp4Steps<BF16, kApart> {};
+template <bool BF16>
+struct Format<kWNvfp4, BF16, true, kPairs> : Nvfp4Steps<BF16, kPairs> {};
 
 // 4-bit integers: code - zero has at most 5 bits and is exact in bf16 and fp16.
 // Times a 16-bit scale it would not be, so the scale multiplies the fp32 sums of
@@ -421,12 +438,12 @@ struct Format<kWNvfp4, BF16, true, true> : Format<kWNvfp4, BF16, true, false> {
 // A code in bits 3..0 of the mantissa of 128 (bf16) or 1024 (fp16) makes that
 // number plus the code, and in fp16 one in bits 7..4 makes 1024 + 16 code; either
 // less the zero point is one exact instruction.
-template <bool BF16, bool NATIVE, bool STEPS>
+template <bool BF16, bool NATIVE, int STEPS>
 struct Format<kWInt4, BF16, NATIVE, STEPS> {
     static constexpr bool kHalf = !BF16;
     static constexpr float kPost = 1.0f;
     static constexpr int kStripK = 256, kSteps = 4, kLane = 16, kMma = 4;
-    static constexpr bool kSplit = true;
+    static constexpr bool kSplit = STEPS != kPairs;
     static constexpr bool kAfter = true;
     struct Scales {
         uint32_t scale[2];  // two steps' in a word
@@ -484,6 +501,10 @@ struct Format<kWInt4, BF16, NATIVE, STEPS> {
     }
     __device__ static void operand(const Slice &s, const Scales &sc, int u, uint32_t (&p)[8])
     {
+        if constexpr (!kSplit) {
+            pairs(s, sc, u, p);
+            return;
+        }
         // in a register, so that and and or are one instruction
         const uint32_t base = opaque(BF16 ? 0x43004300u : 0x64006400u);
         const uint32_t less = __byte_perm(sc.zero, 0, 0x4040 + 0x0101 * u) | base;  // 128 or 1024, + zero
@@ -504,6 +525,29 @@ struct Format<kWInt4, BF16, NATIVE, STEPS> {
                     p[4 * h + 2 * b] = sub2<false>(and_or<0x000F000Fu>(v, base), less);
                     p[4 * h + 2 * b + 1] = fma_f16x2(and_or<0x00F000F0u>(v, base), kSixteenth, less16);
                 }
+            }
+        }
+    }
+    // Of a byte's two codes the lower one is taken as above.  The upper one is in
+    // fp16 bits 7..4 as above, and in bf16, moved down by one, bits 6..3 of the
+    // mantissa of 16, which makes 16 plus the code.
+    __device__ static void pairs(const Slice &s, const Scales &sc, int u, uint32_t (&p)[8])
+    {
+        const uint32_t base = opaque(BF16 ? 0x41804300u : 0x64006400u);
+        const uint32_t zero = __byte_perm(sc.zero, 0, 0x4040 + 0x0101 * u);
+        // bf16: 128 + zero and 16 + zero; fp16: -1024 - zero and -64 - zero
+        const uint32_t less = BF16 ? (zero & 0x0000FFFFu | (zero & 0xFFFF0000u) << 3) + 0x41804300u
+                                   : (zero & 0x0000FFFFu | (zero & 0xFFFF0000u) << 4) + 0xD400E400u;
+        const uint2 w8 = lds8(s.at ^ (32 * u));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w = h ? w8.y : w8.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (BF16)
+                    p[4 * h + i] = sub2<true>(and_or<0x0078000Fu>(__byte_perm(w, w >> 1, 0x0400 + 0x0101 * i), base), less);
+                else
+                    p[4 * h + i] = fma_f16x2(and_or<0x00F0000Fu>(__byte_perm(w, w, 0x0400 + 0x0101 * i), base), 0x2C003C00u, less);
             }
         }
     }
@@ -584,7 +628,8 @@ __device__ __forceinline__ void wide_product(float (&sums)[NT][4], uint32_t tile
         F::clear(a, sc[0], left, t);
         F::clear(b, sc[1], left, t);
     }
-#pragma unroll
+    constexpr int kAtOnce = F::kAfter && NT == 8 ? 1 : F::kSteps / SHARES;  // more would spill
+#pragma unroll kAtOnce
     for (int i = 0; i < F::kSteps / SHARES; ++i) {
         const int u = SHARES == 1 ? i : share * (F::kSteps / SHARES) + i;
         uint32_t p[8], q[8];
