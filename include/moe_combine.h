@@ -317,7 +317,9 @@ moe_status moe_tuning_set(int32_t vpt, int32_t rows_per_slot, int32_t ring_kib, 
  * slots, and CTA 0 of the dispatch permute stops loading token rows after
  * that many tokens, so that their bounded waits run out (about 2 s) and the
  * call records MOE_ERR_DEVICE_TIMEOUT in its status word; the other CTAs
- * finish normally.  Nothing faults, and the CUDA context stays usable.
+ * finish normally.  In the products of moe_layer.h, CTA 0's first ring (in the
+ * expert layer, of its first kernel) is filled no further than that many slots,
+ * and what depends on the missing weights becomes NaN.  Nothing faults, and the CUDA context stays usable.
  * -1 (the default) turns it off.  Returns MOE_OK or MOE_ERR_INVALID_ARG.
  * (No counterpart on the pages.) */
 moe_status moe_debug_stall(int64_t slots);

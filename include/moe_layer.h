@@ -6,10 +6,15 @@
  * Conventions are those of moe_combine.h: the caller owns every buffer,
  * the library allocates nothing and keeps no state between calls, all work is
  * enqueued on `stream` and returns without synchronising, arguments are
- * validated on the host before anything is launched, and every kernel is
+ * validated on the host before anything is launched, and every call is
  * launched with programmatic dependent launch and touches global memory only
  * after the previous kernel on the stream has completed.  Unlike the combine,
  * these operators define what non-finite values do; see each.
+ *
+ * Waits inside the kernels are bounded.  One that runs out (after 2 s, which no
+ * healthy launch comes near) turns every result that depends on it into NaN;
+ * the expert layer also records MOE_ERR_DEVICE_TIMEOUT in its status word.
+ * Nothing faults or hangs, and the context stays usable.
  */
 #ifndef MOE_LAYER_H
 #define MOE_LAYER_H
@@ -83,10 +88,14 @@ moe_status moe_select_experts(const void *logits, int64_t T, int32_t E, int64_t 
  *
  * M rows of x, 0 <= M <= MOE_FEW_TOKENS (M == 0 is a no-op); N >= 1 rows of W.
  * x and out may have strides between their rows.  Every weight is exact: an
- * e2m1 code times its e4m3 scale is a bf16 and an fp16 number, and an int4
- * code less its zero point is multiplied by its scale in fp32.  Sums are held
- * in fp32; a result beyond io_dtype's range rounds to an infinity, and a NaN
- * or infinity of x reaches that row of out only.
+ * e2m1 code times its e4m3 scale is a bf16 and an fp16 number, and sums of x
+ * times an int4 code less its zero point are multiplied by the scale in fp32.
+ * x is exact too, but for bf16 rows with NVFP4 weights, few rows and much K:
+ * these are multiplied as fp16 times a power of two for each 256 elements of a
+ * row, and an element below 2^-29 of the largest of its 256 is off by up to 2^-40 of
+ * that one.  Sums are held in fp32 in an order that depends on the sizes alone; a
+ * result beyond io_dtype's range rounds to an infinity, and a NaN or infinity
+ * of x reaches that row of out only.
  * ---------------------------------------------------------------------- */
 typedef struct moe_linear_w4_args {
     int64_t M;
@@ -125,12 +134,15 @@ size_t moe_linear_w4_args_size(void);
  * Numerics: sums, the activation and the products are fp32; the weighted
  * gated product router_weight * h is rounded to io_dtype once between the two
  * kernels (it is the second product's operand), and out once at the end.  In
- * fp16 a weighted product beyond 65504 becomes an infinity.  The result does
- * not depend on the other tokens of the batch in order or number beyond the
- * order of fp32 sums, and is the same from call to call.
+ * fp16 a weighted product beyond 65504 becomes an infinity.  With NVFP4 the
+ * first product takes bf16 rows of x as the linear may.  The result does not
+ * depend on the other tokens of the batch in order or number beyond the order
+ * of fp32 sums, and is the same from call to call.
  *
- * workspace: device memory of moe_layer_workspace_size(...) bytes, 16-byte
- * aligned, not shared by calls that may overlap.  Limits: T <= MOE_FEW_TOKENS,
+ * workspace: device memory of moe_layer_workspace_size(...) bytes (a row of I
+ * 16-bit values, rounded up to a multiple of 256, for each of T * top_k slots),
+ * 16-byte aligned, not shared by calls that may overlap; what it holds before a
+ * call does not matter.  Limits: T <= MOE_FEW_TOKENS,
  * E <= MOE_LAYER_MAX_EXPERTS, top_k <= MOE_MAX_TOP_K; H and I multiples of 8
  * (16-bit weights), 16 (NVFP4) or group_size (INT4).  T == 0 is a no-op.
  * ---------------------------------------------------------------------- */
@@ -154,7 +166,7 @@ typedef struct moe_layer_args {
     void *out;                  /* device [T, H] (io_dtype) */
     void *workspace;
     size_t workspace_bytes;
-    int32_t *status;            /* device int32 or NULL, zeroed by the caller */
+    int32_t *status;            /* device int32 or NULL, zeroed by the caller; the first error found */
     int32_t w_format;           /* moe_weight_format */
     int32_t group_size;         /* INT4 */
     int32_t activation;         /* moe_activation */

@@ -2,6 +2,7 @@
 selection, the 4-bit linear and the expert layer, at the sizes, masks, ids and
 values where they can go wrong."""
 import math
+import os
 
 import pytest
 import torch
@@ -518,3 +519,51 @@ def test_layer_empty_batch_is_a_no_op():
     nqg.moe_layer(x=p.x.to(DEV), topk_ids=p.ids.to(DEV), router_weights=p.rw.to(DEV),
                   out=torch.empty((0, 64), device=DEV, dtype=torch.bfloat16),
                   workspace=torch.empty(0, device=DEV, dtype=torch.uint8), **c)
+
+
+# ---------------------------------------------------------------- bounded waits
+
+@pytest.mark.parametrize("M,N,K,fmt,group", [(1, 3000, 4096, "nvfp4", 16), (5, 3000, 1024, "int4", 128),
+                                             (40, 3000, 1024, "nvfp4", 16)])
+def test_linear_wait_that_runs_out_marks_its_rows_and_the_context_survives(M, N, K, fmt, group):
+    gen = _gen(3)
+    W = ref.Weights(gen, (), N, K, fmt, group, False)
+    x = torch.randn((M, K), generator=gen).to(torch.bfloat16)
+    good = _linear(x, W, "bf16")
+    try:
+        nqg.moe_debug_stall(0)
+        got = _linear(x, W, "bf16")
+    finally:
+        nqg.moe_debug_stall(-1)
+    assert got[:, :16].isnan().all()
+    late = got.isnan().all(0)
+    assert torch.equal(got[:, ~late], good[:, ~late]) and int(late.sum()) < N // 16
+    assert torch.equal(_linear(x, W, "bf16"), good)
+
+
+def test_layer_wait_that_runs_out_is_reported_and_the_context_survives():
+    p = Problem(4, 512, 256, 8, 2)
+    p.ids[:] = torch.tensor([[0, 1], [2, 3], [0, 4], [5, 6]])
+    good = p.run()
+    assert p.status == 0
+    try:
+        nqg.moe_debug_stall(0)
+        got = p.run()
+    finally:
+        nqg.moe_debug_stall(-1)
+    assert p.status == nqg.MOE_ERR_DEVICE_TIMEOUT
+    assert got[[0, 2]].isnan().all()  # the tokens of the first expert, of whose values the first block makes some
+    assert torch.equal(got[[1, 3]], good[[1, 3]])
+    assert torch.equal(p.run(), good) and p.status == 0
+
+
+def test_example_decode_step():
+    import importlib.util
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_step.py")
+    spec = importlib.util.spec_from_file_location("decode_step", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _, error, status = module.main(["--tokens", "5", "--hidden", "512", "--inner", "256", "--experts", "8",
+                                    "--top-k", "2", "--steps", "3"])
+    # three roundings to bf16 on the way (2^-9 each at most) and the sum's
+    assert status == 0 and error < 4 * 2.0 ** -9
