@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
 
 from .build import LIB_PATH, build  # noqa: F401  (re-exported)
@@ -112,10 +113,10 @@ SYMBOLS = {
     "moe_select_experts": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_int64, C.c_int32, C.c_int32,
                                      C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_void_p, C.c_int32,
                                      C.c_void_p]),
-    "moe_linear_w4": (C.c_int, [C.POINTER(MoeLinearW4Args), C.c_void_p]),
+    "moe_linear_w4": (C.c_int, [C.c_void_p, C.c_void_p]),
     "moe_linear_w4_args_size": (C.c_size_t, []),
     "moe_layer_workspace_size": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
-    "moe_layer": (C.c_int, [C.POINTER(MoeLayerArgs), C.c_void_p]),
+    "moe_layer": (C.c_int, [C.c_void_p, C.c_void_p]),
     "moe_layer_args_size": (C.c_size_t, []),
 }
 
@@ -139,8 +140,8 @@ def lib() -> C.CDLL:
                 raise RuntimeError("libnqg.so ABI version mismatch")
             if L.moe_combine_args_size() != C.sizeof(MoeCombineArgs):
                 raise RuntimeError("moe_combine_args layout mismatch")
-            if (L.moe_linear_w4_args_size() != C.sizeof(MoeLinearW4Args)
-                    or L.moe_layer_args_size() != C.sizeof(MoeLayerArgs)):
+            if (not L.moe_linear_w4_args_size() == C.sizeof(MoeLinearW4Args) == _LINEAR_W4.size
+                    or not L.moe_layer_args_size() == C.sizeof(MoeLayerArgs) == _LAYER.size):
                 raise RuntimeError("moe_layer.h argument layout mismatch")
             _lib = L
     return _lib
@@ -336,26 +337,33 @@ def moe_combine(stream=None, **kw) -> None:
     _check(lib().moe_combine(C.byref(args), _stream(stream)), "moe_combine")
 
 
-def _rows(t, rows: int, width: int, elem: int, name: str):
-    """(pointer, elements from row to row) of a 2-D tensor whose rows may be
-    strided; ValueError if it is not [rows, width] of elem-byte elements or
-    its rows are not contiguous."""
+def _rows(t, elem: int, name: str):
+    """(rows, width, pointer, elements from row to row) of a 2-D CUDA tensor of
+    elem-byte elements whose rows may be strided; ValueError otherwise.
+
+    The few-token operators' kernels take a few microseconds, so their checks
+    and arguments are put together in as few calls as they take."""
     if not t.is_cuda:
         raise ValueError(f"{name}: tensors must be CUDA tensors")
-    if tuple(t.shape) != (rows, width) or t.element_size() != elem:
-        raise ValueError(f"{name} is {tuple(t.shape)} of {t.element_size()}-byte elements; this call needs "
-                         f"{(rows, width)} of {elem}-byte elements")
-    if width > 1 and t.stride(1) != 1:
+    if t.dim() != 2 or t.element_size() != elem:
+        raise ValueError(f"{name} is {tuple(t.shape)} of {t.element_size()}-byte elements; this call needs a matrix "
+                         f"of {elem}-byte elements")
+    rows, width = t.shape
+    stride, one = t.stride()
+    if one != 1 and width > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if rows > 1 else width
+    return rows, width, t.data_ptr(), stride if rows > 1 else width
 
 
 def _sized(t, nbytes: int, name: str):
-    """Pointer of a contiguous CUDA tensor (or None) that holds at least nbytes."""
+    """Pointer of a contiguous CUDA tensor that holds at least nbytes, or 0 for None."""
     if t is None:
-        return None
-    _need(t, nbytes, name)
-    return _ptr(t)
+        return 0
+    if t.nbytes < nbytes:
+        _need(t, nbytes, name)
+    if not t.is_cuda or not t.is_contiguous():
+        _ptr(t)
+    return t.data_ptr()
 
 
 def _scale_bytes(w_format, group_size: int, elements: int):
@@ -372,35 +380,45 @@ def moe_select_experts(logits, topk_ids, router_weights, *, scoring="softmax", r
     """logits [T, E] (rows may be strided) -> topk_ids int32 [T, k], the k
     experts with the largest logits in descending order (ties by the lower
     index; -1 where fewer are open), and router_weights [T, k]."""
-    T, E = logits.shape
+    T, E, lp, stride = _rows(logits, 4 if logits_dtype == "fp32" else 2, "logits")
     k = topk_ids.shape[-1]
-    lp, stride = _rows(logits, T, E, 4 if logits_dtype == "fp32" else 2, "logits")
-    _check(lib().moe_select_experts(lp, T, E, stride, WEIGHT_DTYPE[logits_dtype], k, SCORING[scoring],
-                                    1 if renormalize else 0, scale, _sized(topk_ids, T * k * 4, "topk_ids"),
-                                    _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2),
-                                           "router_weights"),
-                                    WEIGHT_DTYPE[weight_dtype], _stream_of(stream, logits)),
-           "moe_select_experts")
+    st = lib().moe_select_experts(lp, T, E, stride, WEIGHT_DTYPE[logits_dtype], k, SCORING[scoring],
+                                  1 if renormalize else 0, scale, _sized(topk_ids, T * k * 4, "topk_ids"),
+                                  _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2),
+                                         "router_weights"),
+                                  WEIGHT_DTYPE[weight_dtype], _stream_of(stream, logits))
+    if st:
+        raise MoeError(st, "moe_select_experts")
+
+
+# MoeLinearW4Args and MoeLayerArgs as the bytes of their fields: a third of the time a ctypes structure takes
+_LINEAR_W4 = struct.Struct("@qiiPqPPPfiiiPq")
+_LAYER = struct.Struct("@qiiiiPqPPPPPPPPPPPPPPNPiiiii4x")
+
+
+def _linear_w4_fields(x, w, w_scales, out, w_format="nvfp4", group_size=0, zeros=None, global_scale=1.0,
+                      io_dtype="bf16"):
+    M, K, xp, xs = _rows(x, 2, "x")
+    rows, N, op, os_ = _rows(out, 2, "out")
+    if rows != M:
+        raise ValueError(f"out has {rows} rows; x has {M}")
+    sb, zb = _scale_bytes(w_format, group_size, N * K)
+    return (M, N, K, xp, xs, _sized(w, N * K // 2, "w"), _sized(w_scales, sb, "w_scales"),
+            _sized(zeros, zb, "zeros"), global_scale, W_FORMAT[w_format], group_size, IO_DTYPE[io_dtype], op, os_)
 
 
 def linear_w4_args(x, w, w_scales, out, *, w_format="nvfp4", group_size=0, zeros=None, global_scale=1.0,
                    io_dtype="bf16") -> MoeLinearW4Args:
     """Fills a MoeLinearW4Args from tensors: x [M, K], w uint8 [N, K / 2], out [M, N]."""
-    M, K = x.shape
-    N = out.shape[-1]
-    xp, xs = _rows(x, M, K, 2, "x")
-    op, os_ = _rows(out, M, N, 2, "out")
-    sb, zb = _scale_bytes(w_format, group_size, N * K)
-    return MoeLinearW4Args(M, N, K, xp, xs, _sized(w, N * K // 2, "w"), _sized(w_scales, sb, "w_scales"),
-                           _sized(zeros, zb, "zeros"), global_scale, W_FORMAT[w_format], group_size,
-                           IO_DTYPE[io_dtype], op, os_)
+    return MoeLinearW4Args(*_linear_w4_fields(x, w, w_scales, out, w_format, group_size, zeros, global_scale, io_dtype))
 
 
 def moe_linear_w4(x, w, w_scales, out, *, stream=None, **kw) -> None:
     """out [M, N] = x [M, K] W^T with W in 4 bits; M <= 64.  Keyword arguments
     as in linear_w4_args()."""
-    _check(lib().moe_linear_w4(C.byref(linear_w4_args(x, w, w_scales, out, **kw)), _stream_of(stream, x)),
-           "moe_linear_w4")
+    st = lib().moe_linear_w4(_LINEAR_W4.pack(*_linear_w4_fields(x, w, w_scales, out, **kw)), _stream_of(stream, x))
+    if st:
+        raise MoeError(st, "moe_linear_w4")
 
 
 def moe_layer_workspace_size(T: int, top_k: int, I: int) -> int:
@@ -409,33 +427,41 @@ def moe_layer_workspace_size(T: int, top_k: int, I: int) -> int:
     return n.value
 
 
-def layer_args(*, x, topk_ids, router_weights, w13, w2, out, workspace, w13_scales=None, w2_scales=None,
-               w13_zeros=None, w2_zeros=None, w13_global=None, w2_global=None, w_format="none", group_size=0,
-               activation="silu", shared_out=None, residual=None, status=None, io_dtype="bf16",
-               weight_dtype="fp32") -> MoeLayerArgs:
-    """Fills a MoeLayerArgs from tensors.  E, H and I come from w2's shape
-    [E, H, I] (16-bit weights) or [E, H, I / 2] (4-bit codes)."""
-    T, H = x.shape
+def _layer_fields(x, topk_ids, router_weights, w13, w2, out, workspace, w13_scales=None, w2_scales=None,
+                  w13_zeros=None, w2_zeros=None, w13_global=None, w2_global=None, w_format="none", group_size=0,
+                  activation="silu", shared_out=None, residual=None, status=None, io_dtype="bf16",
+                  weight_dtype="fp32"):
+    E, H, inner = w2.shape
+    if x.shape[-1] != H:
+        raise ValueError(f"w2 has rows for H = {H}; x has H = {x.shape[-1]}")
+    T, H, xp, xs = _rows(x, 2, "x")
     k = topk_ids.shape[-1]
-    E, h2, i2 = w2.shape
     fmt = W_FORMAT[w_format]
-    inner = i2 if fmt == 0 else 2 * i2
-    if h2 != H:
-        raise ValueError(f"w2 has rows for H = {h2}; x has H = {H}")
-    xp, xs = _rows(x, T, H, 2, "x")
+    if fmt:
+        inner *= 2
     n2 = E * H * inner
     s2, z2 = _scale_bytes(w_format, group_size, n2)
     rows = T * H * 2
-    return MoeLayerArgs(
-        T, H, inner, E, k, xp, xs, _sized(topk_ids, T * k * 4, "topk_ids"),
-        _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2), "router_weights"),
-        _sized(w13, n2 * 4 if fmt == 0 else n2, "w13"), _sized(w13_scales, 2 * s2, "w13_scales"),
-        _sized(w13_zeros, 2 * z2, "w13_zeros"), _sized(w13_global, 4 * E, "w13_global"),
-        _sized(w2, n2 * 2 if fmt == 0 else n2 // 2, "w2"), _sized(w2_scales, s2, "w2_scales"),
-        _sized(w2_zeros, z2, "w2_zeros"), _sized(w2_global, 4 * E, "w2_global"),
-        _sized(shared_out, rows, "shared_out"), _sized(residual, rows, "residual"), _sized(out, rows, "out"),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _sized(status, 4, "status"),
-        fmt, group_size, ACTIVATION[activation], IO_DTYPE[io_dtype], WEIGHT_DTYPE[weight_dtype])
+    b2 = n2 // 2 if fmt else n2 * 2  # bytes of w2
+    return (T, H, inner, E, k, xp, xs, _sized(topk_ids, T * k * 4, "topk_ids"),
+            _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2), "router_weights"),
+            _sized(w13, 2 * b2, "w13"), _sized(w13_scales, 2 * s2, "w13_scales"),
+            _sized(w13_zeros, 2 * z2, "w13_zeros"), _sized(w13_global, 4 * E, "w13_global"),
+            _sized(w2, b2, "w2"), _sized(w2_scales, s2, "w2_scales"),
+            _sized(w2_zeros, z2, "w2_zeros"), _sized(w2_global, 4 * E, "w2_global"),
+            _sized(shared_out, rows, "shared_out"), _sized(residual, rows, "residual"), _sized(out, rows, "out"),
+            _sized(workspace, 0, "workspace"), workspace.nbytes, _sized(status, 4, "status"),
+            fmt, group_size, ACTIVATION[activation], IO_DTYPE[io_dtype], WEIGHT_DTYPE[weight_dtype])
+
+
+def layer_args(**kw) -> MoeLayerArgs:
+    """Fills a MoeLayerArgs from tensors, all by name: x [T, H], topk_ids and
+    router_weights [T, k], w13, w2, out, workspace, and optionally w13_scales,
+    w2_scales, w13_zeros, w2_zeros, w13_global, w2_global, w_format ("none"),
+    group_size, activation ("silu"), shared_out, residual, status, io_dtype
+    ("bf16") and weight_dtype ("fp32").  E, H and I come from w2's shape
+    [E, H, I] (16-bit weights) or [E, H, I / 2] (4-bit codes)."""
+    return MoeLayerArgs(*_layer_fields(**kw))
 
 
 def moe_layer(stream=None, **kw) -> None:
@@ -443,6 +469,8 @@ def moe_layer(stream=None, **kw) -> None:
     in layer_args() (or args=, a MoeLayerArgs)."""
     args = kw.pop("args", None)
     if args is not None:
-        _check(lib().moe_layer(C.byref(args), _stream(stream)), "moe_layer")
+        st = lib().moe_layer(C.byref(args), _stream(stream))
     else:
-        _check(lib().moe_layer(C.byref(layer_args(**kw)), _stream_of(stream, kw["x"])), "moe_layer")
+        st = lib().moe_layer(_LAYER.pack(*_layer_fields(**kw)), _stream_of(stream, kw["x"]))
+    if st:
+        raise MoeError(st, "moe_layer")
