@@ -50,6 +50,11 @@ __host__ __device__ inline uint32_t columns_at(const SlotPlan &s, int groups, in
     return sums_at(s, groups, panels) + groups * s.warps * 1024;
 }
 
+// The resident kernel.  The consumer warps form groups, each with a ring of its
+// own: the warps of a group split k, and the groups take different blocks of 16
+// rows.  Bound by the instructions that widen codes, about 300 a warp for 4096
+// weights.  K = 7168, M = 1: N = 16384, 17.4 us, 3.8 TB/s of weights; N = 2048, 4.7 us, of
+// which 2.5 are the launch.
 __global__ void __launch_bounds__(32 * (kMaxConsumers<kWNvfp4> + 1), 1)
     linear_w4_resident_kernel(const __grid_constant__ LinearParams p)
 {
@@ -199,8 +204,8 @@ moe_status launch_resident(LinearParams &p, int sms, size_t smem, moe_stream_t s
 // columns, against 100 that the strip's bytes take; below that it is the issue
 // of the instructions that widen and lay out, 270 a strip.
 // N = 16384, K = 7168: fp16 columns and NVFP4, M = 1 to 8, 17.3 us, 3.8 TB/s of
-// weights; integers, group 128, 22 us.  N = K = 7168, M = 32: 17.1 us; M = 64, integers:
-// 29.5 us, 223 Tflop/s.
+// weights; integers, group 128, 22 us.  N = K = 7168, NVFP4, M = 32: 16.2 us; M = 64,
+// integers: 24.0 us, 274 Tflop/s.
 //
 // Consumers: with the producer 24 warps, for 80 registers each, or 16, for 128.
 // With 23 instead of 15 consumers and 8 columns N = 16384 takes 17.4 instead of
