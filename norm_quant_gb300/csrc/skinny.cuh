@@ -171,10 +171,11 @@ __device__ __forceinline__ uint16_t narrow16(float f)
 
 constexpr int kStripBytes = 128;
 
-// Consumer warps of a CTA: with the producer's 24, for 80 registers a thread,
-// or 20, for 96 (int4, which would spill).
+// Consumer warps of a CTA: with the producer's 24, for 80 registers a thread, or,
+// for integers, 16, for 128.  With 20, a strip's steps do not fit unrolled: an expert layer
+// of H = 4096, I = 2048, E = 8, k = 2 takes 66 instead of 61 us for 32 tokens.
 template <int FMT>
-constexpr int kMaxConsumers = FMT == kWInt4 ? 19 : 23;
+constexpr int kMaxConsumers = FMT == kWInt4 ? 15 : 23;
 
 constexpr int kColumns = 8;
 
@@ -577,8 +578,7 @@ __device__ __forceinline__ void strip_product(float (&sums)[4], uint32_t tile, u
         F::clear(b, sc[1], left, t);
     }
     const uint32_t even = column + swap, odd = column - swap;
-    constexpr int kAtOnce = F::kAfter ? 2 : F::kSteps;  // fewer registers where the scales take some
-#pragma unroll kAtOnce
+#pragma unroll
     for (int u = 0; u < F::kSteps; ++u) {
         uint32_t p[F::kLane / 2], q[F::kLane / 2], c[F::kLane / 2];
 #pragma unroll
