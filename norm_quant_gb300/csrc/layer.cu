@@ -24,6 +24,12 @@ namespace nqg {
 namespace {
 
 
+// Consumer warps of the first kernel.  With integers 16 warps, for 128 registers a thread:
+// with 20 the steps of a strip do not fit unrolled, and an expert layer of H = 4096, I =
+// 2048, E = 8, k = 2 takes 66 instead of 61 us for 32 tokens.
+template <int FMT>
+constexpr int kGateUpConsumers = FMT == kWInt4 ? 15 : kMaxConsumers<FMT>;
+
 struct LayerParams {
     WeightMaps maps13, maps2;
     WeightView W13, W2;
@@ -214,10 +220,10 @@ __device__ __forceinline__ uint16_t *act_piece(const LayerParams &p, int pair, i
 // 1 token 108 us, 8 tokens 725 us, 0.96 and more of the copy rate.  4-bit weights are
 // bound by the instructions that widen them, 370 to 440 a warp for 4096 weights
 // with what belongs to a unit: 16 tokens, NVFP4, 212 us of 374 for both kernels; 8
-// tokens, H = 4096, I = 8192, E = 8, integers, 70 of 110.  Groups of 3 to 6 instead of 8 warps
+// tokens, H = 4096, I = 8192, E = 8, integers, 61 of 103.  Groups of 3 to 6 instead of 8 warps
 // are 2 % faster to 10 % slower with NVFP4, and with integers those of 4 or 5 are the fastest.
 template <int FMT, bool BF16>
-__global__ void __launch_bounds__(32 * (kMaxConsumers<FMT> + 1), 1) gate_up_kernel(const __grid_constant__ LayerParams p)
+__global__ void __launch_bounds__(32 * (kGateUpConsumers<FMT> + 1), 1) gate_up_kernel(const __grid_constant__ LayerParams p)
 {
     using F = Format<FMT, BF16>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -517,7 +523,7 @@ moe_status launch_layer(LayerParams &p, moe_stream_t stream)
     const int strips = strips_of<F>(p.H);
     const int64_t units = static_cast<int64_t>(p.E < slots ? p.E : slots) * (p.I / 8);
     const int64_t each = (units + sms - 1) / sms;
-    constexpr int kConsumers = kMaxConsumers<FMT>;
+    constexpr int kConsumers = kGateUpConsumers<FMT>;
     const int warps = split_warps(strips, each >= 2 ? (kConsumers < 16 ? 5 : 8) : kConsumers < 16 ? kConsumers : 16);
     const auto gate_bytes = [&](int columns, int depth) {
         SlotPlan s = p.gate_up;
@@ -566,9 +572,9 @@ moe_status launch_layer(LayerParams &p, moe_stream_t stream)
                lists_bytes(p.E, slots, p.down_most);
     };
     for (int tiles = per_cta < 3 ? per_cta : 3;; --tiles) {
-        const int down_warps = panel_strips * tiles > (kConsumers < 16 ? 7 : 12) ? (panel_strips + 1) / 2 : panel_strips;
+        const int down_warps = panel_strips * tiles > 12 ? (panel_strips + 1) / 2 : panel_strips;
         p.down = slot_plan<F2, FMT>(down_warps, panel_strips, tiles, false, column_bytes<F2>(p.down_most, panel_strips), p.W2, p.maps2);
-        p.down_groups = kConsumers / (down_warps * tiles) < kMaxGroups ? kConsumers / (down_warps * tiles) : kMaxGroups;
+        p.down_groups = kMaxConsumers<FMT> / (down_warps * tiles) < kMaxGroups ? kMaxConsumers<FMT> / (down_warps * tiles) : kMaxGroups;
         while (p.down_groups > 1 && down_bytes(2) > kSmemPerCta)
             --p.down_groups;
         if (down_bytes(2) <= kSmemPerCta)

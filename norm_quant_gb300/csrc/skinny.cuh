@@ -171,11 +171,10 @@ __device__ __forceinline__ uint16_t narrow16(float f)
 
 constexpr int kStripBytes = 128;
 
-// Consumer warps of a CTA: with the producer's 24, for 80 registers a thread, or,
-// for integers, 16, for 128.  With 20, a strip's steps do not fit unrolled: an expert layer
-// of H = 4096, I = 2048, E = 8, k = 2 takes 66 instead of 61 us for 32 tokens.
+// Consumer warps of a CTA: with the producer's 24, for 80 registers a thread, or
+// 17 with integers, whose steps would spill.
 template <int FMT>
-constexpr int kMaxConsumers = FMT == kWInt4 ? 15 : 23;
+constexpr int kMaxConsumers = FMT == kWInt4 ? 16 : 23;
 
 constexpr int kColumns = 8;
 
