@@ -218,7 +218,7 @@ __device__ __forceinline__ uint16_t *act_piece(const LayerParams &p, int pair, i
 // one part, whose columns are laid out once for all of them.
 // 16-bit weights are bound by HBM: H = 7168, I = 2048, E = 256, k = 8, both kernels,
 // 1 token 108 us, 8 tokens 725 us, 0.96 and more of the copy rate.  4-bit weights are
-// bound by the instructions that widen them, 370 to 440 a warp for 4096 weights
+// bound by the instructions that widen them, about 370 a warp for 4096 weights
 // with what belongs to a unit: 16 tokens, NVFP4, 212 us of 374 for both kernels; 8
 // tokens, H = 4096, I = 8192, E = 8, integers, 61 of 103.  Groups of 3 to 6 instead of 8 warps
 // are 2 % faster to 10 % slower with NVFP4, and with integers those of 4 or 5 are the fastest.
