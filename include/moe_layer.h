@@ -11,6 +11,9 @@
  * after the previous kernel on the stream has completed.  Unlike the combine,
  * these operators define what non-finite values do; see each.
  *
+ * Outputs must not overlap inputs, except that the layer's out may be its x,
+ * shared_out or residual (with rows one after the other).
+ *
  * Waits inside the kernels are bounded.  One that runs out (after 2 s, which no
  * healthy launch comes near) turns every result that depends on it into NaN;
  * the expert layer also records MOE_ERR_DEVICE_TIMEOUT in its status word.

@@ -513,6 +513,17 @@ def test_select_then_layer_as_a_decode_step():
     assert (out.cpu().double() - want).abs().le(tol).all()
 
 
+@pytest.mark.parametrize("where", ["x", "shared_out", "residual"])
+def test_layer_in_place(where):
+    p = Problem(7, 512, 256, 8, 2)
+    want = p.run()
+    c = lambda t: t.to(DEV)  # noqa: E731
+    kw = dict(x=c(p.x), shared_out=c(p.shared), residual=c(p.residual), **p.w13.cuda("w13"), **p.w2.cuda("w2"))
+    ws = torch.empty(nqg.moe_layer_workspace_size(7, 2, 256), device=DEV, dtype=torch.uint8)
+    nqg.moe_layer(topk_ids=c(p.ids), router_weights=c(p.rw), out=kw[where], workspace=ws, **kw)
+    assert torch.equal(kw[where].cpu(), want)
+
+
 def test_layer_empty_batch_is_a_no_op():
     p = Problem(0, 64, 64, 4, 2)
     c = p.w13.cuda("w13") | p.w2.cuda("w2")
