@@ -183,8 +183,9 @@ __device__ __forceinline__ uint32_t order_word(uint32_t bits, uint32_t e)
     if (bits == 0x8000u)
         bits = 0;  // -0
     const uint32_t key = bits & 0x8000u ? bits ^ 0xFFFFu : bits | 0x8000u;
-    // -inf is kInf's complement, NaNs lie below it or above +inf
-    const bool open = key - (0x8000u - kInf) < 2 * kInf;
+    // open: from next to -inf's key, which is kInf's complement, to +inf's, both included; NaNs lie
+    // below (and wrap around) or above
+    const bool open = key - (0x8000u - kInf) <= 2 * kInf;
     return open ? key << 16 | (0xFFFFu - e) : 0u;
 }
 
