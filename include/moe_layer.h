@@ -95,10 +95,13 @@ moe_status moe_select_experts(const void *logits, int64_t T, int32_t E, int64_t 
  * times an int4 code less its zero point are multiplied by the scale in fp32.
  * x is exact too, but for bf16 rows with NVFP4 weights, few rows and much K:
  * these are multiplied as fp16 times a power of two for each 256 elements of a
- * row, and an element below 2^-29 of the largest of its 256 is off by up to 2^-40 of
- * that one.  Sums are held in fp32 in an order that depends on the sizes alone; a
- * result beyond io_dtype's range rounds to an infinity, and a NaN or infinity
- * of x reaches that row of out only.
+ * row, and an element below 2^-29 of the largest of its 256 is off by up to 2^-39 of
+ * that one, or by up to 2^-150 max(g, 1) if that is more.  Sums are held in fp32 in
+ * an order that depends on the sizes alone (of bf16 rows with NVFP4 weights
+ * otherwise at 2^-26 of the products of x, code and scale, so that they do not
+ * overflow before they are divided by g: what falls below fp32's range is at most
+ * 2^-123 / g a product); a result beyond io_dtype's range rounds to an infinity,
+ * and a NaN or infinity of x reaches that row of out only.
  * ---------------------------------------------------------------------- */
 typedef struct moe_linear_w4_args {
     int64_t M;
@@ -137,8 +140,9 @@ size_t moe_linear_w4_args_size(void);
  * Numerics: sums, the activation and the products are fp32; the weighted
  * gated product router_weight * h is rounded to io_dtype once between the two
  * kernels (it is the second product's operand), and out once at the end.  In
- * fp16 a weighted product beyond 65504 becomes an infinity.  With NVFP4 the
- * first product takes bf16 rows of x as the linear may.  The result does not
+ * fp16 a weighted product beyond 65504 becomes an infinity.  With NVFP4 and bf16
+ * the first product takes rows of x as the linear does with few of them, and the
+ * second holds its sums as the linear does otherwise.  The result does not
  * depend on the other tokens of the batch in order or number beyond the order
  * of fp32 sums, and is the same from call to call.
  *

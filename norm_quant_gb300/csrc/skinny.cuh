@@ -26,8 +26,11 @@
 // are therefore held as fp16 times a power of two, chosen for each column and
 // each strip of k (256 elements) so that the largest magnitude lies in
 // [2^14, 2^15): every element down to 2^-29 of the largest keeps all its bits,
-// and a smaller one is off by at most 2^-40 of the largest, far below the
-// rounding of the fp32 sum that it goes into.
+// and a smaller one is off by at most 2^-39 of the largest (half of fp16's last
+// place, 2^-25, against 2^14), far below the rounding of the fp32 sum that it goes
+// into.  For a strip whose largest is below about 2^-111 max(g, 1), with g the
+// global scale, the power is smaller, so that the factor 2^-e / g stays a normal
+// float; an element is then off by up to 2^-150 max(g, 1).
 #pragma once
 
 #include <cstdint>
@@ -709,10 +712,11 @@ __device__ __forceinline__ uint32_t largest_bf16(uint4 v, uint32_t most)
 }
 
 // The exponent s for which a largest magnitude with bits `most` times 2^s lies
-// in [2^14, 2^15), as far as 2^s and 2^-s are normal floats.
-__device__ __forceinline__ int column_exponent(uint32_t most)
+// in [2^14, 2^15), as far as 2^-s / divisor is a normal float; divisor >= 1.
+__device__ __forceinline__ int column_exponent(uint32_t most, float divisor)
 {
-    return most ? min(14 + 127 - static_cast<int>(most >> 7), 126) : 0;
+    const int top = 125 + 127 - static_cast<int>(__float_as_uint(divisor) >> 23);
+    return most ? min(14 + 127 - static_cast<int>(most >> 7), top) : 0;
 }
 
 // Shared memory of `n` columns of `strips` strips.
@@ -768,8 +772,8 @@ constexpr bool kScaled = BF16 && F::kHalf;
 // Lays out the strips first, first + step, ... of columns [0, n) of K elements,
 // zero past K; strip s comes to columns + s * column_bytes(n, 1).  column(c):
 // where column c lies in global memory.  factors[8 s + c]: what the sums of the
-// strip's column c have to be multiplied by, a power of two over `divisor`
-// (kScaled).  One warp: it copies all its strips as they are, at once, and then
+// strip's column c have to be multiplied by, a power of two over `divisor`,
+// which is at least 1 (kScaled).  One warp: it copies all its strips as they are, at once, and then
 // rearranges each in place.
 template <class F, bool BF16, class Column>
 __device__ __forceinline__ void lay_out_strips(uint32_t columns, float *factors, Column column, int n, int first, int step,
@@ -796,7 +800,7 @@ __device__ __forceinline__ void lay_out_strips(uint32_t columns, float *factors,
             if (c < n)
                 v = lds16(strip + c0 * (F::kStripK * 2) + 16 * lane);
             if constexpr (kScaled<F, BF16>) {  // a column is 32 lanes' pieces
-                const int e = column_exponent(__reduce_max_sync(0xFFFFFFFFu, largest_bf16(v, 0)));
+                const int e = column_exponent(__reduce_max_sync(0xFFFFFFFFu, largest_bf16(v, 0)), divisor);
                 v = scale_to_f16(v, pow2(e));
                 if (lane == 0)
                     factors[s * kColumns + c] = pow2(-e) / divisor;
