@@ -355,10 +355,14 @@ def _rows(t, elem: int, name: str):
     return rows, width, t.data_ptr(), stride if rows > 1 else width
 
 
-def _sized(t, nbytes: int, name: str):
-    """Pointer of a contiguous CUDA tensor that holds at least nbytes, or 0 for None."""
+def _sized(t, nbytes: int, elem: int, name: str):
+    """Pointer of a contiguous CUDA tensor of elem-byte elements that holds at
+    least nbytes, or 0 for None.  Elements of another size (int64 ids, codes
+    packed into wider words) hold something else than the call takes them for."""
     if t is None:
         return 0
+    if t.itemsize != elem:
+        raise ValueError(f"{name} has {t.itemsize}-byte elements; this call takes {elem}-byte ones")
     if t.nbytes < nbytes:
         _need(t, nbytes, name)
     if not t.is_cuda or not t.is_contiguous():
@@ -367,12 +371,12 @@ def _sized(t, nbytes: int, name: str):
 
 
 def _scale_bytes(w_format, group_size: int, elements: int):
-    """(bytes of the scales, bytes of the zero points) of `elements` 4-bit weights."""
+    """(bytes of the scales, bytes of the zero points, bytes of a scale) of `elements` 4-bit weights."""
     if w_format == "nvfp4":
-        return elements // 16, 0
+        return elements // 16, 0, 1
     if w_format == "int4" and group_size > 0:
-        return elements // group_size * 2, elements // group_size
-    return 0, 0
+        return elements // group_size * 2, elements // group_size, 2
+    return 0, 0, 2 if w_format == "int4" else 1
 
 
 def moe_select_experts(logits, topk_ids, router_weights, *, scoring="softmax", renormalize=True, scale=1.0,
@@ -382,10 +386,10 @@ def moe_select_experts(logits, topk_ids, router_weights, *, scoring="softmax", r
     index; -1 where fewer are open), and router_weights [T, k]."""
     T, E, lp, stride = _rows(logits, 4 if logits_dtype == "fp32" else 2, "logits")
     k = topk_ids.shape[-1]
+    we = 4 if weight_dtype == "fp32" else 2
     st = lib().moe_select_experts(lp, T, E, stride, WEIGHT_DTYPE[logits_dtype], k, SCORING[scoring],
-                                  1 if renormalize else 0, scale, _sized(topk_ids, T * k * 4, "topk_ids"),
-                                  _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2),
-                                         "router_weights"),
+                                  1 if renormalize else 0, scale, _sized(topk_ids, T * k * 4, 4, "topk_ids"),
+                                  _sized(router_weights, T * k * we, we, "router_weights"),
                                   WEIGHT_DTYPE[weight_dtype], _stream_of(stream, logits))
     if st:
         raise MoeError(st, "moe_select_experts")
@@ -402,9 +406,9 @@ def _linear_w4_fields(x, w, w_scales, out, w_format="nvfp4", group_size=0, zeros
     rows, N, op, os_ = _rows(out, 2, "out")
     if rows != M:
         raise ValueError(f"out has {rows} rows; x has {M}")
-    sb, zb = _scale_bytes(w_format, group_size, N * K)
-    return (M, N, K, xp, xs, _sized(w, N * K // 2, "w"), _sized(w_scales, sb, "w_scales"),
-            _sized(zeros, zb, "zeros"), global_scale, W_FORMAT[w_format], group_size, IO_DTYPE[io_dtype], op, os_)
+    sb, zb, se = _scale_bytes(w_format, group_size, N * K)
+    return (M, N, K, xp, xs, _sized(w, N * K // 2, 1, "w"), _sized(w_scales, sb, se, "w_scales"),
+            _sized(zeros, zb, 1, "zeros"), global_scale, W_FORMAT[w_format], group_size, IO_DTYPE[io_dtype], op, os_)
 
 
 def linear_w4_args(x, w, w_scales, out, *, w_format="nvfp4", group_size=0, zeros=None, global_scale=1.0,
@@ -440,17 +444,19 @@ def _layer_fields(x, topk_ids, router_weights, w13, w2, out, workspace, w13_scal
     if fmt:
         inner *= 2
     n2 = E * H * inner
-    s2, z2 = _scale_bytes(w_format, group_size, n2)
+    s2, z2, se = _scale_bytes(w_format, group_size, n2)
     rows = T * H * 2
-    b2 = n2 // 2 if fmt else n2 * 2  # bytes of w2
-    return (T, H, inner, E, k, xp, xs, _sized(topk_ids, T * k * 4, "topk_ids"),
-            _sized(router_weights, T * k * (4 if weight_dtype == "fp32" else 2), "router_weights"),
-            _sized(w13, 2 * b2, "w13"), _sized(w13_scales, 2 * s2, "w13_scales"),
-            _sized(w13_zeros, 2 * z2, "w13_zeros"), _sized(w13_global, 4 * E, "w13_global"),
-            _sized(w2, b2, "w2"), _sized(w2_scales, s2, "w2_scales"),
-            _sized(w2_zeros, z2, "w2_zeros"), _sized(w2_global, 4 * E, "w2_global"),
-            _sized(shared_out, rows, "shared_out"), _sized(residual, rows, "residual"), _sized(out, rows, "out"),
-            _sized(workspace, 0, "workspace"), workspace.nbytes, _sized(status, 4, "status"),
+    b2, ce = (n2 // 2, 1) if fmt else (n2 * 2, 2)  # bytes of w2 and of its elements
+    we = 4 if weight_dtype == "fp32" else 2
+    return (T, H, inner, E, k, xp, xs, _sized(topk_ids, T * k * 4, 4, "topk_ids"),
+            _sized(router_weights, T * k * we, we, "router_weights"),
+            _sized(w13, 2 * b2, ce, "w13"), _sized(w13_scales, 2 * s2, se, "w13_scales"),
+            _sized(w13_zeros, 2 * z2, 1, "w13_zeros"), _sized(w13_global, 4 * E, 4, "w13_global"),
+            _sized(w2, b2, ce, "w2"), _sized(w2_scales, s2, se, "w2_scales"),
+            _sized(w2_zeros, z2, 1, "w2_zeros"), _sized(w2_global, 4 * E, 4, "w2_global"),
+            _sized(shared_out, rows, 2, "shared_out"), _sized(residual, rows, 2, "residual"),
+            _sized(out, rows, 2, "out"),
+            _ptr(workspace), workspace.nbytes, _sized(status, 4, 4, "status"),
             fmt, group_size, ACTIVATION[activation], IO_DTYPE[io_dtype], WEIGHT_DTYPE[weight_dtype])
 
 
