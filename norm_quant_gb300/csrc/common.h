@@ -49,43 +49,6 @@ cudaError_t ensure_dynamic_smem(Kern kern, int dev, int need, SmemLimit &lim)
     return e;
 }
 
-// A launch as a programmatic dependent of the previous kernel on the stream.
-struct PdlLaunch {
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = {};
-    PdlLaunch(unsigned grid, unsigned block, size_t smem, moe_stream_t stream)
-    {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.gridDim = dim3(grid);
-        cfg.blockDim = dim3(block);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    PdlLaunch(const PdlLaunch &) = delete;
-    template <typename P>
-    moe_status run(void (*kern)(P), const P &p) const
-    {
-        if (cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess)
-            return MOE_OK;
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
-};
-
-// log2 of an int4 group size (a power of two >= 64), or -1 for any other.
-inline int group_shift(int32_t group)
-{
-    if (group < 64 || (group & (group - 1)) != 0)
-        return -1;
-    int s = 6;
-    while ((1 << s) < group)
-        ++s;
-    return s;
-}
-
 // Status of the launches just made: MOE_ERR_CUDA if any failed.
 inline moe_status launch_status()
 {

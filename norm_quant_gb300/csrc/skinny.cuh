@@ -38,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include "common.h"
+#include "few_token.h"
 #include "ptx.cuh"
 
 namespace nqg {
