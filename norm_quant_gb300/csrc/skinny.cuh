@@ -1118,11 +1118,18 @@ __device__ __forceinline__ void produce(Items items, int groups, uint32_t slots,
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    // No copy is left in flight when the CTA ends, even if the consumers have given up: every slot's last fill,
+    // of this lap up to the next slot and of the lap before from it on.  (A parity that was never filled passes.)
+    for (int s = 0; lane < groups && s < plan.depth; ++s)
+        if (!mbar_wait_bounded(ring_bars + s * kBarrierBytes, at.phase ^ (s >= at.slot ? 1u : 0u), kWaitLimitNs))
+            break;
 }
 
 // Waits of the consumers.  Once one has run out (after two seconds, which no
 // healthy launch comes near) the warp goes through the rest of its work
 // without waiting, so that barriers still match, and the results are marked.
+// It gives no slot back any more, since a copy may still be on its way into it:
+// the producer fills no slot a second time, and its own wait runs out.
 struct Patience {
     volatile int32_t *failed;  // shared memory
     bool gone = false;
@@ -1161,7 +1168,7 @@ struct Consumer {
     __device__ __forceinline__ void give_back()
     {
         __syncwarp();
-        if ((threadIdx.x & 31) == 0)
+        if ((threadIdx.x & 31) == 0 && !patience.gone)
             mbar_arrive(bar + 8);
         slot += plan.bytes;
         bar += kBarrierBytes;
