@@ -258,12 +258,15 @@ __device__ __forceinline__ float exp_sum(const uint32_t (&key)[VPT], float most)
 __device__ __forceinline__ void write_slots(const SelectParams &p, int64_t t, int lane, bool open, float value, int my_id,
                                             float most, float all)
 {
-    // far below zero 1 + exp(l) is 1 in fp32: the sigmoids' ratios are those of
-    // the exponentials, which relative to the largest do not all underflow
-    const bool sigmoid = p.sigmoid && !(p.renorm && most < -60.0f);
     float w = 0.0f;
-    if (open)
-        w = sigmoid ? 1.0f / (1.0f + expf(-value)) : expf(finite(value) - most);
+    if (open && p.sigmoid) {
+        // Below zero exp(l) / (1 + exp(l)), whose ratios hold over the whole range when renormalised: relative to
+        // the largest (or to 0) the exponentials do not underflow before their ratio does.
+        const float from = p.renorm ? fminf(most, 0.0f) : 0.0f;
+        w = value > 0.0f ? 1.0f / (1.0f + expf(-value)) : expf(finite(value) - from) / (1.0f + expf(value));
+    } else if (open) {
+        w = expf(finite(value) - most);
+    }
     const float taken = p.renorm ? warp_sum(w) : 0.0f;
     if (lane >= p.k)
         return;

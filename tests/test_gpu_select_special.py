@@ -66,3 +66,21 @@ def test_select_special_values_in_a_large_batch(dt):
     assert torch.equal(ids, want_ids.repeat(T // 10, 1))
     # exponentials of arguments below 10 in magnitude, a sum of 7 and a division in fp32
     assert (w.double() - want_w.repeat(T // 10, 1)).abs().le(40 * 2.0 ** -24 * want_w.repeat(T // 10, 1)).all()
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16", "fp16"])
+def test_select_renormalised_sigmoid_far_below_zero(dt):
+    """Ratios of sigmoids hold down to the smallest normal float, wherever the largest logit lies."""
+    for most in (5.0, 0.0, -3.0, -16.0, -18.0, -59.0, -61.0, -200.0):
+        down = torch.tensor([0.0, -1.0, -20.0, -45.0, -70.0, -80.0, -86.0])
+        x = (most + down).expand(3, 7).contiguous()
+        for renorm in (True, False):
+            _check_select(x, 7, dt, "sigmoid", renorm, 1.0)
+    x = torch.randn((400, 5), generator=_gen(8)) * 60
+    _check_select(x, 4, dt, "sigmoid", True, 2.5)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16", "fp16"])
+def test_select_sigmoid_of_equal_lowest_values(dt):
+    x = torch.full((2, 40), torch.finfo(DT[dt]).min, dtype=DT[dt])
+    _check_select(x, 8, dt, "sigmoid", True, 1.0)
