@@ -130,8 +130,11 @@ size_t moe_linear_w4_args_size(void);
  *              + shared_out[t] + residual[t]              (both optional)
  *
  * w13 holds W1's I rows and then W3's for each expert ([E, 2 I, H]); w2 is
- * [E, H, I].  An expert's weights are read once however many tokens take it,
- * and only those of experts that a token takes.  A slot with id -1 adds
+ * [E, H, I].  Only the weights of experts that a token takes are read, once for
+ * every part of an expert's tokens.  A part has up to 8 tokens; fewer where the
+ * rows of x do not fit in shared memory, and where T * top_k slots spread thinly
+ * over E experts: at most twice what an expert has on average, at least 2 (T = 64,
+ * E = 256, top_k = 1: 3).  Skewed ids cost most there.  A slot with id -1 adds
  * nothing whatever its weight; other ids outside [0, E) are treated the same
  * and recorded in *status as MOE_ERR_INVALID_EXPERT.  A token may name an
  * expert more than once: its weights add up.  Tokens without any expert still

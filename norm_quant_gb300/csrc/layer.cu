@@ -4,8 +4,9 @@
 //   down     out[t]  = sum_e W2[e] a[t, e] + shared[t] + residual[t]
 //
 // Both are bound by the weights of the experts taken, 3 H I elements each,
-// which are read once.  The router's weight w[t, e] is multiplied into a, so
-// the second product sums over experts without a further step.
+// which are read once for every part of up to 8 of an expert's tokens.  The
+// router's weight w[t, e] is multiplied into a, so the second product sums over
+// experts without a further step.
 //
 // Every CTA makes the list of experts taken and of the tokens of each for
 // itself, from the ids: at most 64 tokens, one bit each.  Tokens of an expert
@@ -175,7 +176,9 @@ __device__ __forceinline__ float activate(float g, bool gelu)
 {
     if (gelu)
         return 0.5f * g * (1.0f + tanhf(0.7978845608f * (g + 0.044715f * g * g * g)));
-    return __fdividef(g, 1.0f + expf(-g));  // the quotient of a huge divisor, 0 here, is below 2^-119
+    // Two units in the last place at most, far below the 16-bit rounding that follows; the quotient of a huge
+    // divisor, 0 here, is below 2^-119.
+    return __fdividef(g, 1.0f + expf(-g));
 }
 
 __device__ __forceinline__ float not_a_number() { return __int_as_float(0x7FC00000); }
@@ -332,6 +335,9 @@ __global__ void __launch_bounds__(32 * (kGateUpConsumers<FMT> + 1), 1) gate_up_k
                     }
                     if (*failed)
                         gate = not_a_number();
+                    // Rounded to the I/O type, as the second product's operand: 32 bits would double its instructions.
+                    // Against 64 bits the layer is then off by 1.8e-3 to 2.4e-3 in bf16, where the rounding of out
+                    // alone makes 1.7e-3 (fp16: 2.1e-4 to 3.0e-4 and 2.1e-4).
                     act_piece<FMT, BF16>(p, first + c, slab)[element_at<Format<FMT, BF16, true>>(r)] = narrow16<BF16>(
                         activate(gate, p.gelu) * up * L.weight[first + c]);
                 }
@@ -512,7 +518,10 @@ moe_status launch_layer(LayerParams &p, moe_stream_t stream)
     const int slots = p.T * p.k;
     // Tokens of a part: twice what an expert that is taken has on average if ids
     // are uniform, at least 2.  Room for columns is taken from the slots in
-    // flight, and the few experts with more tokens are read again, from L2.
+    // flight, and the few experts with more tokens are read again, from L2, and
+    // widened again.  Ids that are not uniform at all pay for it: 64 tokens on one
+    // of E = 256 experts (k = 1, H = 4096, I = 2048) make 22 parts and take 120 us,
+    // 8 tokens 29; with NVFP4 99 and 24.
     const double taken = p.E * (1.0 - std::pow(1.0 - static_cast<double>(p.k < p.E ? p.k : p.E) / p.E, p.T));
     int most = static_cast<int>(std::ceil(2.0 * slots / (taken < 1.0 ? 1.0 : taken)));
     most = most < 2 ? 2 : most > kColumns ? kColumns : most;
