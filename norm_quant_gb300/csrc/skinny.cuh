@@ -81,14 +81,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Loads of columns: written by the kernel before, so they take the coherent path.
-__device__ __forceinline__ uint4 load_column(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-    return v;
-}
-
 // A constant that the compiler does not see.
 __device__ __forceinline__ uint32_t opaque(uint32_t v)
 {
