@@ -9,7 +9,7 @@
 // blocks of a CTA together, so that the columns are read once for up to 4.
 // The resident one holds the columns in shared memory for the whole of k, as
 // fp16 times a power of two.  It is there for bf16 columns and NVFP4 alone: e2m1
-// codes widen to fp16 in one conversion for two but to bf16 in five operations, and
+// codes widen to fp16 in one conversion for two but to bf16 in three or four operations, and
 // with a column or two the widening is what a CTA's time goes into.
 #include <cmath>
 #include <cstdint>
@@ -53,8 +53,8 @@ __host__ __device__ inline uint32_t columns_at(const SlotPlan &s, int groups, in
 // The resident kernel.  The consumer warps form groups, each with a ring of its
 // own: the warps of a group split k, and the groups take different blocks of 16
 // rows.  Bound by the instructions that widen codes, about 300 a warp for 4096
-// weights.  K = 7168, M = 1: N = 16384, 17.4 us, 3.8 TB/s of weights; N = 2048, 4.7 us, of
-// which 2.5 are the launch.
+// weights.  K = 7168, M = 1: N = 16384, 17.3 us, 3.8 TB/s of weights; N = 2048, 5.5 us, and
+// 4.7 with the weights in L2, of which 2.5 are the launch.
 __global__ void __launch_bounds__(32 * (kMaxConsumers<kWNvfp4> + 1), 1)
     linear_w4_resident_kernel(const __grid_constant__ LinearParams p)
 {
@@ -204,8 +204,11 @@ moe_status launch_resident(LinearParams &p, int sms, size_t smem, moe_stream_t s
 // columns, against 100 that the strip's bytes take; below that it is the issue
 // of the instructions that widen and lay out, 270 a strip.
 // N = 16384, K = 7168: fp16 columns and NVFP4, M = 1 to 8, 17.3 us, 3.8 TB/s of
-// weights; integers, group 128, 22 us.  N = K = 7168, NVFP4, M = 32: 16.2 us; M = 64,
-// integers: 24.0 us, 274 Tflop/s.
+// weights; integers, group 128, 22 us.  N = K = 7168, weights from HBM (in L2): NVFP4, M = 32, 16.6
+// (15.9) us; integers, M = 64, 24.9 (23.8) us, 264 Tflop/s.
+// Scales that tensor copies cannot take (rows that are no multiple of 16 bytes) are copied by the
+// producer's lanes: bf16, group 128 with zero points, N = 7168, M = 1: K = 8192 by tensor copies
+// 12.5 us, K = 7168 by lanes 17.5; NVFP4, N = 16384, M = 8: K = 2816 12.9, K = 2880 15.8.
 //
 // Consumers: with the producer 24 warps, for 80 registers each, or 16, for 128.
 // With 23 instead of 15 consumers and 8 columns N = 16384 takes 17.4 instead of
@@ -394,7 +397,7 @@ moe_status launch(LinearParams &p, moe_stream_t stream)
         size_t smem;
         if (sms <= 0)
             return MOE_ERR_CUDA;
-        // Both kernels timed with K = 7168, us, resident against wide: N = 16384,
+        // Both kernels timed with K = 7168 (weights that fit in L2 are there), us, resident against wide: N = 16384,
         // M = 1: 18.3 / 23.9, 4: 21.1 / 23.9, 6: 23.6 / 24.0, 8: 27.7 / 24.0; N = 7168, M = 1:
         // 8.6 / 10.8, 2: 9.4 / 10.5, 3: 10.5 / 10.6, 6: 15.2 / 10.4; N = 2048, M = 1: 4.8 / 5.9,
         // 3: 6.9 / 5.6.  With little k there is not enough to do to lay columns out:

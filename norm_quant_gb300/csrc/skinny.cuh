@@ -1,10 +1,10 @@
 // skinny.cuh -- products of a weight matrix with a few columns, the inner
 // loop of the 4-bit linear and of the few-token expert layer.
 //
-//   D[n, c] = sum_k W[n, k] X[c, k],   c < 8 columns (tokens)
+//   D[n, c] = sum_k W[n, k] X[c, k],   c < 8 columns (tokens), or up to 64 of the linear's
 //
-// One warp computes 16 rows of W by 8 columns over a range of k with
-// mma.sync m16n8k16: W is the 16-row operand, the tokens are the 8-column one,
+// One warp computes 16 rows of W by 8 columns, or by up to 8 times 8 with an
+// operand of W, over a range of k with mma.sync m16n8k16: W is the 16-row operand, the tokens are the 8-column one,
 // and the sums stay in fp32.  The products are bound by the stream of W (a
 // weight is used for a handful of tokens), so what counts is the bytes that
 // are in flight and the instructions spent on each weight.
@@ -19,10 +19,13 @@
 // costs about 80 cycles, 3.7 TB/s with rows of 1 KB.)
 //
 // Instructions: the columns are laid out in the order in which the matrix
-// instruction takes them, once for many rows.  Integers are widened to the
-// type of the columns, with one or-and and a half or three quarters of a shift
-// for two.  e2m1 codes take one conversion for two of them to fp16, and five
-// operations to bf16.  For bf16 columns that are used for many rows, the columns
+// instruction takes them, once for many rows (those that are streamed with the
+// weights are permuted for each use, or spared that by widening neighbours).
+// Integers are widened to the type of the columns with one and-or, one subtraction
+// or fma, and a quarter (fp16) to three quarters (bf16) of a shift for two;
+// neighbours with a permutation and, in bf16, a quarter of a shift.  e2m1 codes take
+// one conversion for two of them to fp16, and three operations and a quarter to
+// bf16 (neighbours one more), and both one multiplication by the scale.  For bf16 columns that are used for many rows, the columns
 // are therefore held as fp16 times a power of two, chosen for each column and
 // each strip of k (256 elements) so that the largest magnitude lies in
 // [2^14, 2^15): every element down to 2^-29 of the largest keeps all its bits,
