@@ -1,11 +1,11 @@
-"""MoE combine/finalize and few-token serving operators on one GB300 --
-Python binding of ``libnqg.so``.
+"""MoE combine/finalize, few-token serving operators and the feed-forward
+block for many tokens on one GB300 -- Python binding of ``libnqg.so``.
 
 Argument marshalling only: every step of the path runs in the library's
 CUDA kernels.  Tensors are torch CUDA tensors (torch provides device memory
 and streams); bf16 tensors may be ``torch.bfloat16`` or raw 16-bit views.
-The entry points have the names of the C ABI in ``include/moe_combine.h`` and
-``include/moe_layer.h``.
+The entry points have the names of the C ABI in ``include/moe_combine.h``,
+``include/moe_layer.h`` and ``include/moe_block.h``.
 
 There is no fallback: if the library is not built, every call raises.
 Build it with ``norm_quant_gb300.build.build()`` (``__graft_entry__.build()``).
@@ -26,6 +26,7 @@ LAYOUT = {"linear": 0, "swizzled": 1, "128x4": 1}
 W_FORMAT = {None: 0, "none": 0, "nvfp4": 1, "int4": 2}
 SCORING = {"softmax": 0, "sigmoid": 1}
 ACTIVATION = {"silu": 0, "gelu_tanh": 1}
+GATE = {None: 0, "none": 0, "channel": 1, "token": 2}
 FEW_TOKENS = 64  # MOE_FEW_TOKENS
 EXPERT_LAYOUT = {"grouped": 0, "slot_major": 1}
 MOE_OK = 0
@@ -80,6 +81,73 @@ class MoeLayerArgs(C.Structure):
     ]
 
 
+class MoeGatedLinearArgs(C.Structure):
+    """Mirror of ``moe_gated_linear_args`` (include/moe_block.h)."""
+    _fields_ = [
+        ("rows", C.c_int64), ("H", C.c_int32), ("I", C.c_int32), ("E", C.c_int32), ("activation", C.c_int32),
+        ("offsets", C.c_void_p), ("x", C.c_void_p), ("x_stride", C.c_int64), ("w13", C.c_void_p),
+        ("gate_up", C.c_void_p), ("gate_up_stride", C.c_int64), ("out", C.c_void_p), ("out_stride", C.c_int64),
+        ("status", C.c_void_p), ("io_dtype", C.c_int32),
+    ]
+
+
+class MoeGatedLinearBackwardArgs(C.Structure):
+    """Mirror of ``moe_gated_linear_backward_args`` (include/moe_block.h)."""
+    _fields_ = [
+        ("rows", C.c_int64), ("H", C.c_int32), ("I", C.c_int32), ("E", C.c_int32), ("activation", C.c_int32),
+        ("offsets", C.c_void_p), ("d_out", C.c_void_p), ("d_out_stride", C.c_int64), ("gate_up", C.c_void_p),
+        ("gate_up_stride", C.c_int64), ("x", C.c_void_p), ("x_stride", C.c_int64), ("w13", C.c_void_p),
+        ("d_x", C.c_void_p), ("d_x_stride", C.c_int64), ("d_w13", C.c_void_p), ("workspace", C.c_void_p),
+        ("workspace_bytes", C.c_size_t), ("status", C.c_void_p), ("io_dtype", C.c_int32), ("grad_dtype", C.c_int32),
+    ]
+
+
+class MoeGroupedLinearArgs(C.Structure):
+    """Mirror of ``moe_grouped_linear_args`` (include/moe_block.h)."""
+    _fields_ = [
+        ("rows", C.c_int64), ("K", C.c_int32), ("N", C.c_int32), ("E", C.c_int32), ("io_dtype", C.c_int32),
+        ("offsets", C.c_void_p), ("x", C.c_void_p), ("x_stride", C.c_int64), ("w", C.c_void_p), ("out", C.c_void_p),
+        ("out_stride", C.c_int64), ("status", C.c_void_p),
+    ]
+
+
+class MoeGroupedLinearBackwardArgs(C.Structure):
+    """Mirror of ``moe_grouped_linear_backward_args`` (include/moe_block.h)."""
+    _fields_ = [
+        ("rows", C.c_int64), ("K", C.c_int32), ("N", C.c_int32), ("E", C.c_int32), ("io_dtype", C.c_int32),
+        ("offsets", C.c_void_p), ("d_out", C.c_void_p), ("d_out_stride", C.c_int64), ("x", C.c_void_p),
+        ("x_stride", C.c_int64), ("w", C.c_void_p), ("d_x", C.c_void_p), ("d_x_stride", C.c_int64),
+        ("d_w", C.c_void_p), ("status", C.c_void_p), ("grad_dtype", C.c_int32),
+    ]
+
+
+class MoeBlockNormArgs(C.Structure):
+    """Mirror of ``moe_block_norm_args`` (include/moe_block.h)."""
+    _fields_ = [
+        ("T", C.c_int64), ("H", C.c_int32), ("io_dtype", C.c_int32), ("y", C.c_void_p), ("residual", C.c_void_p),
+        ("post_gamma", C.c_void_p), ("pre_gamma", C.c_void_p), ("gate", C.c_void_p), ("gate_kind", C.c_int32),
+        ("block_scale", C.c_float), ("residual_scale", C.c_float), ("eps", C.c_float), ("weight_bias", C.c_float),
+        ("residual_out", C.c_void_p), ("norm_out", C.c_void_p),
+    ]
+
+
+class MoeBlockNormBackwardArgs(C.Structure):
+    """Mirror of ``moe_block_norm_backward_args`` (include/moe_block.h)."""
+    _fields_ = [
+        ("T", C.c_int64), ("H", C.c_int32), ("io_dtype", C.c_int32), ("y", C.c_void_p), ("residual", C.c_void_p),
+        ("post_gamma", C.c_void_p), ("pre_gamma", C.c_void_p), ("gate", C.c_void_p), ("gate_kind", C.c_int32),
+        ("block_scale", C.c_float), ("residual_scale", C.c_float), ("eps", C.c_float), ("weight_bias", C.c_float),
+        ("d_residual_out", C.c_void_p), ("d_norm_out", C.c_void_p), ("d_y", C.c_void_p), ("d_residual", C.c_void_p),
+        ("d_post_gamma", C.c_void_p), ("d_pre_gamma", C.c_void_p), ("d_gate", C.c_void_p), ("workspace", C.c_void_p),
+        ("workspace_bytes", C.c_size_t),
+    ]
+
+
+_BLOCK_ARGS = {"moe_gated_linear": MoeGatedLinearArgs, "moe_gated_linear_backward": MoeGatedLinearBackwardArgs,
+               "moe_grouped_linear": MoeGroupedLinearArgs, "moe_grouped_linear_backward": MoeGroupedLinearBackwardArgs,
+               "moe_block_norm": MoeBlockNormArgs, "moe_block_norm_backward": MoeBlockNormBackwardArgs}
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {moe_status_string(status)} ({status})")
@@ -89,7 +157,7 @@ class MoeError(RuntimeError):
 _lock = threading.Lock()
 _lib = None
 
-# C symbols declared in include/moe_combine.h and include/moe_layer.h, with (restype, argtypes).
+# C symbols declared in include/*.h, with (restype, argtypes).
 SYMBOLS = {
     "moe_abi_version": (C.c_int, []),
     "moe_status_string": (C.c_char_p, [C.c_int]),
@@ -118,7 +186,12 @@ SYMBOLS = {
     "moe_layer_workspace_size": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
     "moe_layer": (C.c_int, [C.c_void_p, C.c_void_p]),
     "moe_layer_args_size": (C.c_size_t, []),
+    "moe_gated_linear_backward_workspace_size": (C.c_int, [C.c_int64, C.c_int32, C.POINTER(C.c_size_t)]),
+    "moe_block_norm_backward_workspace_size": (C.c_int, [C.c_int64, C.c_int32, C.POINTER(C.c_size_t)]),
 }
+for _name in _BLOCK_ARGS:
+    SYMBOLS[_name] = (C.c_int, [C.c_void_p, C.c_void_p])
+    SYMBOLS[_name + "_args_size"] = (C.c_size_t, [])
 
 
 def lib() -> C.CDLL:
@@ -143,6 +216,9 @@ def lib() -> C.CDLL:
             if (not L.moe_linear_w4_args_size() == C.sizeof(MoeLinearW4Args) == _LINEAR_W4.size
                     or not L.moe_layer_args_size() == C.sizeof(MoeLayerArgs) == _LAYER.size):
                 raise RuntimeError("moe_layer.h argument layout mismatch")
+            if any(not getattr(L, name + "_args_size")() == C.sizeof(cls) == _PACK[name].size
+                   for name, cls in _BLOCK_ARGS.items()):
+                raise RuntimeError("moe_block.h argument layout mismatch")
             _lib = L
     return _lib
 
@@ -480,3 +556,178 @@ def moe_layer(stream=None, **kw) -> None:
         st = lib().moe_layer(_LAYER.pack(*_layer_fields(**kw)), _stream_of(stream, kw["x"]))
     if st:
         raise MoeError(st, "moe_layer")
+
+
+# ------------------------------------------------------------------ the block for many tokens
+
+# The structures of moe_block.h as the bytes of their fields, in the order and with the padding of the ctypes mirrors.
+_CODES = {C.c_int64: "q", C.c_int32: "i", C.c_float: "f", C.c_void_p: "P", C.c_size_t: "N"}
+_PACK = {name: struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0q") for name, cls in _BLOCK_ARGS.items()}
+
+
+def _call(name: str, fields, stream, t) -> None:
+    st = getattr(lib(), name)(_PACK[name].pack(*fields), _stream_of(stream, t))
+    if st:
+        raise MoeError(st, name)
+
+
+def _matrix(t, rows: int, width: int, name: str):
+    """Pointer and stride of a matrix [rows, width] of 16-bit elements whose rows may be strided, or (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    r, w, p, stride = _rows(t, 2, name)
+    if r != rows or w != width:
+        raise ValueError(f"{name} is [{r}, {w}]; this call needs [{rows}, {width}]")
+    return p, stride
+
+
+def _experts(w, name: str, width):
+    """(experts, rows, columns) of weights [E, rows, columns]; ValueError unless there are `width` columns (None: any)."""
+    if w.dim() != 3 or (width is not None and w.shape[2] != width):
+        raise ValueError(f"{name} is {tuple(w.shape)}; this call needs three dimensions"
+                         + ("" if width is None else f", the last of {width}"))
+    return w.shape
+
+
+def _gradient(t, shape, grad_dtype: str, name: str):
+    """Pointer of a contiguous gradient of this shape, or 0 for None."""
+    if t is None:
+        return 0
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {tuple(t.shape)}; this call needs {tuple(shape)}")
+    size = 4 if grad_dtype == "fp32" else 2
+    return _sized(t, t.numel() * size, size, name)
+
+
+def _offsets(offsets, E: int):
+    return _sized(offsets, (E + 1) * 4, 4, "offsets")
+
+
+def moe_gated_linear(x, w13, out, *, offsets=None, gate_up=None, activation="silu", status=None, io_dtype="bf16",
+                     stream=None) -> None:
+    """out [R, I] = act(x W1^T) * (x W3^T) for x [R, H] and w13 [E, 2 I, H]
+    (W1's I rows, then W3's): row r goes through expert e where offsets[e] <= r <
+    offsets[e + 1] (int32 [E + 1]; None with one expert: every row).  gate_up
+    [R, 2 I], if given, receives both products for moe_gated_linear_backward."""
+    R, H, xp, xs = _rows(x, 2, "x")
+    E, two, _ = _experts(w13, "w13", H)
+    inner = two // 2
+    gp, gs = _matrix(gate_up, R, 2 * inner, "gate_up")
+    op, os_ = _matrix(out, R, inner, "out")
+    _call("moe_gated_linear", (
+        R, H, inner, E, ACTIVATION[activation], _offsets(offsets, E), xp, xs, _sized(w13, E * 4 * inner * H, 2, "w13"),
+        gp, gs, op, os_, _sized(status, 4, 4, "status"), IO_DTYPE[io_dtype]), stream, x)
+
+
+def moe_gated_linear_backward_workspace_size(rows: int, I: int) -> int:
+    n = C.c_size_t(0)
+    _check(lib().moe_gated_linear_backward_workspace_size(rows, I, C.byref(n)), "moe_gated_linear_backward_workspace_size")
+    return n.value
+
+
+def moe_gated_linear_backward(d_out, gate_up, *, x=None, w13=None, d_x=None, d_w13=None, workspace=None, offsets=None,
+                              activation="silu", status=None, io_dtype="bf16", grad_dtype=None, stream=None) -> None:
+    """Gradients of moe_gated_linear: d_x [R, H] (needs w13) and d_w13
+    [E, 2 I, H] (needs x) of grad_dtype ("fp32", or io_dtype, the default).
+    gate_up is what the forward call left.  workspace: uint8 CUDA tensor of
+    moe_gated_linear_backward_workspace_size(R, I) bytes."""
+    R, inner, dp, ds = _rows(d_out, 2, "d_out")
+    gp, gs = _matrix(gate_up, R, 2 * inner, "gate_up")
+    grad = grad_dtype or io_dtype
+    if (d_x is not None and w13 is None) or (d_w13 is not None and x is None):
+        raise ValueError("d_x needs w13 and d_w13 needs x")
+    if w13 is None and d_w13 is None:
+        raise ValueError("d_x or d_w13 has to be given")
+    E, two, H = _experts(w13 if w13 is not None else d_w13, "w13", None)
+    if two != 2 * inner:
+        raise ValueError(f"w13 has {two} rows an expert; d_out has {inner} columns, which need {2 * inner}")
+    xp, xs = _matrix(x, R, H, "x")
+    op, os_ = _matrix(d_x, R, H, "d_x")
+    _call("moe_gated_linear_backward", (
+        R, H, inner, E, ACTIVATION[activation], _offsets(offsets, E), dp, ds, gp, gs, xp, xs,
+        _sized(w13, E * 4 * inner * H, 2, "w13"), op, os_, _gradient(d_w13, (E, two, H), grad, "d_w13"),
+        _ptr(workspace) or 0, 0 if workspace is None else workspace.nbytes, _sized(status, 4, 4, "status"),
+        IO_DTYPE[io_dtype], WEIGHT_DTYPE[grad]), stream, d_out)
+
+
+def moe_grouped_linear(x, w, out, *, offsets=None, status=None, io_dtype="bf16", stream=None) -> None:
+    """out [R, N] = x W[e]^T for x [R, K] and w [E, N, K]; rows and experts as
+    in moe_gated_linear()."""
+    R, K, xp, xs = _rows(x, 2, "x")
+    E, N, _ = _experts(w, "w", K)
+    op, os_ = _matrix(out, R, N, "out")
+    _call("moe_grouped_linear", (R, K, N, E, IO_DTYPE[io_dtype], _offsets(offsets, E), xp, xs,
+                                 _sized(w, E * 2 * N * K, 2, "w"), op, os_, _sized(status, 4, 4, "status")), stream, x)
+
+
+def moe_grouped_linear_backward(d_out, *, x=None, w=None, d_x=None, d_w=None, offsets=None, status=None,
+                                io_dtype="bf16", grad_dtype=None, stream=None) -> None:
+    """Gradients of moe_grouped_linear: d_x [R, K] (needs w) and d_w [E, N, K]
+    (needs x) of grad_dtype ("fp32", or io_dtype, the default)."""
+    R, N, dp, ds = _rows(d_out, 2, "d_out")
+    grad = grad_dtype or io_dtype
+    if (d_x is not None and w is None) or (d_w is not None and x is None):
+        raise ValueError("d_x needs w and d_w needs x")
+    if w is None and d_w is None:
+        raise ValueError("d_x or d_w has to be given")
+    E, n, K = _experts(w if w is not None else d_w, "w", None)
+    if n != N:
+        raise ValueError(f"w has {n} rows an expert; d_out has {N} columns")
+    xp, xs = _matrix(x, R, K, "x")
+    op, os_ = _matrix(d_x, R, K, "d_x")
+    _call("moe_grouped_linear_backward", (
+        R, K, N, E, IO_DTYPE[io_dtype], _offsets(offsets, E), dp, ds, xp, xs, _sized(w, E * 2 * N * K, 2, "w"), op, os_,
+        _gradient(d_w, (E, N, K), grad, "d_w"), _sized(status, 4, 4, "status"), WEIGHT_DTYPE[grad]), stream, d_out)
+
+
+def _gate(gate, gate_kind, T: int, H: int):
+    kind = GATE[gate_kind]
+    if (gate is None) != (kind == 0):
+        raise ValueError(f"gate_kind {gate_kind!r} and gate {'missing' if gate is None else 'given'}")
+    if kind == 1:
+        return _sized(gate, 2 * H, 2, "gate"), kind
+    return _sized(gate, 4 * T, 4, "gate"), kind
+
+
+def moe_block_norm(y, residual=None, *, post_gamma=None, pre_gamma=None, gate=None, gate_kind=None, block_scale=1.0,
+                   residual_scale=1.0, eps=1e-6, weight_bias=0.0, residual_out=None, norm_out=None, io_dtype="bf16",
+                   stream=None) -> None:
+    """The norms after a block and before the next: residual_out [T, H] =
+    residual_scale * residual + block_scale * gate * norm(y; post_gamma) and
+    norm_out [T, H] = norm(that, unrounded; pre_gamma).  gate_kind "channel": gate
+    [H] of io_dtype; "token": fp32 [T]."""
+    T, H = y.shape
+    size = 2 * T * H
+    gp, kind = _gate(gate, gate_kind, T, H)
+    _call("moe_block_norm", (
+        T, H, IO_DTYPE[io_dtype], _sized(y, size, 2, "y"), _sized(residual, size, 2, "residual"),
+        _sized(post_gamma, 2 * H, 2, "post_gamma"), _sized(pre_gamma, 2 * H, 2, "pre_gamma"), gp, kind, block_scale,
+        residual_scale, eps, weight_bias, _sized(residual_out, size, 2, "residual_out"),
+        _sized(norm_out, size, 2, "norm_out")), stream, y)
+
+
+def moe_block_norm_backward_workspace_size(T: int, H: int) -> int:
+    n = C.c_size_t(0)
+    _check(lib().moe_block_norm_backward_workspace_size(T, H, C.byref(n)), "moe_block_norm_backward_workspace_size")
+    return n.value
+
+
+def moe_block_norm_backward(y, residual=None, *, post_gamma=None, pre_gamma=None, gate=None, gate_kind=None,
+                            block_scale=1.0, residual_scale=1.0, eps=1e-6, weight_bias=0.0, d_residual_out=None,
+                            d_norm_out=None, d_y=None, d_residual=None, d_post_gamma=None, d_pre_gamma=None, d_gate=None,
+                            workspace=None, io_dtype="bf16", stream=None) -> None:
+    """Gradients of moe_block_norm from those of its outputs (d_residual_out,
+    d_norm_out): d_y and d_residual [T, H], and in fp32 d_post_gamma [H],
+    d_pre_gamma [H] and d_gate ([H] or [T]).  workspace: uint8 CUDA tensor of
+    moe_block_norm_backward_workspace_size(T, H) bytes, for the sums over tokens."""
+    T, H = y.shape
+    size = 2 * T * H
+    gp, kind = _gate(gate, gate_kind, T, H)
+    _call("moe_block_norm_backward", (
+        T, H, IO_DTYPE[io_dtype], _sized(y, size, 2, "y"), _sized(residual, size, 2, "residual"),
+        _sized(post_gamma, 2 * H, 2, "post_gamma"), _sized(pre_gamma, 2 * H, 2, "pre_gamma"), gp, kind, block_scale,
+        residual_scale, eps, weight_bias, _sized(d_residual_out, size, 2, "d_residual_out"),
+        _sized(d_norm_out, size, 2, "d_norm_out"), _sized(d_y, size, 2, "d_y"),
+        _sized(d_residual, size, 2, "d_residual"), _sized(d_post_gamma, 4 * H, 4, "d_post_gamma"),
+        _sized(d_pre_gamma, 4 * H, 4, "d_pre_gamma"), _sized(d_gate, 4 * (T if kind == 2 else H), 4, "d_gate"),
+        _ptr(workspace) or 0, 0 if workspace is None else workspace.nbytes), stream, y)
