@@ -1,152 +1,553 @@
-// block_product.cu -- products of rows that are grouped by expert.
+// block_product.cu -- products of rows that are grouped by expert, on the
+// tensor cores of pairs of CTAs (tcgen05, cta_group::2).
 //
-// A simple form: a block makes 64 x 64 values of the result from tiles of 16
-// of the contraction in shared memory, with fp32 multiply-adds.
+// The four products (block.h) are one kernel over tiles of 256 x N values:
+//
+//   product   the 256 of a tile         its N                    contraction
+//   forward   features of W[e]          up to 256 rows of e      K, in lines of both operands
+//   gated     128 of W1[e] and of W3[e] up to 256 rows of e      K, the same
+//   input     columns of W[e]           up to 256 rows of e      rows of W[e] (an operand across)
+//   weight    columns of Y              columns of X             e's rows (both across)
+//
+// Rows are the N side because N comes in steps of 32: a group's rows are spread over as few tiles as hold them,
+// all of the same N, so that 128 rows an expert cost 128 to 160 columns and not 256.
+//
+// Each CTA of a pair holds 128 of the 256 and half of the N in shared memory (32 KB for 64 of the contraction at N =
+// 256, six such stages), which is what the matrix instruction of a pair wants: 64 bytes a cycle and SM instead of the 96 that a
+// 128 x 256 tile alone would take from L2.  Sums are in tensor memory, in two buffers of 256 columns, so that one
+// tile is written out while the next is multiplied.  Warps: 0 copies (TMA), 1 issues matrix instructions (in the
+// pair's first CTA, for both), 2 clears what a weight gradient's last step reads beyond its expert's rows, 4 to 7 write results.
+//
+// CTAs stay (one pair for two SMs) and take every P-th tile.  Within an expert, blocks of 8 tiles of one side pass along
+// the other, so that the pairs at work share their operands in L2.
 #include <cstdint>
 #include <cuda_runtime.h>
 
 #include "block.h"
 #include "block_math.cuh"
 #include "few_token.h"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace nqg {
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+constexpr int kThreads = 256;
+constexpr int kStages = 6;
+constexpr int kStep = 64;                   // elements of the contraction a stage holds: a line of 128 bytes
+constexpr int kLine = 2 * kStep;
+constexpr int kSide = 128;                  // rows of an operand a CTA holds at most
+constexpr int kOperand = kSide * kLine;
+constexpr int kStage = 2 * kOperand;
+constexpr int kChunk = 64 * kLine;          // 64 rows of an operand across
+constexpr int kMaxN = 256;
+constexpr int kBlock = 8;                   // tiles of one side that pass along the other together
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Params {
-    Product p;
+    CUtensorMap a, b;
+    int64_t n_rows;
+    int32_t E, width, out_width, contraction;  // contraction: 0 for the weights' gradient (an expert's rows)
+    int32_t m_tiles, n_tiles, n_columns;       // n_*: the weights' gradient's N side
+    int32_t box;                               // rows of a box of the rows' map
+    const int32_t *offsets;
+    uint8_t *out, *gate_up;
+    int64_t out_stride, gate_up_stride;        // elements
+    int32_t *status;
+    int32_t fp32_out;
+    int64_t stall;
 };
 
-template <bool BF16>
-__device__ __forceinline__ float value(const void *base, int64_t at)
-{
-    float lo, hi;
-    unpack2<BF16>(static_cast<const uint16_t *>(base)[at], lo, hi);
-    return lo;
-}
+// Shared memory, from its first 1024-byte boundary on.
+struct Layout {
+    static constexpr int staging = kStages * kStage;               // gated: what two warps hand each other, 2 x 4 x 2 KB
+    static constexpr int bars = staging + 16384;
+    static constexpr int full = bars, empty = full + 8 * kStages, tail = empty + 8 * kStages, sums_full = tail + 8 * kStages,
+                         sums_empty = sums_full + 16, done = sums_empty + 16, tmem = done + 8, first = tmem + 8;
+    static int bytes(int E) { return first + 2 * 4 * (E + 1) + 1024; }
+};
 
-template <bool BF16>
-__device__ __forceinline__ void put(void *base, int64_t at, float v)
-{
-    static_cast<uint16_t *>(base)[at] = static_cast<uint16_t>(pack2<BF16>(v, 0.0f));
-}
+struct Tile {
+    int e;
+    int64_t row;     // first row
+    int32_t rows;    // rows of the tile (N side), or of the expert (weights' gradient)
+    int32_t n;       // columns of the matrix instruction
+    int32_t m0, n0;  // first of the 256, first column (weights' gradient)
+    int32_t steps;
+};
 
-// offsets[e] as the kernels take it: within [0, rows], not below an earlier one.
-__device__ bool bounds_of(const Product &p, int e, int64_t &first, int64_t &last)
-{
-    if (!p.offsets) {
-        first = 0;
-        last = p.n_rows;
-        return true;
+template <int KIND>
+struct Schedule {
+    const Params &p;
+    const int32_t *first, *tile0;  // rows and (not for the weights' gradient) tiles of rows before each expert
+    int64_t total;
+
+    __device__ Schedule(const Params &q, const int32_t *f, const int32_t *t) : p(q), first(f), tile0(t)
+    {
+        total = KIND == kWeight ? static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles : static_cast<int64_t>(tile0[p.E]) * p.m_tiles;
     }
-    int64_t at = 0;
+
+    __device__ Tile at(int64_t q) const
+    {
+        Tile t;
+        int64_t within;
+        int along;  // tiles of the side that passes in blocks
+        if constexpr (KIND == kWeight) {
+            const int64_t each = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+            t.e = static_cast<int>(q / each);
+            within = q - t.e * each;
+            along = p.n_tiles;
+        } else {
+            const int32_t x = static_cast<int32_t>(q / p.m_tiles);
+            int lo = 0, hi = p.E;  // the last expert whose first tile is not behind x
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (tile0[mid] <= x)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            t.e = lo;
+            within = q - static_cast<int64_t>(tile0[lo]) * p.m_tiles;
+            along = tile0[lo + 1] - tile0[lo];
+        }
+        const int64_t block = within / (static_cast<int64_t>(kBlock) * p.m_tiles);
+        const int left = along - static_cast<int>(block) * kBlock, g = left < kBlock ? left : kBlock;
+        const int r = static_cast<int>(within - block * kBlock * p.m_tiles), m = r / g;
+        const int64_t i = block * kBlock + (r - m * g);
+        t.m0 = m * (KIND == kGated ? 128 : 256);
+        const int32_t begin = first[t.e], n = first[t.e + 1] - begin;
+        if constexpr (KIND == kWeight) {
+            t.row = begin;
+            t.rows = n;
+            t.n = p.n_columns;
+            t.n0 = static_cast<int>(i) * p.n_columns;
+            t.steps = (n + kStep - 1) / kStep;
+        } else {
+            t.n = ((n + along - 1) / along + 31) / 32 * 32;
+            t.row = begin + i * t.n;
+            const int64_t rest = begin + n - t.row;
+            t.rows = static_cast<int32_t>(rest < t.n ? rest : t.n);
+            t.n0 = 0;
+            t.steps = (p.contraction + kStep - 1) / kStep;
+        }
+        return t;
+    }
+};
+
+// The offsets as the kernels take them (none below its predecessor, all within [0, rows]) and, with TILES, the tiles of
+// rows before each expert.  One warp, 32 at a time.  Returns whether all were as they should be.
+template <bool TILES>
+__device__ bool read_offsets(const Params &p, int32_t *first, int32_t *tile0, int lane)
+{
     bool good = true;
-    for (int i = 0; i <= e + 1; ++i) {
-        int64_t v = p.offsets[i];
-        good = good && v >= at && v <= p.n_rows;
-        v = v < 0 ? 0 : (v > p.n_rows ? p.n_rows : v);
-        at = v > at ? v : at;
-        if (i == e)
-            first = at;
+    int32_t low = 0, tiles = 0, before = 0;
+    for (int base = 0; base <= p.E; base += 32) {
+        const int i = base + lane;
+        int32_t v = 0;
+        if (i <= p.E) {
+            v = p.offsets ? p.offsets[i] : (i == 0 ? 0 : static_cast<int32_t>(p.n_rows));
+            const int32_t c = v < 0 ? 0 : (v > p.n_rows ? static_cast<int32_t>(p.n_rows) : v);
+            good = good && c == v;
+            v = c;
+        }
+        int32_t most = v;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, most, o);
+            if (lane >= o)
+                most = u > most ? u : most;
+        }
+        most = most > low ? most : low;
+        good = good && (i > p.E || most == v);
+        if (i <= p.E)
+            first[i] = most;
+        if constexpr (TILES) {
+            int32_t prev = __shfl_up_sync(0xffffffffu, most, 1);
+            prev = lane == 0 ? before : prev;
+            // tiles of expert i - 1
+            int32_t n = i == 0 || i > p.E ? 0 : (most - prev + kMaxN - 1) / kMaxN;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int32_t u = __shfl_up_sync(0xffffffffu, n, o);
+                n += lane >= o ? u : 0;
+            }
+            if (i <= p.E)
+                tile0[i] = tiles + n;
+            tiles += __shfl_sync(0xffffffffu, n, 31);
+            before = __shfl_sync(0xffffffffu, most, 31);
+        }
+        low = __shfl_sync(0xffffffffu, most, 31);
     }
-    last = at;
-    return good;
+    return __all_sync(0xffffffffu, good);
 }
 
-// grid: (column tiles of the result, row tiles, experts)
-template <int KIND, bool BF16, int ACT>
-__global__ void __launch_bounds__(256) product_kernel(const Params q)
+template <bool BF16>
+__device__ __forceinline__ void store16(uint8_t *base, int64_t at, float v)
 {
-    const Product &p = q.p;
-    __shared__ float a[kStep][kTile + 4], b[2][kStep][kTile + 4];
-    __shared__ int64_t range[2];
+    reinterpret_cast<uint16_t *>(base)[at] = static_cast<uint16_t>(pack2<BF16>(v, 0.0f));
+}
+
+// One tile's sums to their place: warp `quarter` (0 to 3) of the CTA of rank `rank` has lanes 32 quarter on.
+template <int KIND, bool BF16, int ACT>
+__device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint32_t sums, int quarter, int lane, int rank, float *staging,
+                                           int &turn, bool lost)
+{
+    const float nan = __int_as_float(0x7FC00000);
+    const uint32_t from = sums + (static_cast<uint32_t>(quarter) << 21);
+    for (int c = 0; c < t.n; c += 32) {
+        __syncwarp();
+        uint32_t raw[32];
+        float v[32];
+        const bool none = KIND == kWeight && t.steps == 0;
+        if (!none && !lost) {
+            tmem_load32(from + c, raw);
+            tmem_load_wait();
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = lost ? nan : (none ? 0.0f : __uint_as_float(raw[j]));
+        if constexpr (KIND == kWeight) {
+            const int row = t.m0 + rank * kSide + 32 * quarter + lane;
+            const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
+            const int left = row < p.width ? p.out_width - t.n0 - c : 0;  // a multiple of 8
+            if (p.fp32_out) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                    if (j < left)
+                        *reinterpret_cast<float4 *>(p.out + 4 * (at + j)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; j += 8)
+                    if (j < left)
+                        *reinterpret_cast<uint4 *>(p.out + 2 * (at + j)) =
+                            make_uint4(pack2<BF16>(v[j], v[j + 1]), pack2<BF16>(v[j + 2], v[j + 3]), pack2<BF16>(v[j + 4], v[j + 5]),
+                                       pack2<BF16>(v[j + 6], v[j + 7]));
+            }
+        } else if constexpr (KIND == kGated) {
+            // quarters 0 and 1 hold W1's sums, 2 and 3 W3's of the same features
+            const int f = t.m0 + rank * 64 + 32 * (quarter & 1) + lane;
+            const bool up = quarter >= 2;
+            if (p.gate_up && f < p.out_width) {
+                const int64_t at = (t.row + c) * p.gate_up_stride + (up ? p.out_width : 0) + f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c + j < t.rows)
+                        store16<BF16>(p.gate_up, at + j * p.gate_up_stride, v[j]);
+            }
+            // the gate's warp takes the chunk's first 16 columns, the other the last
+            float *give = staging + (turn * 4 + quarter) * 512, *take = staging + (turn * 4 + (quarter ^ 2)) * 512;
+            turn ^= 1;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                give[j * 32 + lane] = up ? v[j] : v[16 + j];
+            named_barrier_sync(1 + (quarter & 1), 64);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float other = take[j * 32 + lane];
+                const float g = up ? other : v[j], u = up ? v[16 + j] : other;
+                const int column = c + (up ? 16 : 0) + j;
+                if (column < t.rows && f < p.out_width)
+                    store16<BF16>(p.out, (t.row + column) * p.out_stride + f, act<ACT>(g) * u);
+            }
+        } else {
+            const int f = t.m0 + rank * kSide + 32 * quarter + lane;
+            const int64_t at = (t.row + c) * p.out_stride + f;
+            const int left = f < p.out_width ? t.rows - c : 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < left)
+                    store16<BF16>(p.out, at + j * p.out_stride, v[j]);
+        }
+    }
+}
+
+template <int KIND, bool BF16, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p)
+{
+    constexpr bool kAcrossA = KIND == kInput || KIND == kWeight, kAcrossB = KIND == kWeight;
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t *smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+    const uint32_t base = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_rank());
+    int32_t *first = reinterpret_cast<int32_t *>(smem + Layout::first), *tile0 = first + p.E + 1;
+    const uint32_t full = base + Layout::full, empty = base + Layout::empty, tail = base + Layout::tail,
+                   sums_full = base + Layout::sums_full, sums_empty = base + Layout::sums_empty, done = base + Layout::done;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + 8 * s, 2);   // both CTAs' copies (or the clearing of their last rows)
+            mbar_init(empty + 8 * s, 1);
+            mbar_init(tail + 8 * s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sums_full + 8 * i, 1);
+            mbar_init(sums_empty + 8 * i, 8);  // the writing warps of both CTAs
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+        prefetch_map(&p.a);
+        prefetch_map(&p.b);
+    }
+    if (warp == 2)
+        tmem_alloc_pair(base + Layout::tmem, 512);
     grid_dependency_wait();
-    const int tid = threadIdx.x, e = blockIdx.z;
-    if (tid == 0) {
-        if (!bounds_of(p, e, range[0], range[1]) && p.status)
+    if (warp == 0) {
+        if (!read_offsets<KIND != kWeight>(p, first, tile0, lane) && lane == 0 && p.status && blockIdx.x == 0)
             atomicCAS(p.status, 0, MOE_ERR_ROW_OUT_OF_RANGE);
     }
+    tcgen05_fence_before();
     __syncthreads();
-    const int64_t first = range[0], last = range[1];
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const int64_t M = KIND == kWeight ? p.width : last - first;     // rows of the result
-    const int64_t K = KIND == kWeight ? last - first : p.width;     // the contraction
-    const int64_t N = p.out_width;
-    if (m0 >= M)
-        return;
-    const int F = KIND == kGated ? 2 : 1;
-    float acc[2][4][4] = {};
-    const int ty = tid / 16, tx = tid % 16;
-    for (int64_t k0 = 0; k0 < K; k0 += kStep) {
-        for (int i = tid; i < kStep * kTile; i += 256) {
-            const int64_t k = k0 + i % kStep, m = m0 + i / kStep;
-            float v = 0.0f;
-            if (k < K && m < M)
-                v = KIND == kWeight ? value<BF16>(p.rows, (first + k) * p.rows_stride + m)
-                                    : value<BF16>(p.rows, (first + m) * p.rows_stride + k);
-            a[i % kStep][i / kStep] = v;
-        }
-        for (int f = 0; f < F; ++f)
-            for (int i = tid; i < kStep * kTile; i += 256) {
-                const int64_t k = k0 + i % kStep, n = n0 + i / kStep;
-                float v = 0.0f;
-                if (k < K && n < N) {
-                    if (KIND == kForward || KIND == kGated)
-                        v = value<BF16>(p.other, ((static_cast<int64_t>(e) * F + f) * N + n) * K + k);
-                    else if (KIND == kInput)
-                        v = value<BF16>(p.other, (static_cast<int64_t>(e) * K + k) * N + n);
-                    else
-                        v = value<BF16>(p.other, (first + k) * p.other_stride + n);
+    cluster_arrive_rel();
+    cluster_wait_acq();
+    tcgen05_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + Layout::tmem);
+    const Schedule<KIND> plan(p, first, tile0);
+    const int64_t pair = cluster_id_x(), pairs = cluster_count_x();
+
+    if (warp == 0 && lane == 0) {
+        // copies: this CTA's 128 of the tile's 256 and half of its N
+        const uint32_t full_of_pair = cluster_map(full, 0);
+        int64_t left = pair == 0 && rank == 0 && p.stall >= 0 ? p.stall : INT64_MAX;  // test hook (moe_debug_stall)
+        uint32_t slot = 0, phase = 1, used = 0;
+        bool good = true;
+        for (int64_t q = pair; q < plan.total && good; q += pairs) {
+            const Tile t = plan.at(q);
+            const int half = t.n / 2;
+            const int boxes = kAcrossB ? (half + 63) / 64 : (half + p.box - 1) / p.box;
+            const uint32_t bytes = kOperand + static_cast<uint32_t>(boxes) * (kAcrossB ? kChunk : p.box * kLine);
+            for (int k = 0; k < t.steps; ++k) {
+                if (left-- <= 0 || !mbar_wait_bounded(empty + 8 * slot, phase, kWaitLimitNs)) {
+                    good = false;
+                    break;
                 }
-                b[f][i % kStep][i / kStep] = v;
+                const uint32_t a = base + slot * kStage, b = a + kOperand;
+                uint32_t bar = full_of_pair + 8 * slot;
+                if (KIND == kWeight && k == t.steps - 1 && t.rows % kStep != 0) {
+                    bar = tail + 8 * slot;  // warp 2 clears what lies behind the rows, and then says that the slot is full
+                    mbar_arrive_expect_tx(bar, bytes);
+                } else {
+                    mbar_arrive_expect_tx_cluster(bar, bytes);
+                }
+                const int x = k * kStep;
+                if constexpr (KIND == kForward) {
+                    tensor_load_pair(a, &p.a, x, t.m0 + rank * kSide, t.e, bar);
+                } else if constexpr (KIND == kGated) {
+                    const int f = t.m0 + rank * 64;
+                    tensor_load_pair(a, &p.a, x, f, t.e, bar);
+                    tensor_load_pair(a + kChunk, &p.a, x, p.out_width + f, t.e, bar);
+                } else {
+                    const int y = KIND == kInput ? x : static_cast<int32_t>(t.row + x);
+                    for (int c = 0; c < 2; ++c)
+                        tensor_load_pair(a + c * kChunk, &p.a, t.m0 + rank * kSide + 64 * c, y, KIND == kInput ? t.e : 0, bar);
+                }
+                if constexpr (kAcrossB) {
+                    for (int c = 0; c < boxes; ++c)
+                        tensor_load_pair(b + c * kChunk, &p.b, t.n0 + rank * half + 64 * c, static_cast<int32_t>(t.row + x), 0, bar);
+                } else {
+                    for (int c = 0; c < boxes; ++c)
+                        tensor_load_pair(b + c * p.box * kLine, &p.b, x, static_cast<int32_t>(t.row + rank * half + c * p.box), 0, bar);
+                }
+                ++used;
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
-        __syncthreads();
-        for (int k = 0; k < kStep; ++k)
-            for (int f = 0; f < F; ++f)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[f][i][j] += a[k][ty + 16 * i] * b[f][k][tx + 16 * j];
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m >= M || n >= N)
+        }
+        // the last arrivals at this CTA's barriers land before it leaves
+        for (uint32_t i = 0; good && i < (used < kStages ? used : kStages); ++i) {
+            good = mbar_wait_bounded(empty + 8 * slot, phase, kWaitLimitNs);
+            if (++slot == kStages) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        uint32_t slot = 0, phase = 0, turn = 0;
+        bool good = true;
+        for (int64_t q = pair; q < plan.total && good; q += pairs) {
+            const Tile t = plan.at(q);
+            if (t.steps == 0)
                 continue;
-            const float v = acc[0][i][j];
-            if constexpr (KIND == kWeight) {
-                const int64_t at = (static_cast<int64_t>(e) * M + m) * N + n;
-                if (p.fp32_out)
-                    static_cast<float *>(p.out)[at] = v;
-                else
-                    put<BF16>(p.out, at, v);
-            } else if constexpr (KIND == kGated) {
-                const float u = acc[1][i][j];
-                put<BF16>(p.out, (first + m) * p.out_stride + n, act<ACT>(v) * u);
-                if (p.gate_up) {
-                    put<BF16>(p.gate_up, (first + m) * p.gate_up_stride + n, v);
-                    put<BF16>(p.gate_up, (first + m) * p.gate_up_stride + N + n, u);
+            const uint32_t idesc = mma_f16_descriptor(BF16, kAcrossA, kAcrossB, 256, static_cast<uint32_t>(t.n));
+            const uint32_t sums = tmem + (turn & 1) * kMaxN;
+            good = mbar_wait_cluster_bounded(sums_empty + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1, kWaitLimitNs);
+            tcgen05_fence_after();
+            for (int k = 0; k < t.steps && good; ++k) {
+                good = mbar_wait_cluster_bounded(full + 8 * slot, phase, kWaitLimitNs);
+                if (!good)
+                    break;
+                tcgen05_fence_after();
+                const uint32_t at = base + slot * kStage;
+                const uint64_t a = kAcrossA ? operand_across(at, kChunk) : operand_along(at);
+                const uint64_t b = kAcrossB ? operand_across(at + kOperand, kChunk) : operand_along(at + kOperand);
+#pragma unroll
+                for (int j = 0; j < kStep / 16; ++j)  // 16 of the contraction: 32 bytes of a line, or 16 lines
+                    mma_pair_f16(sums, a + j * (kAcrossA ? 16 * kLine / 16 : 2), b + j * (kAcrossB ? 16 * kLine / 16 : 2), idesc, k > 0 || j > 0);
+                mma_pair_commit(empty + 8 * slot);
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
                 }
-            } else {
-                put<BF16>(p.out, (first + m) * p.out_stride + n, v);
+            }
+            if (good)
+                mma_pair_commit(sums_full + 8 * (turn & 1));
+            ++turn;
+        }
+        if (!good) {
+            // what is in flight ends before the pair leaves: matrix instructions, and copies (those of a slot that only one CTA
+            // filled never complete its barrier, and have long landed after the wait)
+            mma_pair_commit(done);
+            mbar_wait_bounded(done, 0, kWaitLimitNs);
+            const uint64_t t0 = globaltimer_ns();
+            for (int s = 0; s < kStages; ++s) {
+                while (!mbar_try_wait(full + 8 * slot, phase) && globaltimer_ns() - t0 < kWaitLimitNs / 4) {
+                }
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
         }
+    } else if (warp == 2 && KIND == kWeight) {
+        // the last step of an expert's rows: lines behind them, in both operands, become zeros (a neighbour's values
+        // times zero would not do, as they may be infinities)
+        const uint32_t full_of_pair = cluster_map(full, 0);
+        uint32_t slot = 0, phases = 0;
+        bool good = true;
+        for (int64_t q = pair; q < plan.total && good; q += pairs) {
+            const Tile t = plan.at(q);
+            if (t.steps == 0)
+                continue;
+            slot = static_cast<uint32_t>((slot + t.steps - 1) % kStages);
+            const int rest = t.rows % kStep;
+            if (rest != 0) {
+                good = mbar_wait_bounded(tail + 8 * slot, (phases >> slot) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
+                good = __all_sync(0xffffffffu, good);
+                if (!good)
+                    break;
+                phases ^= 1u << slot;
+                const int chunks = 2 + (t.n / 2 + 63) / 64;
+                for (int c = 0; c < chunks; ++c)
+                    for (int i = 8 * rest + lane; i < 8 * kStep; i += 32)
+                        *reinterpret_cast<uint4 *>(smem + slot * kStage + c * kChunk + 16 * i) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(full_of_pair + 8 * slot);
+            }
+            slot = (slot + 1) % kStages;
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp - 4;
+        const uint32_t empty_of_pair = cluster_map(sums_empty, 0);
+        float *staging = reinterpret_cast<float *>(smem + Layout::staging);
+        uint32_t turn = 0;
+        int swap = 0;
+        bool lost = false;
+        for (int64_t q = pair; q < plan.total; q += pairs) {
+            const Tile t = plan.at(q);
+            const uint32_t i = turn & 1;
+            if (t.steps > 0 && !lost) {
+                // a long contraction takes longer than the limit alone
+                lost = !mbar_wait_cluster_bounded(sums_full + 8 * i, (turn >> 1) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
+                lost = __any_sync(0xffffffffu, lost);
+                tcgen05_fence_after();
+            }
+            write_tile<KIND, BF16, ACT>(p, t, tmem + i * kMaxN, quarter, lane, rank, staging, swap, lost);
+            if (t.steps > 0) {
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0 && !lost)
+                    mbar_arrive_cluster(empty_of_pair + 8 * i);
+                ++turn;
+            }
+        }
+        if (lost && lane == 0 && p.status)
+            atomicCAS(p.status, 0, MOE_ERR_DEVICE_TIMEOUT);
+    }
+    __syncwarp();
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_arrive_rel();
+    cluster_wait_acq();
+    tcgen05_fence_after();
+    if (warp == 2)
+        tmem_free_pair(tmem, 512);
+    allow_dependent_launch();
 }
 
+// -------------------------------------------------------------------------------------------------- launch
+
 template <int KIND, bool BF16, int ACT>
-moe_status launch(const Product &p, moe_stream_t stream)
+moe_status launch(const Product &a, moe_stream_t stream)
 {
-    const int64_t M = KIND == kWeight ? p.width : p.n_rows;
-    const dim3 grid(static_cast<unsigned>((p.out_width + kTile - 1) / kTile), static_cast<unsigned>((M + kTile - 1) / kTile),
-                    static_cast<unsigned>(p.E));
-    if (grid.y > 65535)
-        return MOE_ERR_UNSUPPORTED;
-    PdlLaunch l(1, 256, 0, stream);
-    l.cfg.gridDim = grid;
-    return l.run(product_kernel<KIND, BF16, ACT>, Params{p});
+    static SmemLimit limit;
+    const auto kern = product_kernel<KIND, BF16, ACT>;
+    const int sms = sm_count();
+    int dev = 0;
+    Params p{};
+    p.n_rows = a.n_rows;
+    p.E = a.E;
+    p.width = a.width;
+    p.out_width = a.out_width;
+    p.contraction = KIND == kWeight ? 0 : a.width;
+    p.offsets = a.offsets;
+    p.out = static_cast<uint8_t *>(a.out);
+    p.out_stride = a.out_stride;
+    p.gate_up = static_cast<uint8_t *>(a.gate_up);
+    p.gate_up_stride = a.gate_up_stride;
+    p.status = a.status;
+    p.fp32_out = a.fp32_out;
+    p.stall = a.stall;
+    // boxes of 32 rows: few copies for a full tile, and little beyond the rows of a small one
+    p.box = a.n_rows / a.E < 16 ? 8 : 32;
+    int64_t tiles;
+    if (KIND == kWeight) {
+        p.n_columns = a.out_width > 128 ? 256 : (a.out_width > 64 ? 128 : 64);
+        p.m_tiles = (a.width + 255) / 256;
+        p.n_tiles = (a.out_width + p.n_columns - 1) / p.n_columns;
+        tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
+    } else {
+        p.m_tiles = KIND == kGated ? (a.out_width + 127) / 128 : (a.out_width + 255) / 256;
+        tiles = (a.n_rows / kMaxN + (a.n_rows < a.E ? a.n_rows : a.E)) * p.m_tiles;
+    }
+    bool ok;
+    if (KIND == kForward || KIND == kGated)
+        ok = encode_rows(p.a, a.other, a.width, KIND == kGated ? 2 * a.out_width : a.out_width, a.E, a.width, 64, KIND == kGated ? 64 : 128);
+    else if (KIND == kInput)
+        ok = encode_rows(p.a, a.other, a.out_width, a.width, a.E, a.out_width, 64, 64);
+    else
+        ok = encode_rows(p.a, a.rows, a.width, a.n_rows, 1, a.rows_stride, 64, 64);
+    if (KIND == kWeight)
+        ok = ok && encode_rows(p.b, a.other, a.out_width, a.n_rows, 1, a.other_stride, 64, 64);
+    else
+        ok = ok && encode_rows(p.b, a.rows, a.width, a.n_rows, 1, a.rows_stride, 64, p.box);
+    const size_t smem = static_cast<size_t>(Layout::bytes(a.E));
+    if (!ok || sms < 2 || cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limit) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < 1 ? 1 : pairs)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess)
+        return MOE_OK;
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
 }
 
 template <bool BF16>

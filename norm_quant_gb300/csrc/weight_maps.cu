@@ -1,11 +1,12 @@
 // weight_maps.cu -- the tensor maps through which the few-token products copy
-// their weights to shared memory.
+// their weights to shared memory, and those of the products of grouped rows.
 #include <cstdint>
 #include <mutex>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "skinny.cuh"
+#include "tensor_map.h"
 
 namespace nqg {
 namespace {
@@ -85,6 +86,20 @@ moe_status make_column_map(CUtensorMap &map, const void *at, int row_bytes, int 
     const bool ok = row_bytes % kStripBytes == 0 ? encode(map, at, 3, size3, stride3, boxes, CU_TENSOR_MAP_SWIZZLE_128B)
                                                  : encode(map, at, 2, size2, stride3, boxes, CU_TENSOR_MAP_SWIZZLE_128B);
     return ok ? MOE_OK : MOE_ERR_CUDA;
+}
+
+bool encode_rows(CUtensorMap &map, const void *at, int32_t width, int64_t rows, int32_t groups, int64_t stride, int32_t box_width,
+                 int32_t box_rows)
+{
+    if (!encoder())
+        return false;
+    const cuuint64_t pitch = 2 * static_cast<cuuint64_t>(stride), n = static_cast<cuuint64_t>(rows);
+    const cuuint64_t size[3] = {static_cast<cuuint64_t>(width), n, static_cast<cuuint64_t>(groups)};
+    const cuuint64_t strides[2] = {pitch, groups > 1 ? n * pitch : pitch};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_width), static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
+    return encoder()(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(at), size, strides, box, step,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 } // namespace nqg

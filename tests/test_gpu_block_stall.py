@@ -1,0 +1,67 @@
+"""Waits that run out in the block's products: the first CTA's copies stop after
+a few slots.  The call ends within a few seconds, the status says why, results
+of the first pair from that tile on are NaN, everything else is as it was, and the
+context stays usable."""
+import time
+
+import pytest
+import torch
+
+import norm_quant_gb300 as nqg
+from norm_quant_gb300.build import build
+
+from test_gpu_block import DEV, dev_offsets, gen, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build()
+    nqg.lib()
+
+
+def stalled(slots, call):
+    t0 = time.monotonic()
+    try:
+        nqg.moe_debug_stall(slots)
+        call()
+        torch.cuda.synchronize()
+    finally:
+        nqg.moe_debug_stall(-1)
+    assert time.monotonic() - t0 < 30
+
+
+@pytest.mark.parametrize("slots", [0, 3, 12])  # in the first tile or the second, or a later one
+@pytest.mark.parametrize("what", ["linear", "gated", "input", "weight"])
+def test_copies_that_stop(what, slots):
+    bounds, rows, K, N = [0, 100, 900, 1000], 1000, 520, 8192
+    g = gen(slots)
+    x, w, dy = normal(g, rows, K).to(DEV), normal(g, 3, N, K, std=K ** -0.5).to(DEV), normal(g, rows, N).to(DEV)
+    off, status = dev_offsets(bounds), torch.zeros(1, dtype=torch.int32, device=DEV)
+    shape = {"linear": (rows, N), "gated": (rows, N // 2), "input": (rows, K), "weight": (3, N, K)}[what]
+    out = torch.empty(shape, dtype=torch.bfloat16, device=DEV)
+
+    def call():
+        kw = dict(offsets=off, status=status)
+        if what == "linear":
+            nqg.moe_grouped_linear(x, w, out, **kw)
+        elif what == "gated":
+            nqg.moe_gated_linear(x, w, out, **kw)
+        elif what == "input":
+            nqg.moe_grouped_linear_backward(dy, w=w, d_x=out, **kw)
+        else:
+            nqg.moe_grouped_linear_backward(dy, x=x, d_w=out, **kw)
+
+    call()
+    good = out.clone()
+    assert bool(good.isfinite().all()) and int(status) == 0
+    stalled(slots, call)
+    assert int(status) == nqg.MOE_ERR_DEVICE_TIMEOUT
+    late = out.isnan()
+    # the first pair has the first tile of each round of tiles
+    assert 0 < float(late.double().mean()) <= 0.5
+    assert torch.equal(out[~late], good[~late])
+    status.zero_()
+    call()
+    assert torch.equal(out, good) and int(status) == 0
