@@ -41,15 +41,16 @@ constexpr int kOperand = kSide * kLine;
 constexpr int kStage = 2 * kOperand;
 constexpr int kChunk = 64 * kLine;          // 64 rows of an operand across
 constexpr int kMaxN = 256;
+constexpr int kRowBoxes = 4;
 constexpr int kBlock = 8;                   // tiles of one side that pass along the other together
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Params {
-    CUtensorMap a, b;
+    CUtensorMap a, b[kRowBoxes];  // b: of rows in boxes of 16, 32, 64 and 128; the weights' gradient has one
     int64_t n_rows;
     int32_t E, width, out_width, contraction;  // contraction: 0 for the weights' gradient (an expert's rows)
     int32_t m_tiles, n_tiles, n_columns;       // n_*: the weights' gradient's N side
-    int32_t box;                               // rows of a box of the rows' map
+    int32_t wide_a, wide_b;                    // an operand across comes in boxes of 128 columns (two chunks), not 64
     const int32_t *offsets;
     uint8_t *out, *gate_up;
     int64_t out_stride, gate_up_stride;        // elements
@@ -287,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         mbar_init(done, 1);
         fence_mbar_init();
         prefetch_map(&p.a);
-        prefetch_map(&p.b);
+        for (int i = 0; i < (kAcrossB ? 1 : kRowBoxes); ++i)
+            prefetch_map(&p.b[i]);
     }
     if (warp == 2)
         tmem_alloc_pair(base + Layout::tmem, 512);
@@ -314,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         for (int64_t q = pair; q < plan.total && good; q += pairs) {
             const Tile t = plan.at(q);
             const int half = t.n / 2;
-            const int boxes = kAcrossB ? (half + 63) / 64 : (half + p.box - 1) / p.box;
-            const uint32_t bytes = kOperand + static_cast<uint32_t>(boxes) * (kAcrossB ? kChunk : p.box * kLine);
+            const int chunks = (half + 63) / 64;
+            const uint32_t bytes = kOperand + static_cast<uint32_t>(kAcrossB ? (p.wide_b ? 2 * kChunk : chunks * kChunk) : half * kLine);
             for (int k = 0; k < t.steps; ++k) {
                 if (left-- <= 0 || !mbar_wait_bounded(empty + 8 * slot, phase, kWaitLimitNs)) {
                     good = false;
@@ -330,23 +332,37 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     mbar_arrive_expect_tx_cluster(bar, bytes);
                 }
                 const int x = k * kStep;
+                const int32_t row = static_cast<int32_t>(t.row) + (KIND == kWeight ? x : rank * half);
                 if constexpr (KIND == kForward) {
                     tensor_load_pair(a, &p.a, x, t.m0 + rank * kSide, t.e, bar);
                 } else if constexpr (KIND == kGated) {
-                    const int f = t.m0 + rank * 64;
-                    tensor_load_pair(a, &p.a, x, f, t.e, bar);
-                    tensor_load_pair(a + kChunk, &p.a, x, p.out_width + f, t.e, bar);
+                    tensor_load_pair(a, &p.a, x, t.m0 + rank * 64, 0, t.e, bar);  // 64 rows of W1 and the same of W3
                 } else {
-                    const int y = KIND == kInput ? x : static_cast<int32_t>(t.row + x);
-                    for (int c = 0; c < 2; ++c)
-                        tensor_load_pair(a + c * kChunk, &p.a, t.m0 + rank * kSide + 64 * c, y, KIND == kInput ? t.e : 0, bar);
+                    const int y = KIND == kInput ? x : row, e = KIND == kInput ? t.e : 0, column = t.m0 + rank * kSide;
+                    if (p.wide_a) {
+                        tensor_load_pair(a, &p.a, 0, y, column / 64, e, bar);
+                    } else {
+                        tensor_load_pair(a, &p.a, column, y, 0, e, bar);
+                        tensor_load_pair(a + kChunk, &p.a, column + 64, y, 0, e, bar);
+                    }
                 }
                 if constexpr (kAcrossB) {
-                    for (int c = 0; c < boxes; ++c)
-                        tensor_load_pair(b + c * kChunk, &p.b, t.n0 + rank * half + 64 * c, static_cast<int32_t>(t.row + x), 0, bar);
+                    const int column = t.n0 + rank * half;
+                    if (p.wide_b) {
+                        tensor_load_pair(b, &p.b[0], 0, row, column / 64, 0, bar);
+                    } else {
+                        for (int c = 0; c < chunks; ++c)
+                            tensor_load_pair(b + c * kChunk, &p.b[0], column + 64 * c, row, 0, 0, bar);
+                    }
                 } else {
-                    for (int c = 0; c < boxes; ++c)
-                        tensor_load_pair(b + c * p.box * kLine, &p.b, x, static_cast<int32_t>(t.row + rank * half + c * p.box), 0, bar);
+                    // half is a multiple of 16: one box for each of its bits
+                    int at = 0;
+#pragma unroll
+                    for (int i = kRowBoxes - 1; i >= 0; --i)
+                        if (half & (16 << i)) {
+                            tensor_load_pair(b + at * kLine, &p.b[i], x, row + at, 0, bar);
+                            at += 16 << i;
+                        }
                 }
                 ++used;
                 if (++slot == kStages) {
@@ -372,10 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 continue;
             const uint32_t idesc = mma_f16_descriptor(BF16, kAcrossA, kAcrossB, 256, static_cast<uint32_t>(t.n));
             const uint32_t sums = tmem + (turn & 1) * kMaxN;
-            good = mbar_wait_cluster_bounded(sums_empty + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1, kWaitLimitNs);
+            good = mbar_wait_bounded(sums_empty + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1, kWaitLimitNs);
             tcgen05_fence_after();
             for (int k = 0; k < t.steps && good; ++k) {
-                good = mbar_wait_cluster_bounded(full + 8 * slot, phase, kWaitLimitNs);
+                // an acquire for the pair, which costs the most of a microsecond, is for the lines that warp 2 has cleared alone
+                good = KIND == kWeight && k == t.steps - 1 && t.rows % kStep != 0 ? mbar_wait_cluster_bounded(full + 8 * slot, phase, kWaitLimitNs)
+                                                                                 : mbar_wait_bounded(full + 8 * slot, phase, kWaitLimitNs);
                 if (!good)
                     break;
                 tcgen05_fence_after();
@@ -435,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(full_of_pair + 8 * slot);
+                    mbar_arrive_release_cluster(full_of_pair + 8 * slot);
             }
             slot = (slot + 1) % kStages;
         }
@@ -451,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint32_t i = turn & 1;
             if (t.steps > 0 && !lost) {
                 // a long contraction takes longer than the limit alone
-                lost = !mbar_wait_cluster_bounded(sums_full + 8 * i, (turn >> 1) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
+                lost = !mbar_wait_bounded(sums_full + 8 * i, (turn >> 1) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
                 lost = __any_sync(0xffffffffu, lost);
                 tcgen05_fence_after();
             }
@@ -501,8 +519,6 @@ moe_status launch(const Product &a, moe_stream_t stream)
     p.status = a.status;
     p.fp32_out = a.fp32_out;
     p.stall = a.stall;
-    // boxes of 32 rows: few copies for a full tile, and little beyond the rows of a small one
-    p.box = a.n_rows / a.E < 16 ? 8 : 32;
     int64_t tiles;
     if (KIND == kWeight) {
         p.n_columns = a.out_width > 128 ? 256 : (a.out_width > 64 ? 128 : 64);
@@ -513,17 +529,28 @@ moe_status launch(const Product &a, moe_stream_t stream)
         p.m_tiles = KIND == kGated ? (a.out_width + 127) / 128 : (a.out_width + 255) / 256;
         tiles = (a.n_rows / kMaxN + (a.n_rows < a.E ? a.n_rows : a.E)) * p.m_tiles;
     }
-    bool ok;
-    if (KIND == kForward || KIND == kGated)
-        ok = encode_rows(p.a, a.other, a.width, KIND == kGated ? 2 * a.out_width : a.out_width, a.E, a.width, 64, KIND == kGated ? 64 : 128);
-    else if (KIND == kInput)
-        ok = encode_rows(p.a, a.other, a.out_width, a.width, a.E, a.out_width, 64, 64);
-    else
-        ok = encode_rows(p.a, a.rows, a.width, a.n_rows, 1, a.rows_stride, 64, 64);
-    if (KIND == kWeight)
-        ok = ok && encode_rows(p.b, a.other, a.out_width, a.n_rows, 1, a.other_stride, 64, 64);
-    else
-        ok = ok && encode_rows(p.b, a.rows, a.width, a.n_rows, 1, a.rows_stride, 64, p.box);
+    const int64_t W = a.width, F = a.out_width;
+    // [rows, columns] across, of `groups` matrices: chunks of 64 columns, two in a box where the columns are whole chunks
+    const auto across = [](CUtensorMap &map, const void *at, int64_t columns, int64_t rows, int64_t groups, int64_t stride, bool wide) {
+        if (wide)
+            return encode_tensor(map, at, {4, {64, rows, columns / 64, groups}, {stride, 64, groups > 1 ? rows * stride : stride}, {64, kStep, 2, 1}});
+        return encode_tensor(map, at, {4, {columns, rows, 1, groups}, {stride, stride, groups > 1 ? rows * stride : stride}, {64, kStep, 1, 1}});
+    };
+    bool ok = true;
+    if (KIND == kForward) {
+        ok = encode_tensor(p.a, a.other, {3, {W, F, a.E}, {W, F * W}, {kStep, kSide, 1}});
+    } else if (KIND == kGated) {
+        ok = encode_tensor(p.a, a.other, {4, {W, F, 2, a.E}, {W, F * W, 2 * F * W}, {kStep, 64, 2, 1}});
+    } else if (KIND == kInput) {
+        p.wide_a = F % 64 == 0;
+        ok = across(p.a, a.other, F, W, a.E, F, p.wide_a);
+    } else {
+        p.wide_a = W % 64 == 0;
+        p.wide_b = F % 64 == 0 && p.n_columns == 256;
+        ok = across(p.a, a.rows, W, a.n_rows, 1, a.rows_stride, p.wide_a) && across(p.b[0], a.other, F, a.n_rows, 1, a.other_stride, p.wide_b);
+    }
+    for (int i = 0; KIND != kWeight && i < kRowBoxes; ++i)
+        ok = ok && encode_tensor(p.b[i], a.rows, {3, {W, a.n_rows, 1}, {a.rows_stride, a.rows_stride}, {kStep, 16 << i, 1}});
     const size_t smem = static_cast<size_t>(Layout::bytes(a.E));
     if (!ok || sms < 2 || cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limit) != cudaSuccess) {
         cudaGetLastError();

@@ -89,23 +89,38 @@ __device__ __forceinline__ uint64_t operand_across(uint32_t at, uint32_t chunk)
 
 // ----------------------------------------------------------------- the pair's barriers
 
-// Arrives at a barrier of either CTA (address from cluster_map), with or without transaction bytes to expect.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+// Arrives at a barrier of either CTA (address from cluster_map).  The first orders this thread's earlier memory
+// accesses for the whole pair, and waits for its stores; the others order nothing beyond this CTA, which is enough where
+// the data is tensor memory or a copy's (and its fences or transaction bytes say when it is there).
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// A box of a three-dimensional tensor to this CTA's shared memory, counted on a barrier of either CTA.
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// A box of a three- or four-dimensional tensor to this CTA's shared memory, counted on a barrier of either CTA.
 __device__ __forceinline__ void tensor_load_pair(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, uint32_t bar)
 {
     asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
                  "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
                  "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tensor_load_pair(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z, int32_t u, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
                  : "memory");
 }
 

@@ -6,9 +6,15 @@
 
 namespace nqg {
 
-// [groups, rows, width] of 16-bit elements, `stride` of them from row to row and rows * stride from group to group, in
-// boxes of box_rows rows x box_width elements with the 128-byte swizzle.  What lies outside reads as zeros.
-bool encode_rows(CUtensorMap &map, const void *at, int32_t width, int64_t rows, int32_t groups, int64_t stride, int32_t box_width,
-                 int32_t box_rows);
+// A tensor of 16-bit elements, the innermost dimension first, in boxes with the 128-byte swizzle.  What lies outside reads
+// as zeros.
+struct TensorShape {
+    int32_t dims;
+    int64_t size[4];
+    int64_t stride[3];  // elements from one to the next of dimensions 1 to 3
+    int32_t box[4];
+};
+
+bool encode_tensor(CUtensorMap &map, const void *at, const TensorShape &shape);
 
 } // namespace nqg

@@ -88,17 +88,21 @@ moe_status make_column_map(CUtensorMap &map, const void *at, int row_bytes, int 
     return ok ? MOE_OK : MOE_ERR_CUDA;
 }
 
-bool encode_rows(CUtensorMap &map, const void *at, int32_t width, int64_t rows, int32_t groups, int64_t stride, int32_t box_width,
-                 int32_t box_rows)
+bool encode_tensor(CUtensorMap &map, const void *at, const TensorShape &shape)
 {
     if (!encoder())
         return false;
-    const cuuint64_t pitch = 2 * static_cast<cuuint64_t>(stride), n = static_cast<cuuint64_t>(rows);
-    const cuuint64_t size[3] = {static_cast<cuuint64_t>(width), n, static_cast<cuuint64_t>(groups)};
-    const cuuint64_t strides[2] = {pitch, groups > 1 ? n * pitch : pitch};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_width), static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
-    return encoder()(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(at), size, strides, box, step,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    cuuint64_t size[4], stride[3];
+    cuuint32_t box[4], step[4];
+    for (int i = 0; i < shape.dims; ++i) {
+        size[i] = static_cast<cuuint64_t>(shape.size[i]);
+        box[i] = static_cast<cuuint32_t>(shape.box[i]);
+        step[i] = 1;
+        if (i > 0)
+            stride[i - 1] = 2 * static_cast<cuuint64_t>(shape.stride[i - 1]);
+    }
+    return encoder()(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(shape.dims), const_cast<void *>(at), size, stride, box,
+                     step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
