@@ -183,6 +183,12 @@ __device__ bool read_offsets(const Params &p, int32_t *first, int32_t *tile0, in
     return __all_sync(0xffffffffu, good);
 }
 
+// A bounded wait by a whole warp, which stays together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs));
+}
+
 template <bool BF16>
 __device__ __forceinline__ void store16(uint8_t *base, int64_t at, float v)
 {
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     extern __shared__ uint8_t raw_smem[];
     uint8_t *smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     const uint32_t base = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
     int32_t *first = reinterpret_cast<int32_t *>(smem + Layout::first), *tile0 = first + p.E + 1;
     const uint32_t full = base + Layout::full, empty = base + Layout::empty, tail = base + Layout::tail,
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const Schedule<KIND> plan(p, first, tile0);
     const int64_t pair = cluster_id_x(), pairs = cluster_count_x();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // copies: this CTA's 128 of the tile's 256 and half of its N
         const uint32_t full_of_pair = cluster_map(full, 0);
         int64_t left = pair == 0 && rank == 0 && p.stall >= 0 ? p.stall : INT64_MAX;  // test hook (moe_debug_stall)
@@ -319,14 +325,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int chunks = (half + 63) / 64;
             const uint32_t bytes = kOperand + static_cast<uint32_t>(kAcrossB ? (p.wide_b ? 2 * kChunk : chunks * kChunk) : half * kLine);
             for (int k = 0; k < t.steps; ++k) {
-                if (left-- <= 0 || !mbar_wait_bounded(empty + 8 * slot, phase, kWaitLimitNs)) {
+                if (left-- <= 0 || !warp_wait(empty + 8 * slot, phase)) {
                     good = false;
                     break;
                 }
                 const uint32_t a = base + slot * kStage, b = a + kOperand;
                 uint32_t bar = full_of_pair + 8 * slot;
+                ++used;
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                if (!elect_lane())
+                    continue;
                 if (KIND == kWeight && k == t.steps - 1 && t.rows % kStep != 0) {
-                    bar = tail + 8 * slot;  // warp 2 clears what lies behind the rows, and then says that the slot is full
+                    bar = tail + (a - base) / kStage * 8;  // warp 2 clears what lies behind the rows, and then says that the slot is full
                     mbar_arrive_expect_tx(bar, bytes);
                 } else {
                     mbar_arrive_expect_tx_cluster(bar, bytes);
@@ -364,22 +377,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                             at += 16 << i;
                         }
                 }
-                ++used;
-                if (++slot == kStages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
             }
         }
         // the last arrivals at this CTA's barriers land before it leaves
         for (uint32_t i = 0; good && i < (used < kStages ? used : kStages); ++i) {
-            good = mbar_wait_bounded(empty + 8 * slot, phase, kWaitLimitNs);
+            good = warp_wait(empty + 8 * slot, phase);
             if (++slot == kStages) {
                 slot = 0;
                 phase ^= 1;
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         uint32_t slot = 0, phase = 0, turn = 0;
         bool good = true;
         for (int64_t q = pair; q < plan.total && good; q += pairs) {
@@ -388,36 +396,43 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 continue;
             const uint32_t idesc = mma_f16_descriptor(BF16, kAcrossA, kAcrossB, 256, static_cast<uint32_t>(t.n));
             const uint32_t sums = tmem + (turn & 1) * kMaxN;
-            good = mbar_wait_bounded(sums_empty + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1, kWaitLimitNs);
+            good = warp_wait(sums_empty + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1);
             tcgen05_fence_after();
             for (int k = 0; k < t.steps && good; ++k) {
                 // an acquire for the pair, which costs the most of a microsecond, is for the lines that warp 2 has cleared alone
-                good = KIND == kWeight && k == t.steps - 1 && t.rows % kStep != 0 ? mbar_wait_cluster_bounded(full + 8 * slot, phase, kWaitLimitNs)
-                                                                                 : mbar_wait_bounded(full + 8 * slot, phase, kWaitLimitNs);
+                good = KIND == kWeight && k == t.steps - 1 && t.rows % kStep != 0
+                           ? __all_sync(0xffffffffu, mbar_wait_cluster_bounded(full + 8 * slot, phase, kWaitLimitNs))
+                           : warp_wait(full + 8 * slot, phase);
                 if (!good)
                     break;
                 tcgen05_fence_after();
                 const uint32_t at = base + slot * kStage;
                 const uint64_t a = kAcrossA ? operand_across(at, kChunk) : operand_along(at);
                 const uint64_t b = kAcrossB ? operand_across(at + kOperand, kChunk) : operand_along(at + kOperand);
+                if (elect_lane()) {
 #pragma unroll
-                for (int j = 0; j < kStep / 16; ++j)  // 16 of the contraction: 32 bytes of a line, or 16 lines
-                    mma_pair_f16(sums, a + j * (kAcrossA ? 16 * kLine / 16 : 2), b + j * (kAcrossB ? 16 * kLine / 16 : 2), idesc, k > 0 || j > 0);
-                mma_pair_commit(empty + 8 * slot);
+                    for (int j = 0; j < kStep / 16; ++j)  // 16 of the contraction: 32 bytes of a line, or 16 lines
+                        mma_pair_f16(sums, a + j * (kAcrossA ? 16 * kLine / 16 : 2), b + j * (kAcrossB ? 16 * kLine / 16 : 2), idesc, k > 0 || j > 0);
+                    mma_pair_commit(empty + 8 * slot);
+                }
+                __syncwarp();
                 if (++slot == kStages) {
                     slot = 0;
                     phase ^= 1;
                 }
             }
-            if (good)
+            if (good && elect_lane())
                 mma_pair_commit(sums_full + 8 * (turn & 1));
+            __syncwarp();
             ++turn;
         }
         if (!good) {
             // what is in flight ends before the pair leaves: matrix instructions, and copies (those of a slot that only one CTA
             // filled never complete its barrier, and have long landed after the wait)
-            mma_pair_commit(done);
-            mbar_wait_bounded(done, 0, kWaitLimitNs);
+            if (elect_lane())
+                mma_pair_commit(done);
+            __syncwarp();
+            warp_wait(done, 0);
             const uint64_t t0 = globaltimer_ns();
             for (int s = 0; s < kStages; ++s) {
                 while (!mbar_try_wait(full + 8 * slot, phase) && globaltimer_ns() - t0 < kWaitLimitNs / 4) {

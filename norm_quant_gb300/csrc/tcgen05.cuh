@@ -12,6 +12,18 @@
 
 namespace nqg {
 
+// True in one lane of a converged warp.  Copies and matrix instructions are issued under it by a warp that stays together:
+// their operands then go to uniform registers as they are.
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t yes;
+    asm volatile("{ .reg .pred p;\n"
+                 "  elect.sync _|p, 0xffffffff;\n"
+                 "  selp.u32 %0, 1, 0, p; }"
+                 : "=r"(yes));
+    return yes != 0;
+}
+
 // ---------------------------------------------------------------- tensor memory
 
 // One warp of each CTA of the pair, all lanes; the address is written to shared memory.
