@@ -42,6 +42,7 @@ constexpr int kStage = 2 * kOperand;
 constexpr int kChunk = 64 * kLine;          // 64 rows of an operand across
 constexpr int kMaxN = 256;
 constexpr int kRowBoxes = 4;
+constexpr int kPitch = 80;                  // bytes from row to row of the staging: 16 more than a row, so that eight rows meet no bank twice
 constexpr int kBlock = 8;                   // tiles of one side that pass along the other together
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -61,8 +62,9 @@ struct Params {
 
 // Shared memory, from its first 1024-byte boundary on.
 struct Layout {
-    static constexpr int staging = kStages * kStage;               // gated: what two warps hand each other, 2 x 4 x 2 KB
-    static constexpr int bars = staging + 16384;
+    static constexpr int staging = kStages * kStage;       // each writing warp's rows of results (16, or 32 where there is no exchange)
+    static constexpr int exchange = staging + 4 * 16 * kPitch;  // gated: what two warps hand each other, 2 x 4 x 2 KB
+    static constexpr int bars = exchange + 16384;
     static constexpr int full = bars, empty = full + 8 * kStages, tail = empty + 8 * kStages, sums_full = tail + 8 * kStages,
                          sums_empty = sums_full + 16, done = sums_empty + 16, tmem = done + 8, first = tmem + 8;
     static int bytes(int E) { return first + 2 * 4 * (E + 1) + 1024; }
@@ -189,82 +191,108 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs));
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store16(uint8_t *base, int64_t at, float v)
+// Rows of 32 16-bit values in a warp's staging to global memory, in pieces of 16 bytes: row r to out + r * stride for r < rows,
+// and of each the first `left` values (a multiple of 8).  Lines of 64 bytes, so whole sectors.
+template <int ROWS>
+__device__ __forceinline__ void store_rows(const uint8_t *staging, uint8_t *out, int64_t stride, int rows, int left, int lane)
 {
-    reinterpret_cast<uint16_t *>(base)[at] = static_cast<uint16_t>(pack2<BF16>(v, 0.0f));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < ROWS; i += 8) {
+        const int r = i + lane / 4, part = lane % 4;
+        if (r < rows && 8 * part < left)
+            *reinterpret_cast<uint4 *>(out + 2 * (r * stride + 8 * part)) = *reinterpret_cast<const uint4 *>(staging + r * kPitch + 16 * part);
+    }
+    __syncwarp();
 }
 
-// One tile's sums to their place: warp `quarter` (0 to 3) of the CTA of rank `rank` has lanes 32 quarter on.
+// One tile's sums to their place: warp `quarter` (0 to 3) of the CTA of rank `rank` has lanes 32 quarter on.  Sums come as
+// fragments of 8 x 8, which go through the warp's staging so that 64 bytes of a row of the result are written together.
 template <int KIND, bool BF16, int ACT>
-__device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint32_t sums, int quarter, int lane, int rank, float *staging,
-                                           int &turn, bool lost)
+__device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint32_t sums, int quarter, int lane, int rank, uint8_t *staging,
+                                           float *exchange, int &turn, bool lost)
 {
-    const float nan = __int_as_float(0x7FC00000);
     const uint32_t from = sums + (static_cast<uint32_t>(quarter) << 21);
+    const bool none = KIND == kWeight && t.steps == 0;
+    const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16;
     for (int c = 0; c < t.n; c += 32) {
-        __syncwarp();
-        uint32_t raw[32];
-        float v[32];
-        const bool none = KIND == kWeight && t.steps == 0;
+        uint32_t raw[2][16];
         if (!none && !lost) {
-            tmem_load32(from + c, raw);
+            tmem_load_fragments(from + c, raw[0]);
+            tmem_load_fragments(from + (16u << 16) + c, raw[1]);
             tmem_load_wait();
-        }
+        } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            v[j] = lost ? nan : (none ? 0.0f : __uint_as_float(raw[j]));
+            for (int j = 0; j < 16; ++j)
+                raw[0][j] = raw[1][j] = lost ? 0x7FC00000u : 0u;
+        }
+        // the sum of lane 8 i + (lane / 4), column 8 b + 2 (lane % 4) + j of the chunk
+        const auto sum = [&](int i, int b, int j) { return __uint_as_float(raw[i / 2][4 * b + 2 * (i % 2) + j]); };
+        const auto pair = [&](int i, int b) { return pack2<BF16>(sum(i, b, 0), sum(i, b, 1)); };
         if constexpr (KIND == kWeight) {
-            const int row = t.m0 + rank * kSide + 32 * quarter + lane;
+            // rows of the result are lanes
+            const int row = t.m0 + rank * kSide + 32 * quarter, left = p.out_width - t.n0 - c;
             const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
-            const int left = row < p.width ? p.out_width - t.n0 - c : 0;  // a multiple of 8
             if (p.fp32_out) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    if (j < left)
-                        *reinterpret_cast<float4 *>(p.out + 4 * (at + j)) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int r = 8 * i + lane / 4, column = 8 * b + 2 * (lane % 4);
+                        if (row + r < p.width && column < left)
+                            *reinterpret_cast<float2 *>(p.out + 4 * (at + static_cast<int64_t>(r) * p.out_width + column)) =
+                                make_float2(sum(i, b, 0), sum(i, b, 1));
+                    }
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; j += 8)
-                    if (j < left)
-                        *reinterpret_cast<uint4 *>(p.out + 2 * (at + j)) =
-                            make_uint4(pack2<BF16>(v[j], v[j + 1]), pack2<BF16>(v[j + 2], v[j + 3]), pack2<BF16>(v[j + 4], v[j + 5]),
-                                       pack2<BF16>(v[j + 6], v[j + 7]));
+                for (int i = 0; i < 4; ++i)
+                    store_fragments<false>(at_lane + 8 * i * kPitch, pair(i, 0), pair(i, 1), pair(i, 2), pair(i, 3));
+                store_rows<32>(staging, p.out + 2 * at, p.out_width, p.width - row, left, lane);
             }
         } else if constexpr (KIND == kGated) {
             // quarters 0 and 1 hold W1's sums, 2 and 3 W3's of the same features
-            const int f = t.m0 + rank * 64 + 32 * (quarter & 1) + lane;
+            const int f = t.m0 + rank * 64 + 32 * (quarter & 1);
             const bool up = quarter >= 2;
-            if (p.gate_up && f < p.out_width) {
-                const int64_t at = (t.row + c) * p.gate_up_stride + (up ? p.out_width : 0) + f;
+            if (p.gate_up) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (c + j < t.rows)
-                        store16<BF16>(p.gate_up, at + j * p.gate_up_stride, v[j]);
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        store_fragments<true>(at_lane + 8 * b * kPitch, pair(0, 2 * h + b), pair(1, 2 * h + b), pair(2, 2 * h + b), pair(3, 2 * h + b));
+                    const int column = c + 16 * h;
+                    store_rows<16>(staging, p.gate_up + 2 * ((t.row + column) * p.gate_up_stride + (up ? p.out_width : 0) + f), p.gate_up_stride,
+                                   t.rows - column, p.out_width - f, lane);
+                }
             }
             // the gate's warp takes the chunk's first 16 columns, the other the last
-            float *give = staging + (turn * 4 + quarter) * 512, *take = staging + (turn * 4 + (quarter ^ 2)) * 512;
+            float *give = exchange + (turn * 4 + quarter) * 512 + lane, *take = exchange + (turn * 4 + (quarter ^ 2)) * 512 + lane;
             turn ^= 1;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                give[j * 32 + lane] = up ? v[j] : v[16 + j];
+            for (int j = 0; j < 16; ++j) {
+                const int i = j / 4, b = j / 2 % 2;
+                give[32 * j] = up ? sum(i, b, j % 2) : sum(i, 2 + b, j % 2);
+            }
             named_barrier_sync(1 + (quarter & 1), 64);
+            float h[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float other = take[j * 32 + lane];
-                const float g = up ? other : v[j], u = up ? v[16 + j] : other;
-                const int column = c + (up ? 16 : 0) + j;
-                if (column < t.rows && f < p.out_width)
-                    store16<BF16>(p.out, (t.row + column) * p.out_stride + f, act<ACT>(g) * u);
+                const int i = j / 4, b = j / 2 % 2;
+                const float other = take[32 * j];
+                const float g = up ? other : sum(i, b, j % 2), u = up ? sum(i, 2 + b, j % 2) : other;
+                h[j] = act<ACT>(g) * u;
             }
-        } else {
-            const int f = t.m0 + rank * kSide + 32 * quarter + lane;
-            const int64_t at = (t.row + c) * p.out_stride + f;
-            const int left = f < p.out_width ? t.rows - c : 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < left)
-                    store16<BF16>(p.out, at + j * p.out_stride, v[j]);
+            for (int b = 0; b < 2; ++b)
+                store_fragments<true>(at_lane + 8 * b * kPitch, pack2<BF16>(h[2 * b], h[2 * b + 1]), pack2<BF16>(h[4 + 2 * b], h[5 + 2 * b]),
+                                      pack2<BF16>(h[8 + 2 * b], h[9 + 2 * b]), pack2<BF16>(h[12 + 2 * b], h[13 + 2 * b]));
+            const int column = c + (up ? 16 : 0);
+            store_rows<16>(staging, p.out + 2 * ((t.row + column) * p.out_stride + f), p.out_stride, t.rows - column, p.out_width - f, lane);
+        } else {
+            const int f = t.m0 + rank * kSide + 32 * quarter;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                store_fragments<true>(at_lane + 8 * b * kPitch, pair(0, b), pair(1, b), pair(2, b), pair(3, b));
+            store_rows<32>(staging, p.out + 2 * ((t.row + c) * p.out_stride + f), p.out_stride, t.rows - c, p.out_width - f, lane);
         }
     }
 }
@@ -475,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp >= 4) {
         const int quarter = warp - 4;
         const uint32_t empty_of_pair = cluster_map(sums_empty, 0);
-        float *staging = reinterpret_cast<float *>(smem + Layout::staging);
+        uint8_t *staging = smem + Layout::staging + quarter * (KIND == kGated ? 16 : 32) * kPitch;
+        float *exchange = reinterpret_cast<float *>(smem + Layout::exchange);
         uint32_t turn = 0;
         int swap = 0;
         bool lost = false;
@@ -488,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 lost = __any_sync(0xffffffffu, lost);
                 tcgen05_fence_after();
             }
-            write_tile<KIND, BF16, ACT>(p, t, tmem + i * kMaxN, quarter, lane, rank, staging, swap, lost);
+            write_tile<KIND, BF16, ACT>(p, t, tmem + i * kMaxN, quarter, lane, rank, staging, exchange, swap, lost);
             if (t.steps > 0) {
                 tcgen05_fence_before();
                 __syncwarp();
