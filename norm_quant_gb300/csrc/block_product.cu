@@ -16,7 +16,7 @@
 // 256, six such stages), which is what the matrix instruction of a pair wants: 64 bytes a cycle and SM instead of the 96 that a
 // 128 x 256 tile alone would take from L2.  Sums are in tensor memory, in two buffers of 256 columns, so that one
 // tile is written out while the next is multiplied.  Warps: 0 copies (TMA), 1 issues matrix instructions (in the
-// pair's first CTA, for both), 2 clears what a weight gradient's last step reads beyond its expert's rows, 4 to 7 write results.
+// pair's first CTA, for both), 2 clears what a weight gradient's last step reads beyond its expert's rows, 4 to 11 write results.
 //
 // CTAs stay (one pair for two SMs) and take every P-th tile.  Within an expert, blocks of 8 tiles of one side pass along
 // the other, so that the pairs at work share their operands in L2.
@@ -32,7 +32,8 @@
 namespace nqg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWriters = 8;                 // writing warps: two for each 32 lanes of tensor memory, which take chunks of 32 columns in turns
+constexpr int kThreads = 128 + 32 * kWriters;
 constexpr int kStages = 6;
 constexpr int kStep = 64;                   // elements of the contraction a stage holds: a line of 128 bytes
 constexpr int kLine = 2 * kStep;
@@ -60,15 +61,17 @@ struct Params {
     int64_t stall;
 };
 
-// Shared memory, from its first 1024-byte boundary on.
+// Shared memory.
 struct Layout {
-    static constexpr int staging = kStages * kStage;       // each writing warp's rows of results (16, or 32 where there is no exchange)
-    static constexpr int exchange = staging + 4 * 16 * kPitch;  // gated: what two warps hand each other, 2 x 4 x 2 KB
-    static constexpr int bars = exchange + 16384;
+    static constexpr int staging = kStages * kStage;  // each writing warp's rows of results: 32, or 16 where two warps exchange sums
+    static constexpr int exchange = staging + kWriters * 16 * kPitch;  // gated: 2 KB for each of them
+    static constexpr int bars = exchange + kWriters * 2048;
     static constexpr int full = bars, empty = full + 8 * kStages, tail = empty + 8 * kStages, sums_full = tail + 8 * kStages,
                          sums_empty = sums_full + 16, done = sums_empty + 16, tmem = done + 8, first = tmem + 8;
-    static int bytes(int E) { return first + 2 * 4 * (E + 1) + 1024; }
+    static int bytes(int E) { return first + 2 * 4 * (E + 1); }
 };
+static_assert(kWriters * 2048 >= kWriters * 16 * kPitch, "32 rows of staging reach into the room of the exchange");
+static_assert(Layout::first + 2 * 4 * (MOE_LAYER_MAX_EXPERTS + 1) <= 232448, "shared memory of a CTA");
 
 struct Tile {
     int e;
@@ -83,25 +86,25 @@ template <int KIND>
 struct Schedule {
     const Params &p;
     const int32_t *first, *tile0;  // rows and (not for the weights' gradient) tiles of rows before each expert
-    int64_t total;
+    uint32_t total;  // below 2^31
 
     __device__ Schedule(const Params &q, const int32_t *f, const int32_t *t) : p(q), first(f), tile0(t)
     {
-        total = KIND == kWeight ? static_cast<int64_t>(p.E) * p.m_tiles * p.n_tiles : static_cast<int64_t>(tile0[p.E]) * p.m_tiles;
+        total = static_cast<uint32_t>(KIND == kWeight ? p.E * p.n_tiles : tile0[p.E]) * p.m_tiles;
     }
 
-    __device__ Tile at(int64_t q) const
+    __device__ Tile at(uint32_t q) const
     {
         Tile t;
-        int64_t within;
-        int along;  // tiles of the side that passes in blocks
+        const uint32_t m_tiles = static_cast<uint32_t>(p.m_tiles);
+        uint32_t within, along;  // along: tiles of the side that passes in blocks
         if constexpr (KIND == kWeight) {
-            const int64_t each = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+            const uint32_t each = m_tiles * p.n_tiles;
             t.e = static_cast<int>(q / each);
             within = q - t.e * each;
-            along = p.n_tiles;
+            along = static_cast<uint32_t>(p.n_tiles);
         } else {
-            const int32_t x = static_cast<int32_t>(q / p.m_tiles);
+            const int32_t x = static_cast<int32_t>(q / m_tiles);
             int lo = 0, hi = p.E;  // the last expert whose first tile is not behind x
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
@@ -111,24 +114,22 @@ struct Schedule {
                     hi = mid;
             }
             t.e = lo;
-            within = q - static_cast<int64_t>(tile0[lo]) * p.m_tiles;
-            along = tile0[lo + 1] - tile0[lo];
+            within = q - static_cast<uint32_t>(tile0[lo]) * m_tiles;
+            along = static_cast<uint32_t>(tile0[lo + 1] - tile0[lo]);
         }
-        const int64_t block = within / (static_cast<int64_t>(kBlock) * p.m_tiles);
-        const int left = along - static_cast<int>(block) * kBlock, g = left < kBlock ? left : kBlock;
-        const int r = static_cast<int>(within - block * kBlock * p.m_tiles), m = r / g;
-        const int64_t i = block * kBlock + (r - m * g);
-        t.m0 = m * (KIND == kGated ? 128 : 256);
+        const uint32_t block = within / (kBlock * m_tiles), left = along - block * kBlock, g = left < kBlock ? left : kBlock;
+        const uint32_t r = within - block * kBlock * m_tiles, m = r / g, i = block * kBlock + (r - m * g);
+        t.m0 = static_cast<int32_t>(m) * (KIND == kGated ? 128 : 256);
         const int32_t begin = first[t.e], n = first[t.e + 1] - begin;
         if constexpr (KIND == kWeight) {
             t.row = begin;
             t.rows = n;
             t.n = p.n_columns;
-            t.n0 = static_cast<int>(i) * p.n_columns;
+            t.n0 = static_cast<int32_t>(i) * p.n_columns;
             t.steps = (n + kStep - 1) / kStep;
         } else {
-            t.n = ((n + along - 1) / along + 31) / 32 * 32;
-            t.row = begin + i * t.n;
+            t.n = static_cast<int32_t>((static_cast<uint32_t>(n) + along - 1) / along + 31) / 32 * 32;
+            t.row = begin + static_cast<int64_t>(i) * t.n;
             const int64_t rest = begin + n - t.row;
             t.rows = static_cast<int32_t>(rest < t.n ? rest : t.n);
             t.n0 = 0;
@@ -206,16 +207,16 @@ __device__ __forceinline__ void store_rows(const uint8_t *staging, uint8_t *out,
     __syncwarp();
 }
 
-// One tile's sums to their place: warp `quarter` (0 to 3) of the CTA of rank `rank` has lanes 32 quarter on.  Sums come as
+// One tile's sums to their place: warps `quarter` (0 to 3) of the CTA of rank `rank` have lanes 32 quarter on, and take turns.  Sums come as
 // fragments of 8 x 8, which go through the warp's staging so that 64 bytes of a row of the result are written together.
 template <int KIND, bool BF16, int ACT>
-__device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint32_t sums, int quarter, int lane, int rank, uint8_t *staging,
-                                           float *exchange, int &turn, bool lost)
+__device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint32_t sums, int quarter, int part, int lane, int rank,
+                                           uint8_t *staging, float *exchange, bool lost)
 {
     const uint32_t from = sums + (static_cast<uint32_t>(quarter) << 21);
     const bool none = KIND == kWeight && t.steps == 0;
     const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16;
-    for (int c = 0; c < t.n; c += 32) {
+    for (int c = 32 * part; c < t.n; c += 64) {
         uint32_t raw[2][16];
         if (!none && !lost) {
             tmem_load_fragments(from + c, raw[0]);
@@ -265,14 +266,14 @@ __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint3
                 }
             }
             // the gate's warp takes the chunk's first 16 columns, the other the last
-            float *give = exchange + (turn * 4 + quarter) * 512 + lane, *take = exchange + (turn * 4 + (quarter ^ 2)) * 512 + lane;
-            turn ^= 1;
+            float *give = exchange + (4 * part + quarter) * 512 + lane, *take = exchange + (4 * part + (quarter ^ 2)) * 512 + lane;
+            const uint32_t both = 1 + 2 * part + (quarter & 1);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const int i = j / 4, b = j / 2 % 2;
                 give[32 * j] = up ? sum(i, b, j % 2) : sum(i, 2 + b, j % 2);
             }
-            named_barrier_sync(1 + (quarter & 1), 64);
+            named_barrier_sync(both, 64);
             float h[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -281,6 +282,7 @@ __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint3
                 const float g = up ? other : sum(i, b, j % 2), u = up ? sum(i, 2 + b, j % 2) : other;
                 h[j] = act<ACT>(g) * u;
             }
+            named_barrier_sync(both, 64);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 store_fragments<true>(at_lane + 8 * b * kPitch, pack2<BF16>(h[2 * b], h[2 * b + 1]), pack2<BF16>(h[4 + 2 * b], h[5 + 2 * b]),
@@ -301,8 +303,7 @@ template <int KIND, bool BF16, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p)
 {
     constexpr bool kAcrossA = KIND == kInput || KIND == kWeight, kAcrossB = KIND == kWeight;
-    extern __shared__ uint8_t raw_smem[];
-    uint8_t *smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sums_full + 8 * i, 1);
-            mbar_init(sums_empty + 8 * i, 8);  // the writing warps of both CTAs
+            mbar_init(sums_empty + 8 * i, 2 * kWriters);  // the writing warps of both CTAs
         }
         mbar_init(done, 1);
         fence_mbar_init();
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     tcgen05_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + Layout::tmem);
     const Schedule<KIND> plan(p, first, tile0);
-    const int64_t pair = cluster_id_x(), pairs = cluster_count_x();
+    const uint32_t pair = cluster_id_x(), pairs = cluster_count_x();
 
     if (warp == 0) {
         // copies: this CTA's 128 of the tile's 256 and half of its N
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         int64_t left = pair == 0 && rank == 0 && p.stall >= 0 ? p.stall : INT64_MAX;  // test hook (moe_debug_stall)
         uint32_t slot = 0, phase = 1, used = 0;
         bool good = true;
-        for (int64_t q = pair; q < plan.total && good; q += pairs) {
+        for (uint32_t q = pair; q < plan.total && good; q += pairs) {
             const Tile t = plan.at(q);
             const int half = t.n / 2;
             const int chunks = (half + 63) / 64;
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp == 1 && rank == 0) {
         uint32_t slot = 0, phase = 0, turn = 0;
         bool good = true;
-        for (int64_t q = pair; q < plan.total && good; q += pairs) {
+        for (uint32_t q = pair; q < plan.total && good; q += pairs) {
             const Tile t = plan.at(q);
             if (t.steps == 0)
                 continue;
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint32_t full_of_pair = cluster_map(full, 0);
         uint32_t slot = 0, phases = 0;
         bool good = true;
-        for (int64_t q = pair; q < plan.total && good; q += pairs) {
+        for (uint32_t q = pair; q < plan.total && good; q += pairs) {
             const Tile t = plan.at(q);
             if (t.steps == 0)
                 continue;
@@ -501,14 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             slot = (slot + 1) % kStages;
         }
     } else if (warp >= 4) {
-        const int quarter = warp - 4;
+        const int quarter = warp & 3, part = warp / 4 - 1;
         const uint32_t empty_of_pair = cluster_map(sums_empty, 0);
-        uint8_t *staging = smem + Layout::staging + quarter * (KIND == kGated ? 16 : 32) * kPitch;
+        uint8_t *staging = smem + Layout::staging + (warp - 4) * (KIND == kGated ? 16 : 32) * kPitch;
         float *exchange = reinterpret_cast<float *>(smem + Layout::exchange);
         uint32_t turn = 0;
-        int swap = 0;
         bool lost = false;
-        for (int64_t q = pair; q < plan.total; q += pairs) {
+        for (uint32_t q = pair; q < plan.total; q += pairs) {
             const Tile t = plan.at(q);
             const uint32_t i = turn & 1;
             if (t.steps > 0 && !lost) {
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 lost = __any_sync(0xffffffffu, lost);
                 tcgen05_fence_after();
             }
-            write_tile<KIND, BF16, ACT>(p, t, tmem + i * kMaxN, quarter, lane, rank, staging, exchange, swap, lost);
+            write_tile<KIND, BF16, ACT>(p, t, tmem + i * kMaxN, quarter, part, lane, rank, staging, exchange, lost);
             if (t.steps > 0) {
                 tcgen05_fence_before();
                 __syncwarp();
@@ -580,6 +580,8 @@ moe_status launch(const Product &a, moe_stream_t stream)
             return encode_tensor(map, at, {4, {64, rows, columns / 64, groups}, {stride, 64, groups > 1 ? rows * stride : stride}, {64, kStep, 2, 1}});
         return encode_tensor(map, at, {4, {columns, rows, 1, groups}, {stride, stride, groups > 1 ? rows * stride : stride}, {64, kStep, 1, 1}});
     };
+    if (tiles >= int64_t{1} << 31)
+        return MOE_ERR_UNSUPPORTED;
     bool ok = true;
     if (KIND == kForward) {
         ok = encode_tensor(p.a, a.other, {3, {W, F, a.E}, {W, F * W}, {kStep, kSide, 1}});
