@@ -43,6 +43,7 @@ constexpr int kStage = 2 * kOperand;
 constexpr int kChunk = 64 * kLine;          // 64 rows of an operand across
 constexpr int kMaxN = 256;
 constexpr int kRowBoxes = 4;
+constexpr int kLinePitch = 144;
 constexpr int kPitch = 80;                  // bytes from row to row of the staging: 16 more than a row, so that eight rows meet no bank twice
 constexpr int kBlock = 8;                   // tiles of one side that pass along the other together
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -70,7 +71,7 @@ struct Layout {
                          sums_empty = sums_full + 16, done = sums_empty + 16, tmem = done + 8, first = tmem + 8;
     static int bytes(int E) { return first + 2 * 4 * (E + 1); }
 };
-static_assert(kWriters * 2048 >= kWriters * 16 * kPitch, "32 rows of staging reach into the room of the exchange");
+static_assert(2048 >= 16 * kPitch && 2048 + 16 * kPitch >= 16 * kLinePitch, "longer stagings reach into the room of the exchange");
 static_assert(Layout::first + 2 * 4 * (MOE_LAYER_MAX_EXPERTS + 1) <= 232448, "shared memory of a CTA");
 
 struct Tile {
@@ -207,50 +208,89 @@ __device__ __forceinline__ void store_rows(const uint8_t *staging, uint8_t *out,
     __syncwarp();
 }
 
-// One tile's sums to their place: warps `quarter` (0 to 3) of the CTA of rank `rank` have lanes 32 quarter on, and take turns.  Sums come as
-// fragments of 8 x 8, which go through the warp's staging so that 64 bytes of a row of the result are written together.
+// 16 rows of 128 bytes of a warp's staging, the same way: whole lines.
+__device__ __forceinline__ void store_lines(const uint8_t *staging, uint8_t *out, int64_t stride, int rows, int left, int lane)
+{
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        const int r = i + lane / 8, part = lane % 8;
+        if (r < rows && 16 * part < left)
+            *reinterpret_cast<uint4 *>(out + r * stride + 16 * part) = *reinterpret_cast<const uint4 *>(staging + r * kLinePitch + 16 * part);
+    }
+    __syncwarp();
+}
+
+// A tile of the weights' gradient: lanes are rows of the result, so a warp has whole lines of it, 64 columns (32 of fp32) of
+// 16 rows at a time.
+template <bool BF16>
+__device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, uint32_t sums, int quarter, int part, int lane, int rank,
+                                               uint8_t *staging, bool lost)
+{
+    for (int c = 64 * part; c < t.n; c += 128) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            uint32_t raw[32];
+            if (t.steps > 0 && !lost) {
+                tmem_load_fragments(sums + (static_cast<uint32_t>(32 * quarter + 16 * h) << 16) + c, raw);
+                tmem_load_wait();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    raw[j] = lost ? 0x7FC00000u : 0u;
+            }
+            const auto sum = [&](int s, int b, int j) { return __uint_as_float(raw[4 * b + 2 * s + j]); };
+            const int row = t.m0 + rank * kSide + 32 * quarter + 16 * h, left = p.out_width - t.n0 - c;
+            const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
+            if (p.fp32_out) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            *reinterpret_cast<float2 *>(staging + (8 * s + lane / 4) * kLinePitch + 32 * b + 8 * (lane % 4)) =
+                                make_float2(sum(s, 4 * x + b, 0), sum(s, 4 * x + b, 1));
+                    store_lines(staging, p.out + 4 * (at + 32 * x), 4 * static_cast<int64_t>(p.out_width), p.width - row, 4 * (left - 32 * x), lane);
+                }
+            } else {
+                const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kLinePitch + (lane / 8) * 16;
+                const auto pair = [&](int s, int b) { return pack2<BF16>(sum(s, b, 0), sum(s, b, 1)); };
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int b = 0; b < 8; b += 4)
+                        store_fragments<false>(at_lane + 8 * s * kLinePitch + 16 * b, pair(s, b), pair(s, b + 1), pair(s, b + 2), pair(s, b + 3));
+                store_lines(staging, p.out + 2 * at, 2 * static_cast<int64_t>(p.out_width), p.width - row, 2 * left, lane);
+            }
+        }
+    }
+}
+
+// A tile of rows to its place: warps `quarter` (0 to 3) of the CTA of rank `rank` have lanes 32 quarter on, and take turns.
+// Lanes are columns of the result here.  Sums come as fragments of 8 x 8, which go through the warp's staging so that 64
+// bytes of a row of the result are written together.
 template <int KIND, bool BF16, int ACT>
 __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint32_t sums, int quarter, int part, int lane, int rank,
                                            uint8_t *staging, float *exchange, bool lost)
 {
     const uint32_t from = sums + (static_cast<uint32_t>(quarter) << 21);
-    const bool none = KIND == kWeight && t.steps == 0;
     const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16;
     for (int c = 32 * part; c < t.n; c += 64) {
         uint32_t raw[2][16];
-        if (!none && !lost) {
+        if (!lost) {
             tmem_load_fragments(from + c, raw[0]);
             tmem_load_fragments(from + (16u << 16) + c, raw[1]);
             tmem_load_wait();
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                raw[0][j] = raw[1][j] = lost ? 0x7FC00000u : 0u;
+                raw[0][j] = raw[1][j] = 0x7FC00000u;
         }
         // the sum of lane 8 i + (lane / 4), column 8 b + 2 (lane % 4) + j of the chunk
         const auto sum = [&](int i, int b, int j) { return __uint_as_float(raw[i / 2][4 * b + 2 * (i % 2) + j]); };
         const auto pair = [&](int i, int b) { return pack2<BF16>(sum(i, b, 0), sum(i, b, 1)); };
-        if constexpr (KIND == kWeight) {
-            // rows of the result are lanes
-            const int row = t.m0 + rank * kSide + 32 * quarter, left = p.out_width - t.n0 - c;
-            const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
-            if (p.fp32_out) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int r = 8 * i + lane / 4, column = 8 * b + 2 * (lane % 4);
-                        if (row + r < p.width && column < left)
-                            *reinterpret_cast<float2 *>(p.out + 4 * (at + static_cast<int64_t>(r) * p.out_width + column)) =
-                                make_float2(sum(i, b, 0), sum(i, b, 1));
-                    }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    store_fragments<false>(at_lane + 8 * i * kPitch, pair(i, 0), pair(i, 1), pair(i, 2), pair(i, 3));
-                store_rows<32>(staging, p.out + 2 * at, p.out_width, p.width - row, left, lane);
-            }
-        } else if constexpr (KIND == kGated) {
+        if constexpr (KIND == kGated) {
             // quarters 0 and 1 hold W1's sums, 2 and 3 W3's of the same features
             const int f = t.m0 + rank * 64 + 32 * (quarter & 1);
             const bool up = quarter >= 2;
@@ -504,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp >= 4) {
         const int quarter = warp & 3, part = warp / 4 - 1;
         const uint32_t empty_of_pair = cluster_map(sums_empty, 0);
-        uint8_t *staging = smem + Layout::staging + (warp - 4) * (KIND == kGated ? 16 : 32) * kPitch;
+        uint8_t *staging = smem + Layout::staging + (warp - 4) * (KIND == kWeight ? 16 * kLinePitch : (KIND == kGated ? 16 : 32) * kPitch);
         float *exchange = reinterpret_cast<float *>(smem + Layout::exchange);
         uint32_t turn = 0;
         bool lost = false;
@@ -517,7 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 lost = __any_sync(0xffffffffu, lost);
                 tcgen05_fence_after();
             }
-            write_tile<KIND, BF16, ACT>(p, t, tmem + i * kMaxN, quarter, part, lane, rank, staging, exchange, lost);
+            if constexpr (KIND == kWeight)
+                write_gradient<BF16>(p, t, tmem + i * kMaxN, quarter, part, lane, rank, staging, lost);
+            else
+                write_tile<KIND, BF16, ACT>(p, t, tmem + i * kMaxN, quarter, part, lane, rank, staging, exchange, lost);
             if (t.steps > 0) {
                 tcgen05_fence_before();
                 __syncwarp();
