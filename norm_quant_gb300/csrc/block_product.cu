@@ -43,8 +43,7 @@ constexpr int kStage = 2 * kOperand;
 constexpr int kChunk = 64 * kLine;          // 64 rows of an operand across
 constexpr int kMaxN = 256;
 constexpr int kRowBoxes = 4;
-constexpr int kLinePitch = 144;
-constexpr int kPitch = 80;                  // bytes from row to row of the staging: 16 more than a row, so that eight rows meet no bank twice
+constexpr int kPitch = 144;                 // bytes from row to row of a staging: 16 more than a line, so that eight rows meet no bank twice
 constexpr int kBlock = 8;                   // tiles of one side that pass along the other together
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -64,14 +63,14 @@ struct Params {
 
 // Shared memory.
 struct Layout {
-    static constexpr int staging = kStages * kStage;  // each writing warp's rows of results: 32, or 16 where two warps exchange sums
-    static constexpr int exchange = staging + kWriters * 16 * kPitch;  // gated: 2 KB for each of them
+    static constexpr int staging = kStages * kStage;  // 32 lines for two writing warps, or 16 where sums are exchanged
+    static constexpr int exchange = staging + kWriters / 2 * 16 * kPitch;  // gated: 2 KB a writing warp
     static constexpr int bars = exchange + kWriters * 2048;
     static constexpr int full = bars, empty = full + 8 * kStages, tail = empty + 8 * kStages, sums_full = tail + 8 * kStages,
                          sums_empty = sums_full + 16, done = sums_empty + 16, tmem = done + 8, first = tmem + 8;
     static int bytes(int E) { return first + 2 * 4 * (E + 1); }
 };
-static_assert(2048 >= 16 * kPitch && 2048 + 16 * kPitch >= 16 * kLinePitch, "longer stagings reach into the room of the exchange");
+static_assert(kWriters * 2048 >= kWriters / 2 * 16 * kPitch, "stagings of 32 lines reach into the room of the exchange");
 static_assert(Layout::first + 2 * 4 * (MOE_LAYER_MAX_EXPERTS + 1) <= 232448, "shared memory of a CTA");
 
 struct Tile {
@@ -193,32 +192,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs));
 }
 
-// Rows of 32 16-bit values in a warp's staging to global memory, in pieces of 16 bytes: row r to out + r * stride for r < rows,
-// and of each the first `left` values (a multiple of 8).  Lines of 64 bytes, so whole sectors.
+// ROWS rows of 128 bytes in shared memory to global memory: row r to out + r * stride (bytes) for r < rows, and of each the first
+// `left` bytes (a multiple of 16).  Whole lines: lines written half by half, by whichever warps, took twice the time (a weights' gradient of 1.07 GB 311
+// us, 3.5 TB/s; whole lines 174 us).
 template <int ROWS>
-__device__ __forceinline__ void store_rows(const uint8_t *staging, uint8_t *out, int64_t stride, int rows, int left, int lane)
-{
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < ROWS; i += 8) {
-        const int r = i + lane / 4, part = lane % 4;
-        if (r < rows && 8 * part < left)
-            *reinterpret_cast<uint4 *>(out + 2 * (r * stride + 8 * part)) = *reinterpret_cast<const uint4 *>(staging + r * kPitch + 16 * part);
-    }
-    __syncwarp();
-}
-
-// 16 rows of 128 bytes of a warp's staging, the same way: whole lines.
 __device__ __forceinline__ void store_lines(const uint8_t *staging, uint8_t *out, int64_t stride, int rows, int left, int lane)
 {
-    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
+    for (int i = 0; i < ROWS; i += 4) {
         const int r = i + lane / 8, part = lane % 8;
         if (r < rows && 16 * part < left)
-            *reinterpret_cast<uint4 *>(out + r * stride + 16 * part) = *reinterpret_cast<const uint4 *>(staging + r * kLinePitch + 16 * part);
+            *reinterpret_cast<uint4 *>(out + r * stride + 16 * part) = *reinterpret_cast<const uint4 *>(staging + r * kPitch + 16 * part);
     }
-    __syncwarp();
 }
 
 // A tile of the weights' gradient: lanes are rows of the result, so a warp has whole lines of it, 64 columns (32 of fp32) of
@@ -249,34 +234,40 @@ __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, u
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
-                            *reinterpret_cast<float2 *>(staging + (8 * s + lane / 4) * kLinePitch + 32 * b + 8 * (lane % 4)) =
+                            *reinterpret_cast<float2 *>(staging + (8 * s + lane / 4) * kPitch + 32 * b + 8 * (lane % 4)) =
                                 make_float2(sum(s, 4 * x + b, 0), sum(s, 4 * x + b, 1));
-                    store_lines(staging, p.out + 4 * (at + 32 * x), 4 * static_cast<int64_t>(p.out_width), p.width - row, 4 * (left - 32 * x), lane);
+                    __syncwarp();
+                    store_lines<16>(staging, p.out + 4 * (at + 32 * x), 4 * static_cast<int64_t>(p.out_width), p.width - row, 4 * (left - 32 * x), lane);
+                    __syncwarp();
                 }
             } else {
-                const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kLinePitch + (lane / 8) * 16;
+                const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16;
                 const auto pair = [&](int s, int b) { return pack2<BF16>(sum(s, b, 0), sum(s, b, 1)); };
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int b = 0; b < 8; b += 4)
-                        store_fragments<false>(at_lane + 8 * s * kLinePitch + 16 * b, pair(s, b), pair(s, b + 1), pair(s, b + 2), pair(s, b + 3));
-                store_lines(staging, p.out + 2 * at, 2 * static_cast<int64_t>(p.out_width), p.width - row, 2 * left, lane);
+                        store_fragments<false>(at_lane + 8 * s * kPitch + 16 * b, pair(s, b), pair(s, b + 1), pair(s, b + 2), pair(s, b + 3));
+                __syncwarp();
+                store_lines<16>(staging, p.out + 2 * at, 2 * static_cast<int64_t>(p.out_width), p.width - row, 2 * left, lane);
+                __syncwarp();
             }
         }
     }
 }
 
 // A tile of rows to its place: warps `quarter` (0 to 3) of the CTA of rank `rank` have lanes 32 quarter on, and take turns.
-// Lanes are columns of the result here.  Sums come as fragments of 8 x 8, which go through the warp's staging so that 64
-// bytes of a row of the result are written together.
+// Lanes are columns of the result here.  Sums come as fragments of 8 x 8, and two warps put the 64 columns of theirs together
+// in a staging, so that whole lines are written.
 template <int KIND, bool BF16, int ACT>
 __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint32_t sums, int quarter, int part, int lane, int rank,
                                            uint8_t *staging, float *exchange, bool lost)
 {
     const uint32_t from = sums + (static_cast<uint32_t>(quarter) << 21);
-    const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16;
+    const int second = quarter & 1;  // of the two warps
+    const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16 + 64 * second;
     for (int c = 32 * part; c < t.n; c += 64) {
+        __syncwarp();
         uint32_t raw[2][16];
         if (!lost) {
             tmem_load_fragments(from + c, raw[0]);
@@ -291,29 +282,32 @@ __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint3
         const auto sum = [&](int i, int b, int j) { return __uint_as_float(raw[i / 2][4 * b + 2 * (i % 2) + j]); };
         const auto pair = [&](int i, int b) { return pack2<BF16>(sum(i, b, 0), sum(i, b, 1)); };
         if constexpr (KIND == kGated) {
-            // quarters 0 and 1 hold W1's sums, 2 and 3 W3's of the same features
-            const int f = t.m0 + rank * 64 + 32 * (quarter & 1);
+            // quarters 0 and 1 hold W1's sums, 2 and 3 W3's of the same features; the gate's warps take the chunk's first 16
+            // columns and the others the last, and each gives the other what it needs
+            const int f = t.m0 + rank * 64;
             const bool up = quarter >= 2;
+            const uint32_t all = 1 + part;  // the barrier of the four warps
+            float *give = exchange + (4 * part + quarter) * 512 + lane, *take = exchange + (4 * part + (quarter ^ 2)) * 512 + lane;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int i = j / 4, b = j / 2 % 2;
+                give[32 * j] = up ? sum(i, b, j % 2) : sum(i, 2 + b, j % 2);
+            }
             if (p.gate_up) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
                         store_fragments<true>(at_lane + 8 * b * kPitch, pair(0, 2 * h + b), pair(1, 2 * h + b), pair(2, 2 * h + b), pair(3, 2 * h + b));
-                    const int column = c + 16 * h;
-                    store_rows<16>(staging, p.gate_up + 2 * ((t.row + column) * p.gate_up_stride + (up ? p.out_width : 0) + f), p.gate_up_stride,
-                                   t.rows - column, p.out_width - f, lane);
+                    named_barrier_sync(all, 128);
+                    const int column = c + 16 * h + 8 * second;
+                    store_lines<8>(staging + 8 * second * kPitch, p.gate_up + 2 * ((t.row + column) * p.gate_up_stride + (up ? p.out_width : 0) + f),
+                                   2 * p.gate_up_stride, t.rows - column, 2 * (p.out_width - f), lane);
+                    named_barrier_sync(all, 128);
                 }
+            } else {
+                named_barrier_sync(all, 128);
             }
-            // the gate's warp takes the chunk's first 16 columns, the other the last
-            float *give = exchange + (4 * part + quarter) * 512 + lane, *take = exchange + (4 * part + (quarter ^ 2)) * 512 + lane;
-            const uint32_t both = 1 + 2 * part + (quarter & 1);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int i = j / 4, b = j / 2 % 2;
-                give[32 * j] = up ? sum(i, b, j % 2) : sum(i, 2 + b, j % 2);
-            }
-            named_barrier_sync(both, 64);
             float h[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -322,19 +316,26 @@ __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint3
                 const float g = up ? other : sum(i, b, j % 2), u = up ? sum(i, 2 + b, j % 2) : other;
                 h[j] = act<ACT>(g) * u;
             }
-            named_barrier_sync(both, 64);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 store_fragments<true>(at_lane + 8 * b * kPitch, pack2<BF16>(h[2 * b], h[2 * b + 1]), pack2<BF16>(h[4 + 2 * b], h[5 + 2 * b]),
                                       pack2<BF16>(h[8 + 2 * b], h[9 + 2 * b]), pack2<BF16>(h[12 + 2 * b], h[13 + 2 * b]));
-            const int column = c + (up ? 16 : 0);
-            store_rows<16>(staging, p.out + 2 * ((t.row + column) * p.out_stride + f), p.out_stride, t.rows - column, p.out_width - f, lane);
+            named_barrier_sync(all, 128);
+            const int column = c + (up ? 16 : 0) + 8 * second;
+            store_lines<8>(staging + 8 * second * kPitch, p.out + 2 * ((t.row + column) * p.out_stride + f), 2 * p.out_stride, t.rows - column,
+                           2 * (p.out_width - f), lane);
+            named_barrier_sync(all, 128);
         } else {
-            const int f = t.m0 + rank * kSide + 32 * quarter;
+            const int f = t.m0 + rank * kSide + 64 * (quarter / 2);
+            const uint32_t both = 1 + 2 * part + quarter / 2;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 store_fragments<true>(at_lane + 8 * b * kPitch, pair(0, b), pair(1, b), pair(2, b), pair(3, b));
-            store_rows<32>(staging, p.out + 2 * ((t.row + c) * p.out_stride + f), p.out_stride, t.rows - c, p.out_width - f, lane);
+            named_barrier_sync(both, 64);
+            const int column = c + 16 * second;
+            store_lines<16>(staging + 16 * second * kPitch, p.out + 2 * ((t.row + column) * p.out_stride + f), 2 * p.out_stride, t.rows - column,
+                            2 * (p.out_width - f), lane);
+            named_barrier_sync(both, 64);
         }
     }
 }
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp >= 4) {
         const int quarter = warp & 3, part = warp / 4 - 1;
         const uint32_t empty_of_pair = cluster_map(sums_empty, 0);
-        uint8_t *staging = smem + Layout::staging + (warp - 4) * (KIND == kWeight ? 16 * kLinePitch : (KIND == kGated ? 16 : 32) * kPitch);
+        uint8_t *staging = smem + Layout::staging + (KIND == kWeight ? warp - 4 : (KIND == kGated ? 1 : 2) * (warp / 2 - 2)) * 16 * kPitch;
         float *exchange = reinterpret_cast<float *>(smem + Layout::exchange);
         uint32_t turn = 0;
         bool lost = false;
