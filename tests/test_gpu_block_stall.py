@@ -65,3 +65,39 @@ def test_copies_that_stop(what, slots):
     status.zero_()
     call()
     assert torch.equal(out, good) and int(status) == 0
+
+
+@pytest.mark.parametrize("slots", [0, 1, 3])
+@pytest.mark.parametrize("H", [96, 4096, 16384])
+def test_norm_rows_that_stop(slots, H):
+    """Rows of the first CTA's first group from that one on are NaN, and so are the sums over tokens that they are part of."""
+    T = 12000 if H == 96 else 3000
+    g = gen(H)
+    y, r, d = (normal(g, T, H).to(DEV) for _ in range(3))
+    gamma = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    out = [torch.empty_like(y) for _ in range(4)]
+    sums = [torch.empty(H, device=DEV) for _ in range(2)]
+    ws = torch.empty(nqg.moe_block_norm_backward_workspace_size(T, H), dtype=torch.uint8, device=DEV)
+
+    def forward():
+        nqg.moe_block_norm(y, r, post_gamma=gamma, pre_gamma=gamma, residual_out=out[0], norm_out=out[1])
+
+    def backward():
+        nqg.moe_block_norm_backward(y, r, post_gamma=gamma, pre_gamma=gamma, d_residual_out=d, d_norm_out=d, d_y=out[2], d_residual=out[3],
+                                    d_post_gamma=sums[0], d_pre_gamma=sums[1], workspace=ws)
+
+    for call, results in ((forward, out[:2]), (backward, out[2:])):
+        if call is backward and H > 8192:
+            continue  # rows this wide are not copied ahead there
+        call()
+        good = [t.clone() for t in results]
+        assert all(bool(t.isfinite().all()) for t in good)
+        stalled(slots, call)
+        for t, was in zip(results, good):
+            late = t.isnan().all(1)
+            assert 0 < int(late.sum()) <= T // 152 + 1
+            assert torch.equal(t[~late], was[~late])
+        if call is backward:
+            assert all(bool(s.isnan().all()) for s in sums)
+        call()
+        assert all(torch.equal(a, b) for a, b in zip(results, good))
