@@ -83,14 +83,91 @@ __device__ __forceinline__ void factors8(float (&v)[8], const NormParams &p, con
         v[i] *= p.gate_kind == MOE_GATE_CHANNEL ? p.block_scale * g[i] : p.block_scale;
 }
 
-__device__ __forceinline__ float token_gate(const NormParams &p, int64_t t)
-{
-    return p.gate_kind == MOE_GATE_TOKEN ? __ldg(reinterpret_cast<const float *>(p.gate) + t) : 1.0f;
-}
-
 __device__ __forceinline__ uint4 vector_of(const uint8_t *p, int i, bool take)
 {
     return take ? ldg16(p + 16 * i) : make_uint4(0, 0, 0, 0);
+}
+
+// Two fp32 in a register pair: the packed instructions do both at once, each rounded like the scalar one.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void split(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t both(float v) { return pair_of(v, v); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ float total(uint64_t v)
+{
+    float lo, hi;
+    split(v, lo, hi);
+    return lo + hi;
+}
+
+// 8 elements as four pairs, and back.
+template <bool BF16>
+__device__ __forceinline__ void pairs8(uint64_t (&v)[4], const uint4 &w)
+{
+    float f[8];
+    unpack8<BF16>(w, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = pair_of(f[2 * i], f[2 * i + 1]);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&v)[4])
+{
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        split(v[i], f[2 * i], f[2 * i + 1]);
+    return pack8<BF16>(f);
+}
+
+// The columns' two factors, block_scale * gate * (post_gamma + bias) and pre_gamma + bias, as fp32 in shared memory: the
+// first four of each vector of 8, and then the others, so that neighbouring lanes read neighbouring 16 bytes.
+struct Factors {
+    const float *c, *c2;
+    int half;  // H / 2
+
+    __device__ __forceinline__ static void read(uint64_t (&v)[4], const float *at, int i, int half)
+    {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(at + 4 * i), b = *reinterpret_cast<const ulonglong2 *>(at + half + 4 * i);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void fill_factors(const NormParams &p, float *c)
+{
+    const int half = p.H / 2;
+    for (int i = threadIdx.x; i < p.H / 8; i += blockDim.x) {
+        float v[8];
+        factors8<BF16>(v, p, vector_of(p.post, i, p.post), vector_of(p.gate, i, p.gate_kind == MOE_GATE_CHANNEL));
+        *reinterpret_cast<float4 *>(c + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(c + half + 4 * i) = make_float4(v[4], v[5], v[6], v[7]);
+        gammas8<BF16>(v, p.pre != nullptr, vector_of(p.pre, i, p.pre), p.bias);
+        *reinterpret_cast<float4 *>(c + p.H + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(c + p.H + half + 4 * i) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+__device__ __forceinline__ float token_gate(const NormParams &p, int64_t t)
+{
+    return p.gate_kind == MOE_GATE_TOKEN ? __ldg(reinterpret_cast<const float *>(p.gate) + t) : 1.0f;
 }
 
 __device__ __forceinline__ void store8(uint8_t *p, const uint4 &v) { *reinterpret_cast<uint4 *>(p) = v; }
@@ -221,95 +298,108 @@ struct Rows {
     }
 };
 
-template <bool BF16, int VPT>
+// FACTORS: the columns' factors are in shared memory behind the slots; else (rows that leave no room) they come from L1 at
+// each use.
+template <bool BF16, int VPT, bool FACTORS>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormParams p)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RingSmem r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *factors = reinterpret_cast<float *>(ring + p.slots * p.groups * p.stage);
     ring_init(p, r);
     grid_dependency_wait();
-    {
-        Group g{p.group_warps, warp % p.group_warps, lane, warp / p.group_warps, r.red[warp / p.group_warps], 0};
-        Rows rows(p, r, ring, g, false);
-        const int vectors = p.H / 8, threads = 32 * g.warps, first = 32 * g.warp + lane;
-        // both factors of a column stay in registers where there is room, and come from L1 at each use where not
-        constexpr bool kKeep = VPT <= 2;
-        const auto factors = [&](float (&c)[8], int i) {
-            factors8<BF16>(c, p, vector_of(p.post, i, i < vectors && p.post), vector_of(p.gate, i, i < vectors && p.gate_kind == MOE_GATE_CHANNEL));
-        };
-        const auto pre_gammas = [&](float (&c)[8], int i) { gammas8<BF16>(c, p.pre != nullptr, vector_of(p.pre, i, i < vectors && p.pre), p.bias); };
-        float kept[kKeep ? VPT : 1][8], kept2[kKeep ? VPT : 1][8];
-        if constexpr (kKeep)
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                factors(kept[j], first + j * threads);
-                pre_gammas(kept2[j], first + j * threads);
-            }
-        while (rows.t < p.T) {
-            const float lost = rows.wait();
-            const uint8_t *at = rows.at;
-            const int64_t t = rows.t, row = 2 * t * p.H;
-            float s[VPT][8], sum[1] = {lost};
-            float ry = 1.0f;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = first + j * threads;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    s[j][k] = 0.0f;
-                if (i < vectors)
-                    load8<BF16>(s[j], at + 16 * i);
-            }
-            if (p.post) {
-#pragma unroll
-                for (int j = 0; j < VPT; ++j)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        sum[0] = fmaf(s[j][k], s[j][k], sum[0]);
-                g.sum(sum);
-                ry = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
-            }
-            ry *= token_gate(p, t);
-            sum[0] = lost;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = first + j * threads;
-                float res[8] = {}, c[8];
-                if (p.residual && i < vectors)
-                    load8<BF16>(res, at + p.at_residual + 16 * i);
-                if constexpr (!kKeep)
-                    factors(c, i);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    s[j][k] = fmaf(s[j][k], ry * (kKeep ? kept[kKeep ? j : 0][k] : c[k]), p.residual ? p.residual_scale * res[k] : 0.0f) + lost;
-                    sum[0] = fmaf(s[j][k], s[j][k], sum[0]);
-                }
-            }
-            rows.release(lane);
-            if (p.residual_out)
-#pragma unroll
-                for (int j = 0; j < VPT; ++j)
-                    if (first + j * threads < vectors)
-                        store8(p.residual_out + row + 16 * (first + j * threads), pack8<BF16>(s[j]));
-            if (!p.norm_out)
-                continue;
-            g.sum(sum);
-            const float rs = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                float c[8];
-                if constexpr (!kKeep)
-                    pre_gammas(c, first + j * threads);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    s[j][k] *= rs * (kKeep ? kept2[kKeep ? j : 0][k] : c[k]);
-                if (first + j * threads < vectors)
-                    store8(p.norm_out + row + 16 * (first + j * threads), pack8<BF16>(s[j]));
-            }
-        }
-        rows.finish();
+    Group g{p.group_warps, warp % p.group_warps, lane, warp / p.group_warps, r.red[warp / p.group_warps], 0};
+    Rows rows(p, r, ring, g, false);
+    const int vectors = p.H / 8, threads = 32 * g.warps, first = 32 * g.warp + lane;
+    if constexpr (FACTORS) {
+        fill_factors<BF16>(p, factors);
+        __syncthreads();
     }
+    const auto factor = [&](uint64_t (&c)[4], int i, bool pre) {
+        if constexpr (FACTORS) {
+            Factors::read(c, factors + (pre ? p.H : 0), i, p.H / 2);
+        } else {
+            float v[8];
+            if (pre)
+                gammas8<BF16>(v, p.pre != nullptr, vector_of(p.pre, i, p.pre), p.bias);
+            else
+                factors8<BF16>(v, p, vector_of(p.post, i, p.post), vector_of(p.gate, i, p.gate_kind == MOE_GATE_CHANNEL));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                c[k] = pair_of(v[2 * k], v[2 * k + 1]);
+        }
+    };
+    while (rows.t < p.T) {
+        const float lost = rows.wait();
+        const uint8_t *at = rows.at;
+        const int64_t t = rows.t, row = 2 * t * p.H;
+        uint64_t s[VPT][4], acc = both(0.0f);
+        float ry = 1.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * threads;
+            pairs8<BF16>(s[j], i < vectors ? *reinterpret_cast<const uint4 *>(at + 16 * i) : make_uint4(0, 0, 0, 0));
+        }
+        if (p.post) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    acc = fma2(s[j][k], s[j][k], acc);
+            float sum[1] = {total(acc) + lost};
+            g.sum(sum);
+            ry = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
+        }
+        const uint64_t scale = both(ry * token_gate(p, t) + lost), from_residual = both(p.residual_scale);
+        acc = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * threads;
+            if (i >= vectors)
+                continue;  // zeros from here on, as they were
+            uint64_t c[4], res[4];
+            factor(c, i, false);
+            if (p.residual) {
+                pairs8<BF16>(res, *reinterpret_cast<const uint4 *>(at + p.at_residual + 16 * i));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[j][k] = fma2(s[j][k], mul2(scale, c[k]), mul2(from_residual, res[k]));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[j][k] = mul2(s[j][k], mul2(scale, c[k]));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                acc = fma2(s[j][k], s[j][k], acc);
+        }
+        rows.release(lane);
+        if (p.residual_out) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (first + j * threads < vectors)
+                    store8(p.residual_out + row + 16 * (first + j * threads), pack_pairs<BF16>(s[j]));
+        }
+        if (!p.norm_out)
+            continue;
+        float sum[1] = {total(acc)};
+        g.sum(sum);
+        const uint64_t rs = both(rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps)));
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * threads;
+            if (i >= vectors)
+                continue;
+            uint64_t c[4];
+            factor(c, i, true);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                s[j][k] = mul2(s[j][k], mul2(rs, c[k]));
+            store8(p.norm_out + row + 16 * i, pack_pairs<BF16>(s[j]));
+        }
+    }
+    rows.finish();
     allow_dependent_launch();
 }
 
@@ -320,124 +410,140 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RingSmem r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *factors = reinterpret_cast<float *>(ring + p.slots * p.groups * p.stage);
     ring_init(p, r);
     grid_dependency_wait();
     Group g{p.group_warps, warp % p.group_warps, lane, warp / p.group_warps, r.red[warp / p.group_warps], 0};
-    const int vectors = p.H / 8, threads = 32 * g.warps, first = 32 * g.warp + lane;
-    float A[VPT][8] = {}, B[VPT][8] = {};
-    {
-        Rows rows(p, r, ring, g, true);
-        // the three vectors come from L1 at each use: registers are for A and B
-        const auto factors = [&](float (&c)[8], int i) {
-            factors8<BF16>(c, p, vector_of(p.post, i, i < vectors && p.post), vector_of(p.gate, i, i < vectors && p.gate_kind == MOE_GATE_CHANNEL));
-        };
-        const auto pre_gammas = [&](float (&c)[8], int i) { gammas8<BF16>(c, true, vector_of(p.pre, i, i < vectors && p.pre), p.bias); };
-        while (rows.t < p.T) {
-            const float lost = rows.wait();
-            const uint8_t *at = rows.at;
-            const int64_t t = rows.t, row = 2 * t * p.H;
-            float ry = 1.0f;
-            if (p.post) {
-                float sum[1] = {lost};
+    Rows rows(p, r, ring, g, true);
+    const int vectors = p.H / 8, threads = 32 * g.warps, first = 32 * g.warp + lane, half = p.H / 2;
+    fill_factors<BF16>(p, factors);
+    __syncthreads();
+    uint64_t A[VPT][4], B[VPT][4];
 #pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int i = first + j * threads;
-                    float y[8] = {};
-                    if (i < vectors)
-                        load8<BF16>(y, at + 16 * i);
+    for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        sum[0] = fmaf(y[k], y[k], sum[0]);
-                }
-                g.sum(sum);
-                ry = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
-            }
-            const float token = token_gate(p, t);
-            float s[VPT][8];  // s, and then ds
-            float sum[2] = {lost, lost};
+        for (int k = 0; k < 4; ++k)
+            A[j][k] = B[j][k] = both(0.0f);
+    while (rows.t < p.T) {
+        const float lost = rows.wait();
+        const uint8_t *at = rows.at;
+        const int64_t t = rows.t, row = 2 * t * p.H;
+        uint64_t y[VPT][4], s[VPT][4], d[VPT][4], acc = both(0.0f), acc2 = both(0.0f);
+        float ry = 1.0f;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = first + j * threads;
-                float y[8] = {}, res[8] = {}, d[8] = {}, c[8];
-                if (i < vectors) {
-                    load8<BF16>(y, at + 16 * i);
-                    if (p.residual)
-                        load8<BF16>(res, at + p.at_residual + 16 * i);
-                    if (p.d_norm_out)
-                        load8<BF16>(d, at + p.at_d_norm + 16 * i);
-                }
-                factors(c, i);
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * threads;
+            pairs8<BF16>(y[j], i < vectors ? *reinterpret_cast<const uint4 *>(at + 16 * i) : make_uint4(0, 0, 0, 0));
+        }
+        if (p.post) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    s[j][k] = fmaf(y[k], token * ry * c[k], p.residual ? p.residual_scale * res[k] : 0.0f);
-                    sum[0] = fmaf(s[j][k], s[j][k], sum[0]);
-                }
-                pre_gammas(c, i);
+            for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    sum[1] = fmaf(s[j][k], d[k] * c[k], sum[1]);
-            }
-            float rs = 0.0f, back = lost;  // back: mean(v m) / rms(s)^2
-            if (p.d_norm_out) {
-                g.sum(sum);
-                rs = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
-                back = sum[1] * p.inv_h * rs * rs * rs;
-            }
-            float dot[1] = {0.0f};
+                for (int k = 0; k < 4; ++k)
+                    acc = fma2(y[j][k], y[j][k], acc);
+            float sum[1] = {total(acc) + lost};
+            g.sum(sum);
+            ry = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
+        }
+        const float token = ry * token_gate(p, t) + lost;  // the token's gate over rms(y)
+        const uint64_t scale = both(token), from_residual = both(p.residual_scale);
+        float rs = 0.0f, back = lost;  // back: mean(v m) / rms(s)^2
+        if (p.d_norm_out) {
+            acc = both(0.0f);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int i = first + j * threads;
-                float y[8] = {}, d[8] = {}, dr[8] = {}, c[8];
-                if (i < vectors) {
-                    load8<BF16>(y, at + 16 * i);
-                    if (p.d_norm_out)
-                        load8<BF16>(d, at + p.at_d_norm + 16 * i);
-                    if (p.d_residual_out)
-                        load8<BF16>(dr, at + p.at_d_residual + 16 * i);
-                }
-                pre_gammas(c, i);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    B[j][k] = fmaf(d[k], s[j][k] * rs, B[j][k]);
-                    s[j][k] = fmaf(rs, d[k] * c[k], fmaf(-back, s[j][k], dr[k]));
-                }
-                factors(c, i);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    dot[0] = fmaf(s[j][k], c[k] * y[k], dot[0]);
-                    A[j][k] = fmaf(s[j][k], y[k] * (ry * token), A[j][k]);
-                }
-            }
-            if (p.post || p.gate_kind == MOE_GATE_TOKEN)
-                g.sum(dot);
-            if (p.d_gate && p.gate_kind == MOE_GATE_TOKEN && g.warp == 0 && lane == 0)
-                p.d_gate[t] = dot[0] * ry;
-            const float pull = p.post ? dot[0] * p.inv_h * token * ry * ry * ry : 0.0f;  // mean(c ds n) / rms(y)^2
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = first + j * threads;
+                for (int k = 0; k < 4; ++k)
+                    s[j][k] = d[j][k] = both(0.0f);
                 if (i >= vectors)
                     continue;
-                if (p.d_y) {
-                    float y[8], c[8];
-                    load8<BF16>(y, at + 16 * i);
-                    factors(c, i);
+                uint64_t c[4], res[4];
+                Factors::read(c, factors, i, half);
+                if (p.residual) {
+                    pairs8<BF16>(res, *reinterpret_cast<const uint4 *>(at + p.at_residual + 16 * i));
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        c[k] = fmaf(ry * token, c[k] * s[j][k], -pull * y[k]);
-                    store8(p.d_y + row + 16 * i, pack8<BF16>(c));
+                    for (int k = 0; k < 4; ++k)
+                        s[j][k] = fma2(y[j][k], mul2(scale, c[k]), mul2(from_residual, res[k]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s[j][k] = mul2(y[j][k], mul2(scale, c[k]));
                 }
-                if (p.d_residual) {
+                pairs8<BF16>(d[j], *reinterpret_cast<const uint4 *>(at + p.at_d_norm + 16 * i));
+                Factors::read(c, factors + p.H, i, half);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        s[j][k] *= p.residual_scale;
-                    store8(p.d_residual + row + 16 * i, pack8<BF16>(s[j]));
+                for (int k = 0; k < 4; ++k) {
+                    acc = fma2(s[j][k], s[j][k], acc);
+                    acc2 = fma2(s[j][k], mul2(d[j][k], c[k]), acc2);
                 }
             }
-            rows.release(lane);
+            float sum[2] = {total(acc), total(acc2)};
+            g.sum(sum);
+            rs = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
+            back = sum[1] * p.inv_h * rs * rs * rs;
         }
-        rows.finish();
+        // s becomes ds
+        acc = both(0.0f);
+        const uint64_t rs2 = both(rs), back2 = both(-back);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * threads;
+            if (i >= vectors)
+                continue;
+            uint64_t c[4], dr[4];
+            pairs8<BF16>(dr, p.d_residual_out ? *reinterpret_cast<const uint4 *>(at + p.at_d_residual + 16 * i) : make_uint4(0, 0, 0, 0));
+            if (p.d_norm_out) {
+                Factors::read(c, factors + p.H, i, half);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    d[j][k] = mul2(d[j][k], rs2);
+                    B[j][k] = fma2(d[j][k], s[j][k], B[j][k]);
+                    s[j][k] = fma2(d[j][k], c[k], fma2(back2, s[j][k], dr[k]));
+                }
+            } else {
+                const uint64_t add = both(lost);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[j][k] = fma2(dr[k], both(1.0f), add);
+            }
+            Factors::read(c, factors, i, half);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t e = mul2(s[j][k], y[j][k]);
+                acc = fma2(e, c[k], acc);
+                A[j][k] = fma2(e, scale, A[j][k]);
+            }
+        }
+        rows.release(lane);
+        float dot[1] = {total(acc)};
+        if (p.post || p.gate_kind == MOE_GATE_TOKEN)
+            g.sum(dot);
+        if (p.d_gate && p.gate_kind == MOE_GATE_TOKEN && g.warp == 0 && lane == 0)
+            p.d_gate[t] = dot[0] * ry;
+        const uint64_t pull = both(p.post ? -dot[0] * p.inv_h * token * ry * ry : 0.0f);  // - mean(c ds n) / rms(y)^2
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * threads;
+            if (i >= vectors)
+                continue;
+            if (p.d_y) {
+                uint64_t c[4];
+                Factors::read(c, factors, i, half);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    c[k] = fma2(mul2(scale, c[k]), s[j][k], mul2(pull, y[j][k]));
+                store8(p.d_y + row + 16 * i, pack_pairs<BF16>(c));
+            }
+            if (p.d_residual) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[j][k] = mul2(from_residual, s[j][k]);
+                store8(p.d_residual + row + 16 * i, pack_pairs<BF16>(s[j]));
+            }
+        }
     }
+    rows.finish();
     if (p.partial) {
         // the groups' sums, added up in their order in the ring's memory
         float *sums = reinterpret_cast<float *>(ring);  // [2, H]
@@ -453,9 +559,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
                 float4 *a = reinterpret_cast<float4 *>(sums + 8 * i), *b = reinterpret_cast<float4 *>(sums + p.H + 8 * i);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float4 x = turn ? a[k] : make_float4(0, 0, 0, 0), y = turn ? b[k] : make_float4(0, 0, 0, 0);
-                    x.x += A[j][4 * k], x.y += A[j][4 * k + 1], x.z += A[j][4 * k + 2], x.w += A[j][4 * k + 3];
-                    y.x += B[j][4 * k], y.y += B[j][4 * k + 1], y.z += B[j][4 * k + 2], y.w += B[j][4 * k + 3];
+                    float4 x, y;
+                    split(A[j][2 * k], x.x, x.y);
+                    split(A[j][2 * k + 1], x.z, x.w);
+                    split(B[j][2 * k], y.x, y.y);
+                    split(B[j][2 * k + 1], y.z, y.w);
+                    if (turn > 0) {
+                        const float4 u = a[k], v = b[k];
+                        x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+                        y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+                    }
                     a[k] = x;
                     b[k] = y;
                 }
@@ -693,32 +806,32 @@ int check_norm_sizes(int64_t T, int32_t H, int32_t io)
 }
 
 // As many groups of warps as a CTA has room for, and as many slots for each.
-unsigned plan_ring(NormParams &p, int vpt, int tensors)
+unsigned plan_ring(NormParams &p, int vpt, int tensors, bool factors)
 {
     p.group_warps = (p.H / 8 + 32 * vpt - 1) / (32 * vpt);
     p.stage = (tensors * 2 * p.H + 127) / 128 * 128;
-    const int room = kRingBytes / p.stage < kMaxSlots ? kRingBytes / p.stage : kMaxSlots;
+    const int bytes = kRingBytes - (factors ? 8 * p.H : 0), room = bytes / p.stage < kMaxSlots ? bytes / p.stage : kMaxSlots;
     p.groups = kWarps / p.group_warps;
     p.groups = p.groups > room ? room : p.groups;
     p.slots = room / p.groups;
     return static_cast<unsigned>(32 * p.groups * p.group_warps);
 }
 
-template <bool BF16, int VPT>
+template <bool BF16, int VPT, bool FACTORS>
 moe_status launch_norm(NormParams &p, moe_stream_t stream)
 {
     static SmemLimit limit;
     int dev = 0;
     const int sms = sm_count();
     p.at_residual = 2 * p.H;
-    const unsigned threads = plan_ring(p, VPT, p.residual ? 2 : 1);
-    const size_t smem = static_cast<size_t>(p.slots) * p.groups * p.stage;
+    const unsigned threads = plan_ring(p, VPT, p.residual ? 2 : 1, FACTORS);
+    const size_t smem = static_cast<size_t>(p.slots) * p.groups * p.stage + (FACTORS ? 8 * p.H : 0);
     if (sms <= 0 || cudaGetDevice(&dev) != cudaSuccess ||
-        ensure_dynamic_smem(norm_kernel<BF16, VPT>, dev, static_cast<int>(smem), limit) != cudaSuccess) {
+        ensure_dynamic_smem(norm_kernel<BF16, VPT, FACTORS>, dev, static_cast<int>(smem), limit) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
-    return PdlLaunch(static_cast<unsigned>(p.T < sms ? p.T : sms), threads, smem, stream).run(norm_kernel<BF16, VPT>, p);
+    return PdlLaunch(static_cast<unsigned>(p.T < sms ? p.T : sms), threads, smem, stream).run(norm_kernel<BF16, VPT, FACTORS>, p);
 }
 
 template <bool BF16>
@@ -738,9 +851,9 @@ moe_status launch_backward(NormParams &p, moe_stream_t stream)
     unsigned threads = kMaxThreads;
     size_t smem = p.partial ? static_cast<size_t>(8) * p.H : 0;
     if (!wide) {
-        threads = plan_ring(p, 2, at / (2 * p.H));
-        // the ring's memory holds the sums at the end
-        const size_t ring = static_cast<size_t>(p.slots) * p.groups * p.stage;
+        threads = plan_ring(p, 2, at / (2 * p.H), true);
+        // the slots' memory holds the sums at the end
+        const size_t ring = static_cast<size_t>(p.slots) * p.groups * p.stage + 8 * p.H;
         smem = smem > ring ? smem : ring;
     }
     const auto kern = wide ? norm_backward_wide_kernel<BF16> : norm_backward_kernel<BF16>;
@@ -789,9 +902,11 @@ extern "C" moe_status moe_block_norm(const moe_block_norm_args *a, moe_stream_t 
     p.norm_out = static_cast<uint8_t *>(a->norm_out);
     p.stall = debug_stall_slots();
     const bool bf16 = a->io_dtype == MOE_IO_BF16;
+    if (a->H <= 2048)
+        return bf16 ? launch_norm<true, 2, true>(p, stream) : launch_norm<false, 2, true>(p, stream);
     if (a->H <= kMaxRingWidth)
-        return bf16 ? launch_norm<true, 2>(p, stream) : launch_norm<false, 2>(p, stream);
-    return bf16 ? launch_norm<true, 4>(p, stream) : launch_norm<false, 4>(p, stream);
+        return bf16 ? launch_norm<true, 4, true>(p, stream) : launch_norm<false, 4, true>(p, stream);
+    return bf16 ? launch_norm<true, 4, false>(p, stream) : launch_norm<false, 4, false>(p, stream);
 }
 
 extern "C" moe_status moe_block_norm_backward_workspace_size(int64_t T, int32_t H, size_t *bytes)
