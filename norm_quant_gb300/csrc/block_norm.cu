@@ -29,6 +29,7 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kMaxThreads = 32 * kWarps;
 constexpr int kMaxSlots = 64;
+constexpr int kSums = 5;  // values that are added up over a row together
 constexpr int kRingBytes = 220 * 1024;
 constexpr int kMaxRingWidth = 8192;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -50,9 +51,9 @@ struct NormParams {
     int64_t stall;
 };
 
-struct RingSmem {
+struct alignas(16) RingSmem {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
-    float red[kWarps][2][2][kWarps];  // of each group: two buffers in turn, two sums, a value a warp
+    float red[kWarps / 2][2][kSums][kWarps];  // of each group of several warps: two buffers in turn, a value a warp
 };
 
 template <bool BF16>
@@ -175,7 +176,7 @@ __device__ __forceinline__ void store8(uint8_t *p, const uint4 &v) { *reinterpre
 // A group of warps that share a row.
 struct Group {
     int warps, warp, lane, index;
-    float (*red)[2][kWarps];
+    float (*red)[kSums][kWarps];
     int turn;
 
     // Sums of N <= 2 values over the group, in every thread.  One barrier: two buffers in turn, and a thread that
@@ -205,6 +206,37 @@ struct Group {
         }
         turn ^= 1;
     }
+
+    // Sums of kSums values over the group; the others are zeros.  Lanes share them out while they add up: 9 exchanges
+    // instead of 40, and lane 4 i has the i-th.  Values of warps that the group does not have are 0 in `red`.
+    __device__ __forceinline__ void sum8(float (&v)[8])
+    {
+#pragma unroll
+        for (int n = 4, o = 16; n; n /= 2, o /= 2)
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const bool upper = lane & o;
+                const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        float mine = v[0];
+        mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+        mine += __shfl_xor_sync(0xffffffffu, mine, 1);
+        if (warps > 1) {
+            const int which = lane / 4 < kSums ? lane / 4 : kSums - 1;
+            if (lane % 4 == 0 && lane / 4 < kSums)
+                red[turn][which][warp] = mine;
+            named_barrier_sync(1 + index, 32 * warps);
+            const float4 w = *reinterpret_cast<const float4 *>(&red[turn][which][4 * (lane % 4)]);
+            mine = (w.x + w.y) + (w.z + w.w);
+            mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+            mine += __shfl_xor_sync(0xffffffffu, mine, 1);
+            turn ^= 1;
+        }
+#pragma unroll
+        for (int i = 0; i < kSums; ++i)
+            v[i] = __shfl_sync(0xffffffffu, mine, 4 * i);
+    }
 };
 
 __device__ __forceinline__ void ring_init(const NormParams &p, RingSmem &r)
@@ -216,45 +248,52 @@ __device__ __forceinline__ void ring_init(const NormParams &p, RingSmem &r)
         }
         fence_mbar_init();
     }
+    for (int i = threadIdx.x; i < kWarps / 2 * 2 * kSums * kWarps; i += blockDim.x)
+        (&r.red[0][0][0][0])[i] = 0.0f;
     __syncthreads();
 }
 
 // A group's rows: t, t + step, and so on, each in the next of its slots.
+template <bool BACKWARD>
 struct Rows {
     const NormParams &p;
-    uint8_t *at;  // the slot of the row that is being worked on
-    uint32_t full, empty;
-    uint32_t t, step, fills;  // rows are below 2^31; fills: copies that may still be issued
+    uint32_t ring, full;  // the group's slots and barriers, in shared memory
+    uint32_t t;           // the row that is being worked on (rows are below 2^31), its slot and the phase of that one's barriers
     int slot;
-    uint32_t phase, bytes;
-    bool issues, backward, lost;
+    uint32_t phase;
+    uint32_t fills;       // copies that this thread may still issue: 0 in all threads but one
+    bool lost;
 
-    __device__ __forceinline__ Rows(const NormParams &q, RingSmem &r, uint8_t *ring, const Group &g, bool back)
-        : p(q), at(ring + static_cast<uint32_t>(g.index * q.slots) * q.stage), full(smem_u32(&r.full[g.index * q.slots])),
-          empty(smem_u32(&r.empty[g.index * q.slots])), t(blockIdx.x + g.index * gridDim.x), step(q.groups * gridDim.x),
-          slot(0), phase(0), issues(g.warp == 0 && g.lane == 0), backward(back),
-          lost(false)
+    __device__ __forceinline__ Rows(const NormParams &q, RingSmem &r, const uint8_t *slots, const Group &g)
+        : p(q), ring(smem_u32(slots) + static_cast<uint32_t>(g.index * q.slots * q.stage)), full(smem_u32(&r.full[g.index * q.slots])),
+          t(blockIdx.x + g.index * gridDim.x), slot(0), phase(0), fills(0), lost(false)
     {
-        bytes = 2u * static_cast<uint32_t>(q.H) * (1u + (q.residual != nullptr) + (back && q.d_norm_out) + (back && q.d_residual_out));
-        fills = blockIdx.x == 0 && g.index == 0 && q.stall >= 0 && q.stall < 0xFFFFFFFF ? static_cast<uint32_t>(q.stall) : 0xFFFFFFFFu;  // test hook (moe_debug_stall)
-        for (int i = 0; issues && i < q.slots; ++i)
-            fill(t + i * step, i, at + static_cast<uint32_t>(i) * q.stage);
+        if (g.warp == 0 && g.lane == 0) {
+            // test hook (moe_debug_stall)
+            fills = blockIdx.x == 0 && g.index == 0 && q.stall >= 0 && q.stall < 0xFFFFFFFF ? static_cast<uint32_t>(q.stall) : 0xFFFFFFFFu;
+            for (int i = 0; i < q.slots; ++i)
+                fill(t + i * step(), i);
+        }
     }
 
-    __device__ __forceinline__ void fill(uint32_t row, int to, const uint8_t *place)
+    __device__ __forceinline__ uint32_t step() const { return p.groups * gridDim.x; }
+    __device__ __forceinline__ uint32_t empty(int i) const { return full + static_cast<uint32_t>(sizeof(RingSmem::full)) + 8u * i; }
+
+    __device__ __forceinline__ void fill(uint32_t row, int to)
     {
         if (row >= p.T || fills == 0)
             return;
         --fills;
-        const uint32_t row_bytes = 2u * static_cast<uint32_t>(p.H), dst = smem_u32(place), bar = full + 8u * to;
+        const uint32_t row_bytes = 2u * static_cast<uint32_t>(p.H), dst = ring + to * p.stage, bar = full + 8u * to;
         const int64_t from = static_cast<int64_t>(row) * row_bytes;
-        mbar_arrive_expect_tx(bar, bytes);
+        const bool dn = BACKWARD && p.d_norm_out, dr = BACKWARD && p.d_residual_out;
+        mbar_arrive_expect_tx(bar, row_bytes * (1u + (p.residual != nullptr) + dn + dr));
         bulk_g2s(dst, p.y + from, row_bytes, bar);
         if (p.residual)
             bulk_g2s(dst + p.at_residual, p.residual + from, row_bytes, bar);
-        if (backward && p.d_norm_out)
+        if (dn)
             bulk_g2s(dst + p.at_d_norm, p.d_norm_out + from, row_bytes, bar);
-        if (backward && p.d_residual_out)
+        if (dr)
             bulk_g2s(dst + p.at_d_residual, p.d_residual_out + from, row_bytes, bar);
     }
 
@@ -265,31 +304,37 @@ struct Rows {
         return lost ? __int_as_float(0x7FC00000) : 0.0f;
     }
 
+    // 16 bytes of the row.
+    __device__ __forceinline__ uint4 read(int at) const
+    {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ring + slot * p.stage + at));
+        return v;
+    }
+
     // The row's slot has been read: the row that comes next into it.
-    __device__ __forceinline__ void release(int lane)
+    __device__ __forceinline__ void release(const Group &g)
     {
         __syncwarp();
-        if (lane == 0)
-            mbar_arrive(empty + 8u * slot);
-        if (issues && !lost && t + p.slots * step < p.T) {
-            if (mbar_wait_bounded(empty + 8u * slot, phase, kWaitLimitNs))
-                fill(t + p.slots * step, slot, at);
+        if (g.lane == 0)
+            mbar_arrive(empty(slot));
+        if (fills && !lost && t + p.slots * step() < p.T) {
+            if (mbar_wait_bounded(empty(slot), phase, kWaitLimitNs))
+                fill(t + p.slots * step(), slot);
             else
                 fills = 0;
         }
-        t += step;
-        at += p.stage;
+        t += step();
         if (++slot == p.slots) {
             slot = 0;
             phase ^= 1;
-            at -= static_cast<uint32_t>(p.slots) * p.stage;
         }
     }
 
     // Copies that were never waited for land before the CTA leaves.
-    __device__ __forceinline__ void finish()
+    __device__ __forceinline__ void finish(const Group &g)
     {
-        if (!issues || !lost)
+        if (g.warp != 0 || g.lane != 0 || !lost)
             return;
         const uint64_t t0 = globaltimer_ns();
         for (int i = 0; i < p.slots; ++i)
@@ -309,8 +354,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormParams p
     float *factors = reinterpret_cast<float *>(ring + p.slots * p.groups * p.stage);
     ring_init(p, r);
     grid_dependency_wait();
-    Group g{p.group_warps, warp % p.group_warps, lane, warp / p.group_warps, r.red[warp / p.group_warps], 0};
-    Rows rows(p, r, ring, g, false);
+    Group g{p.group_warps, warp % p.group_warps, lane, warp / p.group_warps, r.red[warp / p.group_warps % (kWarps / 2)], 0};
+    Rows<false> rows(p, r, ring, g);
     const int vectors = p.H / 8, threads = 32 * g.warps, first = 32 * g.warp + lane;
     if constexpr (FACTORS) {
         fill_factors<BF16>(p, factors);
@@ -332,14 +377,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormParams p
     };
     while (rows.t < p.T) {
         const float lost = rows.wait();
-        const uint8_t *at = rows.at;
         const int64_t t = rows.t, row = 2 * t * p.H;
         uint64_t s[VPT][4], acc = both(0.0f);
         float ry = 1.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = first + j * threads;
-            pairs8<BF16>(s[j], i < vectors ? *reinterpret_cast<const uint4 *>(at + 16 * i) : make_uint4(0, 0, 0, 0));
+            pairs8<BF16>(s[j], i < vectors ? rows.read(16 * i) : make_uint4(0, 0, 0, 0));
         }
         if (p.post) {
 #pragma unroll
@@ -361,7 +405,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormParams p
             uint64_t c[4], res[4];
             factor(c, i, false);
             if (p.residual) {
-                pairs8<BF16>(res, *reinterpret_cast<const uint4 *>(at + p.at_residual + 16 * i));
+                pairs8<BF16>(res, rows.read(p.at_residual + 16 * i));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     s[j][k] = fma2(s[j][k], mul2(scale, c[k]), mul2(from_residual, res[k]));
@@ -374,7 +418,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormParams p
             for (int k = 0; k < 4; ++k)
                 acc = fma2(s[j][k], s[j][k], acc);
         }
-        rows.release(lane);
+        rows.release(g);
         if (p.residual_out) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
@@ -399,7 +443,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormParams p
             store8(p.norm_out + row + 16 * i, pack_pairs<BF16>(s[j]));
         }
     }
-    rows.finish();
+    rows.finish(g);
     allow_dependent_launch();
 }
 
@@ -413,8 +457,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     float *factors = reinterpret_cast<float *>(ring + p.slots * p.groups * p.stage);
     ring_init(p, r);
     grid_dependency_wait();
-    Group g{p.group_warps, warp % p.group_warps, lane, warp / p.group_warps, r.red[warp / p.group_warps], 0};
-    Rows rows(p, r, ring, g, true);
+    Group g{p.group_warps, warp % p.group_warps, lane, warp / p.group_warps, r.red[warp / p.group_warps % (kWarps / 2)], 0};
+    Rows<true> rows(p, r, ring, g);
     const int vectors = p.H / 8, threads = 32 * g.warps, first = 32 * g.warp + lane, half = p.H / 2;
     fill_factors<BF16>(p, factors);
     __syncthreads();
@@ -426,14 +470,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
             A[j][k] = B[j][k] = both(0.0f);
     while (rows.t < p.T) {
         const float lost = rows.wait();
-        const uint8_t *at = rows.at;
-        const int64_t t = rows.t, row = 2 * t * p.H;
-        uint64_t y[VPT][4], s[VPT][4], d[VPT][4], acc = both(0.0f), acc2 = both(0.0f);
+        const uint32_t t = rows.t;
+        uint64_t y[VPT][4], s[VPT][4], acc = both(0.0f);
+        uint4 d[VPT], dr[VPT];
         float ry = 1.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = first + j * threads;
-            pairs8<BF16>(y[j], i < vectors ? *reinterpret_cast<const uint4 *>(at + 16 * i) : make_uint4(0, 0, 0, 0));
+            pairs8<BF16>(y[j], i < vectors ? rows.read(16 * i) : make_uint4(0, 0, 0, 0));
         }
         if (p.post) {
 #pragma unroll
@@ -446,104 +490,104 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
             ry = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
         }
         const float token = ry * token_gate(p, t) + lost;  // the token's gate over rms(y)
-        const uint64_t scale = both(token), from_residual = both(p.residual_scale);
-        float rs = 0.0f, back = lost;  // back: mean(v m) / rms(s)^2
-        if (p.d_norm_out) {
-            acc = both(0.0f);
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = first + j * threads;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    s[j][k] = d[j][k] = both(0.0f);
-                if (i >= vectors)
-                    continue;
-                uint64_t c[4], res[4];
-                Factors::read(c, factors, i, half);
-                if (p.residual) {
-                    pairs8<BF16>(res, *reinterpret_cast<const uint4 *>(at + p.at_residual + 16 * i));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        s[j][k] = fma2(y[j][k], mul2(scale, c[k]), mul2(from_residual, res[k]));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        s[j][k] = mul2(y[j][k], mul2(scale, c[k]));
-                }
-                pairs8<BF16>(d[j], *reinterpret_cast<const uint4 *>(at + p.at_d_norm + 16 * i));
-                Factors::read(c, factors + p.H, i, half);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc = fma2(s[j][k], s[j][k], acc);
-                    acc2 = fma2(s[j][k], mul2(d[j][k], c[k]), acc2);
-                }
-            }
-            float sum[2] = {total(acc), total(acc2)};
-            g.sum(sum);
-            rs = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
-            back = sum[1] * p.inv_h * rs * rs * rs;
-        }
-        // s becomes ds
-        acc = both(0.0f);
-        const uint64_t rs2 = both(rs), back2 = both(-back);
+        const uint64_t scale = both(token);
+        // with e = c y and v = d (pre_gamma + bias): the sums of s s, s v, and of dr e, v e and s e, of which that of ds e is made
+        uint64_t ss = both(0.0f), sv = ss, re = ss, ve = ss, se = ss;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = first + j * threads;
+            d[j] = dr[j] = make_uint4(0, 0, 0, 0);
             if (i >= vectors)
                 continue;
-            uint64_t c[4], dr[4];
-            pairs8<BF16>(dr, p.d_residual_out ? *reinterpret_cast<const uint4 *>(at + p.at_d_residual + 16 * i) : make_uint4(0, 0, 0, 0));
-            if (p.d_norm_out) {
-                Factors::read(c, factors + p.H, i, half);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    d[j][k] = mul2(d[j][k], rs2);
-                    B[j][k] = fma2(d[j][k], s[j][k], B[j][k]);
-                    s[j][k] = fma2(d[j][k], c[k], fma2(back2, s[j][k], dr[k]));
-                }
-            } else {
-                const uint64_t add = both(lost);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    s[j][k] = fma2(dr[k], both(1.0f), add);
-            }
+            uint64_t c[4], e[4], v[4];
             Factors::read(c, factors, i, half);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint64_t e = mul2(s[j][k], y[j][k]);
-                acc = fma2(e, c[k], acc);
-                A[j][k] = fma2(e, scale, A[j][k]);
+                e[k] = mul2(c[k], y[j][k]);
+                s[j][k] = mul2(e[k], scale);
+            }
+            if (p.residual) {
+                pairs8<BF16>(v, rows.read(p.at_residual + 16 * i));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[j][k] = fma2(v[k], both(p.residual_scale), s[j][k]);
+            }
+            if (p.d_residual_out) {
+                dr[j] = rows.read(p.at_d_residual + 16 * i);
+                pairs8<BF16>(v, dr[j]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    re = fma2(v[k], e[k], re);
+            }
+            if (p.d_norm_out) {
+                d[j] = rows.read(p.at_d_norm + 16 * i);
+                pairs8<BF16>(v, d[j]);
+                Factors::read(c, factors + p.H, i, half);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = mul2(v[k], c[k]);
+                    ss = fma2(s[j][k], s[j][k], ss);
+                    sv = fma2(s[j][k], v[k], sv);
+                    ve = fma2(v[k], e[k], ve);
+                    se = fma2(s[j][k], e[k], se);
+                }
             }
         }
-        rows.release(lane);
-        float dot[1] = {total(acc)};
-        if (p.post || p.gate_kind == MOE_GATE_TOKEN)
-            g.sum(dot);
+        rows.release(g);
+        float rs = 0.0f, back = 0.0f, dot = 0.0f;  // 1 / rms(s), mean(v m) / rms(s)^2, the sum of c ds y
+        if (p.d_norm_out) {
+            float sum[8] = {total(ss), total(sv), total(re), total(ve), total(se), 0.0f, 0.0f, 0.0f};
+            g.sum8(sum);
+            rs = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
+            back = sum[1] * p.inv_h * rs * rs * rs;
+            dot = sum[2] + rs * sum[3] - back * sum[4];
+        } else if (p.post || p.gate_kind == MOE_GATE_TOKEN) {
+            float sum[1] = {total(re)};
+            g.sum(sum);
+            dot = sum[0];
+        }
         if (p.d_gate && p.gate_kind == MOE_GATE_TOKEN && g.warp == 0 && lane == 0)
-            p.d_gate[t] = dot[0] * ry;
-        const uint64_t pull = both(p.post ? -dot[0] * p.inv_h * token * ry * ry : 0.0f);  // - mean(c ds n) / rms(y)^2
+            p.d_gate[t] = dot * ry;
+        const uint64_t pull = both(p.post ? -dot * p.inv_h * token * ry * ry : 0.0f);  // - mean(c ds n) / rms(y)^2
+        const uint64_t rs2 = both(rs), back2 = both(lost - back);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = first + j * threads;
             if (i >= vectors)
                 continue;
-            if (p.d_y) {
-                uint64_t c[4];
-                Factors::read(c, factors, i, half);
+            uint64_t c[4], ds[4];
+            pairs8<BF16>(ds, dr[j]);
+            if (p.d_norm_out) {
+                uint64_t v[4];
+                pairs8<BF16>(v, d[j]);
+                Factors::read(c, factors + p.H, i, half);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = mul2(v[k], rs2);
+                    B[j][k] = fma2(v[k], s[j][k], B[j][k]);
+                    ds[k] = fma2(v[k], c[k], fma2(back2, s[j][k], ds[k]));
+                }
+            } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    c[k] = fma2(mul2(scale, c[k]), s[j][k], mul2(pull, y[j][k]));
-                store8(p.d_y + row + 16 * i, pack_pairs<BF16>(c));
+                    ds[k] = fma2(back2, s[j][k], ds[k]);  // back is 0, or NaN for a lost row
             }
-            if (p.d_residual) {
+            Factors::read(c, factors, i, half);
+            uint64_t out[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    s[j][k] = mul2(from_residual, s[j][k]);
-                store8(p.d_residual + row + 16 * i, pack_pairs<BF16>(s[j]));
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t f = mul2(ds[k], scale);
+                A[j][k] = fma2(f, y[j][k], A[j][k]);
+                out[k] = fma2(f, c[k], mul2(pull, y[j][k]));
+                ds[k] = mul2(both(p.residual_scale), ds[k]);
             }
+            if (p.d_y)
+                store8(p.d_y + 2 * static_cast<int64_t>(t) * p.H + 16 * i, pack_pairs<BF16>(out));
+            if (p.d_residual)
+                store8(p.d_residual + 2 * static_cast<int64_t>(t) * p.H + 16 * i, pack_pairs<BF16>(ds));
         }
     }
-    rows.finish();
+    rows.finish(g);
     if (p.partial) {
         // the groups' sums, added up in their order in the ring's memory
         float *sums = reinterpret_cast<float *>(ring);  // [2, H]
@@ -588,7 +632,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_wide_kernel(cons
 {
     constexpr int VPT = MOE_MAX_HIDDEN / 8 / kMaxThreads;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float red[2][2][kWarps];
+    __shared__ float red[2][kSums][kWarps];
     float *A = reinterpret_cast<float *>(ring), *B = A + p.H;
     grid_dependency_wait();
     const int vectors = p.H / 8;
