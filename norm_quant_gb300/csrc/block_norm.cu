@@ -645,138 +645,167 @@ __global__ void __launch_bounds__(2 * kMaxThreads / VPT, 1) norm_backward_kernel
     allow_dependent_launch();
 }
 
-// The backward pass of wider rows: a row at a time in registers, A and B in shared memory.
+// The backward pass of wider rows: a row at a time in registers as it is in memory, A and B in shared memory in the order of
+// Factors.
 template <bool BF16>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_wide_kernel(const NormParams p)
 {
     constexpr int VPT = MOE_MAX_HIDDEN / 8 / kMaxThreads;
-    extern __shared__ __align__(128) uint8_t ring[];
+    extern __shared__ __align__(128) uint8_t dynamic[];
     __shared__ float red[2][kSums][kWarps];
-    float *A = reinterpret_cast<float *>(ring), *B = A + p.H;
+    float *A = reinterpret_cast<float *>(dynamic), *B = A + p.H;
     grid_dependency_wait();
-    const int vectors = p.H / 8;
-    Group g{kMaxThreads / 32, static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31), 0, red, 0};
-    for (int i = threadIdx.x; p.partial && i < vectors; i += kMaxThreads)
-        for (int k = 0; k < 8; ++k)
-            A[8 * i + k] = B[8 * i + k] = 0.0f;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const int64_t row = 2 * t * p.H;
-        uint4 y[VPT], r[VPT], d[VPT];
+    const int vectors = p.H / 8, half = p.H / 2;
+    Group g{kWarps, static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31), 0, red, 0};
+    for (int i = threadIdx.x; p.partial && i < 2 * p.H; i += kMaxThreads)
+        A[i] = 0.0f;
+    __syncthreads();
+    const auto factors = [&](uint64_t (&c)[4], int i, bool pre) {
+        float v[8];
+        if (pre)
+            gammas8<BF16>(v, true, ldg16(p.pre + 16 * i), p.bias);
+        else
+            factors8<BF16>(v, p, vector_of(p.post, i, p.post), vector_of(p.gate, i, p.gate_kind == MOE_GATE_CHANNEL));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            c[k] = pair_of(v[2 * k], v[2 * k + 1]);
+    };
+    const auto add = [&](float *to, int i, const uint64_t (&v)[4]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float4 *at = reinterpret_cast<float4 *>(to + k * half + 4 * i);
+            float4 a = *at, b;
+            split(v[2 * k], b.x, b.y);
+            split(v[2 * k + 1], b.z, b.w);
+            *at = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        }
+    };
+    for (uint32_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const int64_t row = 2 * static_cast<int64_t>(t) * p.H;
+        uint4 y[VPT], r[VPT], d[VPT], dr[VPT];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = threadIdx.x + j * kMaxThreads;
-            y[j] = r[j] = d[j] = make_uint4(0, 0, 0, 0);
+            const int64_t at = row + 16 * i;
+            y[j] = r[j] = d[j] = dr[j] = make_uint4(0, 0, 0, 0);
             if (i < vectors) {
-                y[j] = *reinterpret_cast<const uint4 *>(p.y + row + 16 * i);
+                y[j] = *reinterpret_cast<const uint4 *>(p.y + at);
                 if (p.residual)
-                    r[j] = *reinterpret_cast<const uint4 *>(p.residual + row + 16 * i);
+                    r[j] = *reinterpret_cast<const uint4 *>(p.residual + at);
                 if (p.d_norm_out)
-                    d[j] = *reinterpret_cast<const uint4 *>(p.d_norm_out + row + 16 * i);
+                    d[j] = *reinterpret_cast<const uint4 *>(p.d_norm_out + at);
+                if (p.d_residual_out)
+                    dr[j] = *reinterpret_cast<const uint4 *>(p.d_residual_out + at);
             }
         }
         float ry = 1.0f;
         if (p.post) {
-            float sum[1] = {0.0f};
+            uint64_t acc = both(0.0f);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                float v[8];
-                unpack8<BF16>(y[j], v);
+                uint64_t v[4];
+                pairs8<BF16>(v, y[j]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    sum[0] = fmaf(v[k], v[k], sum[0]);
+                for (int k = 0; k < 4; ++k)
+                    acc = fma2(v[k], v[k], acc);
             }
+            float sum[1] = {total(acc)};
             g.sum(sum);
             ry = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
         }
-        const float token = token_gate(p, t);
-        const auto new_residual = [&](int j, int i, float (&a)[8], float (&c)[8], float (&s)[8]) {
-            unpack8<BF16>(y[j], a);
-            unpack8<BF16>(r[j], s);
-            factors8<BF16>(c, p, vector_of(p.post, i, p.post), vector_of(p.gate, i, p.gate_kind == MOE_GATE_CHANNEL));
+        const float token = ry * token_gate(p, t);
+        const uint64_t scale = both(token), from_residual = both(p.residual_scale);
+        // e = c y and s of a vector
+        const auto parts = [&](int j, int i, uint64_t (&e)[4], uint64_t (&s)[4]) {
+            uint64_t v[4];
+            factors(e, i, false);
+            pairs8<BF16>(v, y[j]);
+            pairs8<BF16>(s, r[j]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                s[k] = fmaf(a[k], token * ry * c[k], p.residual ? p.residual_scale * s[k] : 0.0f);
-        };
-        float sum[2] = {0.0f, 0.0f}, rs = 0.0f, back = 0.0f;
-        if (p.d_norm_out) {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = threadIdx.x + j * kMaxThreads;
-                if (i >= vectors)
-                    continue;
-                float a[8], c[8], s[8], v[8];
-                new_residual(j, i, a, c, s);
-                unpack8<BF16>(d[j], v);
-                gammas8<BF16>(c, true, ldg16(p.pre + 16 * i), p.bias);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    sum[0] = fmaf(s[k], s[k], sum[0]);
-                    sum[1] = fmaf(s[k], v[k] * c[k], sum[1]);
-                }
-            }
-            g.sum(sum);
-            rs = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
-            back = sum[1] * p.inv_h * rs * rs * rs;
-        }
-        // ds of a vector, and what of it adds to A and B
-        const auto gradient = [&](int j, int i, float (&a)[8], float (&c)[8], float (&ds)[8], bool add) {
-            float s[8], v[8], c2[8];
-            new_residual(j, i, a, c, s);
-            unpack8<BF16>(d[j], v);
-            const uint4 direct = p.d_residual_out ? *reinterpret_cast<const uint4 *>(p.d_residual_out + row + 16 * i) : make_uint4(0, 0, 0, 0);
-            unpack8<BF16>(direct, ds);
-            gammas8<BF16>(c2, true, vector_of(p.pre, i, p.pre), p.bias);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                ds[k] = fmaf(rs, v[k] * c2[k], fmaf(-back, s[k], ds[k]));
-                if (add) {
-                    A[8 * i + k] = fmaf(ds[k], a[k] * (ry * token), A[8 * i + k]);
-                    B[8 * i + k] = fmaf(v[k], s[k] * rs, B[8 * i + k]);
-                }
+            for (int k = 0; k < 4; ++k) {
+                e[k] = mul2(e[k], v[k]);
+                s[k] = fma2(e[k], scale, mul2(from_residual, s[k]));
             }
         };
-        float dot[1] = {0.0f};
-        if (p.post || p.gate_kind == MOE_GATE_TOKEN) {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = threadIdx.x + j * kMaxThreads;
-                if (i >= vectors)
-                    continue;
-                float a[8], c[8], ds[8];
-                gradient(j, i, a, c, ds, false);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    dot[0] = fmaf(ds[k], c[k] * a[k], dot[0]);
-            }
-            g.sum(dot);
-        }
-        if (p.d_gate && p.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0)
-            p.d_gate[t] = dot[0] * ry;
-        const float pull = p.post ? dot[0] * p.inv_h * token * ry * ry * ry : 0.0f;
+        uint64_t ss = both(0.0f), sv = ss, re = ss, ve = ss, se = ss;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int i = threadIdx.x + j * kMaxThreads;
             if (i >= vectors)
                 continue;
-            float a[8], c[8], ds[8];
-            gradient(j, i, a, c, ds, p.partial != nullptr);
-            if (p.d_y) {
+            uint64_t e[4], s[4], v[4], c[4];
+            parts(j, i, e, s);
+            pairs8<BF16>(v, dr[j]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    c[k] = fmaf(ry * token, c[k] * ds[k], -pull * a[k]);
-                store8(p.d_y + row + 16 * i, pack8<BF16>(c));
-            }
-            if (p.d_residual) {
+            for (int k = 0; k < 4; ++k)
+                re = fma2(v[k], e[k], re);
+            if (!p.d_norm_out)
+                continue;
+            pairs8<BF16>(v, d[j]);
+            factors(c, i, true);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    ds[k] *= p.residual_scale;
-                store8(p.d_residual + row + 16 * i, pack8<BF16>(ds));
+            for (int k = 0; k < 4; ++k) {
+                v[k] = mul2(v[k], c[k]);
+                ss = fma2(s[k], s[k], ss);
+                sv = fma2(s[k], v[k], sv);
+                ve = fma2(v[k], e[k], ve);
+                se = fma2(s[k], e[k], se);
             }
+        }
+        float sum[8] = {total(ss), total(sv), total(re), total(ve), total(se), 0.0f, 0.0f, 0.0f};
+        g.sum8(sum);
+        float rs = 0.0f, back = 0.0f;
+        if (p.d_norm_out) {
+            rs = rsqrt_newton(fmaf(sum[0], p.inv_h, p.eps));
+            back = sum[1] * p.inv_h * rs * rs * rs;
+        }
+        const float dot = p.d_norm_out ? sum[2] + rs * sum[3] - back * sum[4] : sum[2];
+        if (p.d_gate && p.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0)
+            p.d_gate[t] = dot * ry;
+        const uint64_t pull = both(p.post ? -dot * p.inv_h * token * ry * ry : 0.0f), rs2 = both(rs), back2 = both(-back);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = threadIdx.x + j * kMaxThreads;
+            if (i >= vectors)
+                continue;
+            uint64_t e[4], s[4], v[4], c[4], ds[4];
+            parts(j, i, e, s);
+            pairs8<BF16>(ds, dr[j]);
+            if (p.d_norm_out) {
+                pairs8<BF16>(v, d[j]);
+                factors(c, i, true);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = mul2(v[k], rs2);
+                    ds[k] = fma2(v[k], c[k], fma2(back2, s[k], ds[k]));
+                    v[k] = mul2(v[k], s[k]);
+                }
+                if (p.partial)
+                    add(B, i, v);
+            }
+            factors(c, i, false);
+            pairs8<BF16>(v, y[j]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                e[k] = mul2(ds[k], scale);
+                c[k] = fma2(e[k], c[k], mul2(pull, v[k]));
+                v[k] = mul2(e[k], v[k]);
+                ds[k] = mul2(from_residual, ds[k]);
+            }
+            if (p.partial)
+                add(A, i, v);
+            if (p.d_y)
+                store8(p.d_y + row + 16 * i, pack_pairs<BF16>(c));
+            if (p.d_residual)
+                store8(p.d_residual + row + 16 * i, pack_pairs<BF16>(ds));
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; p.partial && i < 2 * p.H; i += kMaxThreads)
-        p.partial[static_cast<int64_t>(blockIdx.x) * 2 * p.H + i] = A[i];
+    float *out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.H;
+    for (int i = threadIdx.x; p.partial && i < 2 * p.H; i += kMaxThreads) {
+        const int h = i < p.H ? i : i - p.H;
+        out[i] = A[i - h + (h / 4 % 2) * half + h / 8 * 4 + h % 4];
+    }
     allow_dependent_launch();
 }
 
