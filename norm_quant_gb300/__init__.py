@@ -565,8 +565,14 @@ _CODES = {C.c_int64: "q", C.c_int32: "i", C.c_float: "f", C.c_void_p: "P", C.c_s
 _PACK = {name: struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0q") for name, cls in _BLOCK_ARGS.items()}
 
 
+_calls = {}  # name -> (the library's function, the packer of its argument)
+
+
 def _call(name: str, fields, stream, t) -> None:
-    st = getattr(lib(), name)(_PACK[name].pack(*fields), _stream_of(stream, t))
+    fn = _calls.get(name)
+    if fn is None:
+        fn = _calls[name] = getattr(lib(), name), _PACK[name].pack
+    st = fn[0](fn[1](*fields), _stream_of(stream, t))
     if st:
         raise MoeError(st, name)
 

@@ -809,30 +809,36 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_wide_kernel(cons
     allow_dependent_launch();
 }
 
-// A and B over the CTAs, and the gradients that they make: 32 columns a block, 8 threads for each.
+// A and B over the CTAs, and the gradients that they make: 32 columns a block.  A warp adds up every 32nd CTA's, so that a
+// thread has a handful of loads in flight at once, and then the 32 sums of one column.
 template <bool BF16>
-__global__ void __launch_bounds__(256) column_sums_kernel(const NormParams p)
+__global__ void __launch_bounds__(1024) column_sums_kernel(const NormParams p)
 {
-    __shared__ float part[2][8][32];
+    __shared__ float part[2][32][33];
+    const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
     grid_dependency_wait();
-    const int column = threadIdx.x & 31, share = threadIdx.x >> 5, h = blockIdx.x * 32 + column;
+    int h = blockIdx.x * 32 + lane;
     float a = 0.0f, b = 0.0f;
     if (h < p.H) {
-#pragma unroll 4
-        for (int i = share; i < p.ctas; i += 8) {
+#pragma unroll 8
+        for (int i = share; i < p.ctas; i += 32) {
             const float *at = p.partial + static_cast<int64_t>(i) * 2 * p.H + h;
-            a += at[0];
-            b += at[p.H];
+            a += __ldg(at);
+            b += __ldg(at + p.H);
         }
     }
-    part[0][share][column] = a;
-    part[1][share][column] = b;
+    part[0][share][lane] = a;
+    part[1][share][lane] = b;
     __syncthreads();
-    if (share == 0 && h < p.H) {
-        for (int i = 1; i < 8; ++i) {
-            a += part[0][i][column];
-            b += part[1][i][column];
-        }
+    a = part[0][lane][share];
+    b = part[1][lane][share];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    h = blockIdx.x * 32 + share;
+    if (lane == 0 && h < p.H) {
         float gate = p.block_scale, post = p.block_scale, lo, hi;
         if (p.gate_kind == MOE_GATE_CHANNEL) {
             unpack2<BF16>(reinterpret_cast<const uint16_t *>(p.gate)[h], lo, hi);
@@ -959,7 +965,7 @@ moe_status launch_backward(NormParams &p, moe_stream_t stream)
     const moe_status st = PdlLaunch(static_cast<unsigned>(p.ctas), threads, smem, stream).run(kern, p);
     if (st != MOE_OK || !p.partial)
         return st;
-    return PdlLaunch(static_cast<unsigned>((p.H + 31) / 32), 256, 0, stream).run(column_sums_kernel<BF16>, p);
+    return PdlLaunch(static_cast<unsigned>((p.H + 31) / 32), 1024, 0, stream).run(column_sums_kernel<BF16>, p);
 }
 
 moe_status zero_floats(float *at, int64_t n, moe_stream_t stream)
