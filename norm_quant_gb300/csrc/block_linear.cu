@@ -45,7 +45,6 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const GateGradParams p)
         *reinterpret_cast<uint4 *>(out) = pack8<BF16>(dg);
         *reinterpret_cast<uint4 *>(out + half) = pack8<BF16>(du);
     }
-    allow_dependent_launch();
 }
 
 template <bool BF16, int ACT>

@@ -156,15 +156,31 @@ struct Factors {
 template <bool BF16>
 __device__ __forceinline__ void fill_factors(const NormParams &p, float *c)
 {
-    const int half = p.H / 2;
-    for (int i = threadIdx.x; i < p.H / 8; i += blockDim.x) {
-        float v[8];
-        factors8<BF16>(v, p, vector_of(p.post, i, p.post), vector_of(p.gate, i, p.gate_kind == MOE_GATE_CHANNEL));
-        *reinterpret_cast<float4 *>(c + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4 *>(c + half + 4 * i) = make_float4(v[4], v[5], v[6], v[7]);
-        gammas8<BF16>(v, p.pre != nullptr, vector_of(p.pre, i, p.pre), p.bias);
-        *reinterpret_cast<float4 *>(c + p.H + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4 *>(c + p.H + half + 4 * i) = make_float4(v[4], v[5], v[6], v[7]);
+    constexpr int kAtOnce = 4;  // vectors whose loads are in flight together
+    const int half = p.H / 2, vectors = p.H / 8;
+    for (int base = threadIdx.x; base < vectors; base += kAtOnce * blockDim.x) {
+        uint4 post[kAtOnce], gate[kAtOnce], pre[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int i = base + j * blockDim.x;
+            const bool in = i < vectors;
+            post[j] = vector_of(p.post, i, in && p.post);
+            gate[j] = vector_of(p.gate, i, in && p.gate_kind == MOE_GATE_CHANNEL);
+            pre[j] = vector_of(p.pre, i, in && p.pre);
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int i = base + j * blockDim.x;
+            if (i >= vectors)
+                break;
+            float v[8];
+            factors8<BF16>(v, p, post[j], gate[j]);
+            *reinterpret_cast<float4 *>(c + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(c + half + 4 * i) = make_float4(v[4], v[5], v[6], v[7]);
+            gammas8<BF16>(v, p.pre != nullptr, pre[j], p.bias);
+            *reinterpret_cast<float4 *>(c + p.H + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(c + p.H + half + 4 * i) = make_float4(v[4], v[5], v[6], v[7]);
+        }
     }
 }
 
@@ -451,7 +467,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormParams p
         }
     }
     rows.finish(g);
-    allow_dependent_launch();
 }
 
 // ALL: both norms, the residual and both gradients are there, as in training, and nothing has to be asked for them.
@@ -642,7 +657,6 @@ __global__ void __launch_bounds__(2 * kMaxThreads / VPT, 1) norm_backward_kernel
         for (int i = threadIdx.x; i < p.H / 2; i += blockDim.x)
             out[i] = reinterpret_cast<float4 *>(dynamic)[i];
     }
-    allow_dependent_launch();
 }
 
 // The backward pass of wider rows: a row at a time in registers as it is in memory, A and B in shared memory in the order of
@@ -806,7 +820,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_wide_kernel(cons
         const int h = i < p.H ? i : i - p.H;
         out[i] = A[i - h + (h / 4 % 2) * half + h / 8 * 4 + h % 4];
     }
-    allow_dependent_launch();
 }
 
 // A and B over the CTAs, and the gradients that they make: 32 columns a block.  A warp adds up every 32nd CTA's, so that a
@@ -855,7 +868,6 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const NormParams p)
         if (p.d_gate && p.gate_kind == MOE_GATE_CHANNEL)
             p.d_gate[h] = post * a;
     }
-    allow_dependent_launch();
 }
 
 // CTAs of the backward pass whose sums the workspace has room for.

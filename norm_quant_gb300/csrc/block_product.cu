@@ -25,7 +25,6 @@
 
 #include "block.h"
 #include "block_math.cuh"
-#include "few_token.h"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
 
@@ -369,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     if (warp == 2)
         tmem_alloc_pair(base + Layout::tmem, 512);
-    grid_dependency_wait();
     if (warp == 0) {
         if (!read_offsets<KIND != kWeight>(p, first, tile0, lane) && lane == 0 && p.status && blockIdx.x == 0)
             atomicCAS(p.status, 0, MOE_ERR_ROW_OUT_OF_RANGE);
@@ -581,7 +579,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     tcgen05_fence_after();
     if (warp == 2)
         tmem_free_pair(tmem, 512);
-    allow_dependent_launch();
 }
 
 // -------------------------------------------------------------------------------------------------- launch
@@ -647,20 +644,20 @@ moe_status launch(const Product &a, moe_stream_t stream)
         return MOE_ERR_CUDA;
     }
     const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    // an ordinary launch: pairs that were resident before the kernel in front of them had ended were not worth their risk (a
+    // CTA holds all tensor memory of its SM)
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < 1 ? 1 : pairs)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess)
         return MOE_OK;
     cudaGetLastError();
