@@ -26,6 +26,8 @@ struct Product {
     int32_t out_width;    // columns of the result; for kGated I (W has 2 I rows)
     const void *rows;
     int64_t rows_stride;
+    int32_t fold;         // kInput, kWeight: 0, or `rows` is held as a sum: its columns, up to `fold` (a multiple of 64) zeros, what
+                          // they are rounded by, and zeros again
     const void *other;
     int64_t other_stride; // kWeight: elements from row to row of X
     const int32_t *offsets;

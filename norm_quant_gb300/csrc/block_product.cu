@@ -49,7 +49,8 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 struct Params {
     CUtensorMap a, b[kRowBoxes];  // b: of rows in boxes of 16, 32, 64 and 128; the weights' gradient has one
     int64_t n_rows;
-    int32_t E, width, out_width, contraction;  // contraction: 0 for the weights' gradient (an expert's rows)
+    int32_t E, width, out_width;
+    int32_t fold;                              // Product::fold; each step of the contraction is then made twice, once for each part
     int32_t m_tiles, n_tiles, n_columns;       // n_*: the weights' gradient's N side
     int32_t wide_a, wide_b;                    // an operand across comes in boxes of 128 columns (two chunks), not 64
     const int32_t *offsets;
@@ -79,6 +80,9 @@ struct Tile {
     int32_t n;       // columns of the matrix instruction
     int32_t m0, n0;  // first of the 256, first column (weights' gradient)
     int32_t steps;
+
+    // Whether a step of the weights' gradient reads beyond the expert's rows.
+    __device__ bool beyond(int k, int32_t fold) const { return rows % kStep != 0 && k >= steps - (fold ? 2 : 1); }
 };
 
 template <int KIND>
@@ -125,14 +129,14 @@ struct Schedule {
             t.rows = n;
             t.n = p.n_columns;
             t.n0 = static_cast<int32_t>(i) * p.n_columns;
-            t.steps = (n + kStep - 1) / kStep;
+            t.steps = (n + kStep - 1) / kStep * (p.fold ? 2 : 1);
         } else {
             t.n = static_cast<int32_t>((static_cast<uint32_t>(n) + along - 1) / along + 31) / 32 * 32;
             t.row = begin + static_cast<int64_t>(i) * t.n;
             const int64_t rest = begin + n - t.row;
             t.rows = static_cast<int32_t>(rest < t.n ? rest : t.n);
             t.n0 = 0;
-            t.steps = (p.contraction + kStep - 1) / kStep;
+            t.steps = (p.width + kStep - 1) / kStep * (p.fold ? 2 : 1);
         }
         return t;
     }
@@ -406,20 +410,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 }
                 if (!elect_lane())
                     continue;
-                if (KIND == kWeight && k == t.steps - 1 && t.rows % kStep != 0) {
+                if (KIND == kWeight && t.beyond(k, p.fold)) {
                     bar = tail + (a - base) / kStage * 8;  // warp 2 clears what lies behind the rows, and then says that the slot is full
                     mbar_arrive_expect_tx(bar, bytes);
                 } else {
                     mbar_arrive_expect_tx_cluster(bar, bytes);
                 }
-                const int x = k * kStep;
+                const int x = (p.fold ? k / 2 : k) * kStep, part = p.fold && k % 2 ? p.fold : 0;
                 const int32_t row = static_cast<int32_t>(t.row) + (KIND == kWeight ? x : rank * half);
                 if constexpr (KIND == kForward) {
                     tensor_load_pair(a, &p.a, x, t.m0 + rank * kSide, t.e, bar);
                 } else if constexpr (KIND == kGated) {
                     tensor_load_pair(a, &p.a, x, t.m0 + rank * 64, 0, t.e, bar);  // 64 rows of W1 and the same of W3
                 } else {
-                    const int y = KIND == kInput ? x : row, e = KIND == kInput ? t.e : 0, column = t.m0 + rank * kSide;
+                    const int y = KIND == kInput ? x : row, e = KIND == kInput ? t.e : 0, column = t.m0 + rank * kSide + (KIND == kWeight ? part : 0);
                     if (p.wide_a) {
                         tensor_load_pair(a, &p.a, 0, y, column / 64, e, bar);
                     } else {
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
                     for (int i = kRowBoxes - 1; i >= 0; --i)
                         if (half & (16 << i)) {
-                            tensor_load_pair(b + at * kLine, &p.b[i], x, row + at, 0, bar);
+                            tensor_load_pair(b + at * kLine, &p.b[i], x + part, row + at, 0, bar);
                             at += 16 << i;
                         }
                 }
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             tcgen05_fence_after();
             for (int k = 0; k < t.steps && good; ++k) {
                 // an acquire for the pair, which costs the most of a microsecond, is for the lines that warp 2 has cleared alone
-                good = KIND == kWeight && k == t.steps - 1 && t.rows % kStep != 0
+                good = KIND == kWeight && t.beyond(k, p.fold)
                            ? __all_sync(0xffffffffu, mbar_wait_cluster_bounded(full + 8 * slot, phase, kWaitLimitNs))
                            : warp_wait(full + 8 * slot, phase);
                 if (!good)
@@ -521,9 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const Tile t = plan.at(q);
             if (t.steps == 0)
                 continue;
-            slot = static_cast<uint32_t>((slot + t.steps - 1) % kStages);
-            const int rest = t.rows % kStep;
-            if (rest != 0) {
+            const int rest = t.rows % kStep, last = rest != 0 ? (p.fold ? 2 : 1) : 0;  // steps of the tile that read beyond
+            slot = static_cast<uint32_t>((slot + t.steps - last) % kStages);
+            for (int i = 0; i < last && good; ++i) {
                 good = mbar_wait_bounded(tail + 8 * slot, (phases >> slot) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
                 good = __all_sync(0xffffffffu, good);
                 if (!good)
@@ -531,14 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 phases ^= 1u << slot;
                 const int chunks = 2 + (t.n / 2 + 63) / 64;
                 for (int c = 0; c < chunks; ++c)
-                    for (int i = 8 * rest + lane; i < 8 * kStep; i += 32)
-                        *reinterpret_cast<uint4 *>(smem + slot * kStage + c * kChunk + 16 * i) = make_uint4(0, 0, 0, 0);
+                    for (int at = 8 * rest + lane; at < 8 * kStep; at += 32)
+                        *reinterpret_cast<uint4 *>(smem + slot * kStage + c * kChunk + 16 * at) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_release_cluster(full_of_pair + 8 * slot);
+                slot = (slot + 1) % kStages;
             }
-            slot = (slot + 1) % kStages;
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3, part = warp / 4 - 1;
@@ -595,7 +599,7 @@ moe_status launch(const Product &a, moe_stream_t stream)
     p.E = a.E;
     p.width = a.width;
     p.out_width = a.out_width;
-    p.contraction = KIND == kWeight ? 0 : a.width;
+    p.fold = a.fold;
     p.offsets = a.offsets;
     p.out = static_cast<uint8_t *>(a.out);
     p.out_stride = a.out_stride;
@@ -614,7 +618,7 @@ moe_status launch(const Product &a, moe_stream_t stream)
         p.m_tiles = KIND == kGated ? (a.out_width + 127) / 128 : (a.out_width + 255) / 256;
         tiles = (a.n_rows / kMaxN + (a.n_rows < a.E ? a.n_rows : a.E)) * p.m_tiles;
     }
-    const int64_t W = a.width, F = a.out_width;
+    const int64_t W = a.width, F = a.out_width, held = a.fold ? 2 * a.fold : W;  // held: columns of `rows` in memory
     // [rows, columns] across, of `groups` matrices: chunks of 64 columns, two in a box where the columns are whole chunks
     const auto across = [](CUtensorMap &map, const void *at, int64_t columns, int64_t rows, int64_t groups, int64_t stride, bool wide) {
         if (wide)
@@ -632,12 +636,12 @@ moe_status launch(const Product &a, moe_stream_t stream)
         p.wide_a = F % 64 == 0;
         ok = across(p.a, a.other, F, W, a.E, F, p.wide_a);
     } else {
-        p.wide_a = W % 64 == 0;
+        p.wide_a = held % 64 == 0;
         p.wide_b = F % 64 == 0 && p.n_columns == 256;
-        ok = across(p.a, a.rows, W, a.n_rows, 1, a.rows_stride, p.wide_a) && across(p.b[0], a.other, F, a.n_rows, 1, a.other_stride, p.wide_b);
+        ok = across(p.a, a.rows, held, a.n_rows, 1, a.rows_stride, p.wide_a) && across(p.b[0], a.other, F, a.n_rows, 1, a.other_stride, p.wide_b);
     }
     for (int i = 0; KIND != kWeight && i < kRowBoxes; ++i)
-        ok = ok && encode_tensor(p.b[i], a.rows, {3, {W, a.n_rows, 1}, {a.rows_stride, a.rows_stride}, {kStep, 16 << i, 1}});
+        ok = ok && encode_tensor(p.b[i], a.rows, {3, {held, a.n_rows, 1}, {a.rows_stride, a.rows_stride}, {kStep, 16 << i, 1}});
     const size_t smem = static_cast<size_t>(Layout::bytes(a.E));
     if (!ok || sms < 2 || cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limit) != cudaSuccess) {
         cudaGetLastError();

@@ -79,14 +79,22 @@ def weight_grad(dy, dy_err, x, bounds, io, grad):
     return dw, err + 2.0 ** -126 if grad == "fp32" else rounded(dw, err, io)
 
 
+def few(rows, I):
+    """Whether dg and du are held as sums of two 16-bit values."""
+    return rows <= 64 and rows * (I + 56) <= 4096
+
+
 def gate_grad(d_out, gate_up, kind, io):
-    """([dg, du], bound) as the kernel holds them, rounded to the 16-bit type."""
+    """([dg, du], bound) as the kernel holds them: rounded to the 16-bit type, or, where there are few, what is left rounded
+    once more."""
     d, gu = d_out.double(), gate_up.double()
     I = d.shape[1]
     g, u = gu[:, :I], gu[:, I:]
     a, s = act(g, kind), slope(g, kind)
     v = torch.cat((d * u * s, d * a), 1)
     err = 2.0 ** -20 * torch.cat(((d * u).abs() * (1 + g.abs()), d.abs() * (g.abs() + a.abs())), 1)
+    if few(d.shape[0], I):
+        return v, err + U[io] ** 2 * (v.abs() + err) + 2 * TINY[io]
     return v, rounded(v, err, io)
 
 

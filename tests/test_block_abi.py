@@ -48,7 +48,7 @@ def test_gated_linear_refusals(L, kw, want):
 
 GATED_GRAD = dict(rows=4, H=64, I=32, E=2, offsets=0x1000, d_out=0x2000, d_out_stride=32, gate_up=0x3000, gate_up_stride=64,
                   x=0x4000, x_stride=64, w13=0x5000, d_x=0x6000, d_x_stride=64, d_w13=0x7000, workspace=0x8000,
-                  workspace_bytes=512, grad_dtype=1)
+                  workspace_bytes=1024, grad_dtype=1)
 
 
 @pytest.mark.parametrize("kw,want", SHARED + [
@@ -56,7 +56,7 @@ GATED_GRAD = dict(rows=4, H=64, I=32, E=2, offsets=0x1000, d_out=0x2000, d_out_s
     (dict(io_dtype=1, grad_dtype=1), 1), (dict(d_out=None), 1), (dict(gate_up=None), 1), (dict(x=None), 1), (dict(w13=None), 1),
     (dict(d_x=None, d_w13=None), 1), (dict(d_x=0x6008), 1), (dict(d_w13=0x7008), 1), (dict(d_x_stride=56), 1),
     (dict(d_out_stride=24), 1), (dict(gate_up_stride=60), 1), (dict(x_stride=60), 1), (dict(workspace=None), 3),
-    (dict(workspace_bytes=511), 3), (dict(workspace=0x8008), 1), (dict(rows=0, d_w13=None), 0)])
+    (dict(workspace_bytes=1023), 3), (dict(workspace=0x8008), 1), (dict(rows=0, d_w13=None), 0)])
 def test_gated_linear_backward_refusals(L, kw, want):
     assert call(L, "moe_gated_linear_backward", GATED_GRAD, kw) == want
 
@@ -126,6 +126,13 @@ def test_null_arguments(L):
 def test_workspace_sizes(L):
     assert nqg.moe_gated_linear_backward_workspace_size(0, 8) == 0
     assert nqg.moe_gated_linear_backward_workspace_size(100, 24) == 100 * 24 * 4
+    # few values are held as sums of two, each part rounded up to 64 columns
+    assert nqg.moe_gated_linear_backward_workspace_size(4, 32) == 4 * 2 * 64 * 2
+    assert nqg.moe_gated_linear_backward_workspace_size(1, 4040) == 2 * 8128 * 2
+    assert nqg.moe_gated_linear_backward_workspace_size(1, 4048) == 4048 * 4
+    for rows in (1, 2, 16, 64, 65):
+        sizes = [nqg.moe_gated_linear_backward_workspace_size(rows, i) for i in range(8, 8192, 8)]
+        assert all(s <= 4 * rows * i + 65536 for s, i in zip(sizes, range(8, 8192, 8)))
     assert nqg.moe_gated_linear_backward_workspace_size(1 << 30, 65536) == 1 << 48
     n = C.c_size_t(0)
     for rows, inner, want in ((-1, 8, 1), (1, 0, 1), (1, 12, 1), (1, 65544, 2), (1 << 31, 8, 2)):

@@ -76,6 +76,7 @@ GROUPS = {
     "ragged": ([0, 0, 7, 7, 140, 269, 270, 270], 281),
     "before": ([5, 69, 100], 117),
     "none": ([0, 0, 0], 9),
+    "few": ([2, 5, 5, 20], 22),
     "many": ([0] + [3 * (i // 2) + (i % 7) * 0 for i in range(1, 41)], 64),
 }
 SIZES = [(8, 8), (64, 64), (72, 40), (136, 200), (256, 128), (520, 264), (200, 1000)]
@@ -157,7 +158,8 @@ def test_grouped_linear_backward(K, N, name, io):
 @pytest.mark.parametrize("io", ["bf16", "fp16"])
 @pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("name,H,I", [("one", 64, 72), ("ragged", 136, 200), ("before", 72, 40), ("over", 256, 128),
-                                      ("none", 64, 64), ("many", 200, 96)])
+                                      ("none", 64, 64), ("many", 200, 96), ("few", 136, 72),
+                                      ("few", 520, 128), ("few", 64, 8), ("over", 72, 8)])
 def test_gated_linear_backward(name, H, I, kind, io):
     bounds, rows, E = groups_of(name)
     g = gen(H + I + rows)
