@@ -403,3 +403,53 @@ def test_calls_on_two_streams_at_once():
             nqg.moe_grouped_linear(x, w, o, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("E,rows", [(1024, 700), (1024, 5), (300, 2000), (915, 64)])
+def test_many_experts(E, rows):
+    """Most experts empty, and tables of the largest size."""
+    H, I = 72, 40
+    g = gen(E + rows)
+    counts = torch.bincount(torch.randint(0, E, (rows,), generator=g), minlength=E)
+    bounds = [0, *counts.cumsum(0).tolist()]
+    x, w = normal(g, rows, H), normal(g, E, 2 * I, H, std=H ** -0.5)
+    (out, ob), (gu, gb) = ref.gated(x, w, bounds, "silu", "bf16")
+    o, s = Out(rows, I, "bf16"), Out(rows, 2 * I, "bf16")
+    nqg.moe_gated_linear(x.to(DEV), w.to(DEV), o.view, offsets=dev_offsets(bounds), gate_up=s.view)
+    o.check(out, ob, bounds)
+    s.check(gu, gb, bounds)
+    check_linear_backward(bounds, rows, H, 2 * I, "bf16", "bf16")
+
+
+@pytest.mark.parametrize("rows,K,N", [(3, 65536, 16), (5, 16, 65536)])
+def test_widest_matrices(rows, K, N):
+    bounds = [0, rows]
+    g = gen(K)
+    x, w = normal(g, rows, K), normal(g, 1, N, K, std=K ** -0.5)
+    y, bound, _ = ref.product(x, w, bounds, "bf16")
+    o = Out(rows, N, "bf16")
+    nqg.moe_grouped_linear(x.to(DEV), w.to(DEV), o.view)
+    o.check(y, bound, bounds)
+    check_linear_backward(bounds, rows, K, N, "bf16", "fp32")
+
+
+def test_weights_beyond_2_to_the_31_elements():
+    """The last of experts that hold more than 2^31 elements together, forward and backward."""
+    E, N, K, rows = 70, 4096, 8192, 40
+    g = gen(9)
+    tail = normal(g, 1, N, K, std=K ** -0.5)
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device=DEV)
+    w[-1] = tail[0].to(DEV)
+    x, dy = normal(g, rows, K), normal(g, rows, N)
+    bounds = [0] * E + [rows]
+    out = torch.empty((rows, N), dtype=torch.bfloat16, device=DEV)
+    nqg.moe_grouped_linear(x.to(DEV), w, out, offsets=dev_offsets(bounds))
+    y, bound, _ = ref.product(x, tail, [0, rows], "bf16")
+    near(out, y, bound)
+    dx, dw = torch.empty((rows, K), dtype=torch.bfloat16, device=DEV), torch.full_like(w, CANARY)
+    nqg.moe_grouped_linear_backward(dy.to(DEV), x=x.to(DEV), w=w, d_x=dx, d_w=dw, offsets=dev_offsets(bounds))
+    zero = torch.zeros(rows, N, dtype=torch.float64)
+    near(dx, *ref.input_grad(dy.double(), zero, tail, [0, rows], "bf16"))
+    want, bound = ref.weight_grad(dy.double(), zero, x, [0, rows], "bf16", "bf16")
+    near(dw[-1], want[0], bound[0])
+    assert bool((dw[:-1] == 0).all())
