@@ -276,7 +276,7 @@ __device__ __forceinline__ void ring_init(const NormParams &p, RingSmem &r, Grou
 template <bool BACKWARD>
 struct Rows {
     const NormParams &p;
-    uint32_t ring;        // the group's slots in shared memory
+    const uint8_t *ring;  // the group's slots in shared memory
     uint32_t full;        // and their barriers
     uint32_t t;           // the row that is being worked on (rows are below 2^31), its slot and the phase of that one's barriers
     int slot;
@@ -285,7 +285,7 @@ struct Rows {
     static constexpr uint32_t kLost = 2;
 
     __device__ __forceinline__ Rows(const NormParams &q, RingSmem &r, const uint8_t *slots, const Group &g)
-        : p(q), ring(smem_u32(slots) + static_cast<uint32_t>(g.index * q.slots * q.stage)), full(smem_u32(&r.full[g.index * q.slots])),
+        : p(q), ring(slots + g.index * q.slots * q.stage), full(smem_u32(&r.full[g.index * q.slots])),
           t(blockIdx.x + g.index * gridDim.x), slot(0), flags(0), fills(0)
     {
         if (g.warp == 0 && g.lane == 0) {
@@ -304,7 +304,7 @@ struct Rows {
         if (row >= p.T || fills == 0)
             return;
         --fills;
-        const uint32_t row_bytes = 2u * static_cast<uint32_t>(p.H), dst = ring + to * p.stage, bar = full + 8u * to;
+        const uint32_t row_bytes = 2u * static_cast<uint32_t>(p.H), dst = smem_u32(ring + to * p.stage), bar = full + 8u * to;
         const int64_t from = static_cast<int64_t>(row) * row_bytes;
         const bool dn = BACKWARD && p.d_norm_out, dr = BACKWARD && p.d_residual_out;
         mbar_arrive_expect_tx(bar, row_bytes * (1u + (p.residual != nullptr) + dn + dr));
@@ -326,12 +326,7 @@ struct Rows {
     }
 
     // 16 bytes of the row.
-    __device__ __forceinline__ uint4 read(int at) const
-    {
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ring + slot * p.stage + at));
-        return v;
-    }
+    __device__ __forceinline__ uint4 read(int at) const { return *reinterpret_cast<const uint4 *>(ring + slot * p.stage + at); }
 
     // The row's slot has been read: the row that comes next into it.
     __device__ __forceinline__ void release(const Group &g)
