@@ -617,6 +617,8 @@ def moe_gated_linear(x, w13, out, *, offsets=None, gate_up=None, activation="sil
     [R, 2 I], if given, receives both products for moe_gated_linear_backward."""
     R, H, xp, xs = _rows(x, 2, "x")
     E, two, _ = _experts(w13, "w13", H)
+    if two % 2:
+        raise ValueError(f"w13 has {two} rows an expert; this call needs W1's and as many of W3")
     inner = two // 2
     gp, gs = _matrix(gate_up, R, 2 * inner, "gate_up")
     op, os_ = _matrix(out, R, inner, "out")

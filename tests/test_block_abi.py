@@ -181,6 +181,7 @@ def test_binding_of_the_products(L):
     refused("contiguous", nqg.moe_grouped_linear, x, t(2, 64, 32).transpose(1, 2), out, offsets=off)
     refused("status", nqg.moe_grouped_linear, x, w, out, offsets=off, status=t(1, dtype=I64))
     refused("out", nqg.moe_gated_linear, x, w, out, offsets=off)  # I is 16
+    refused("as many of W3", nqg.moe_gated_linear, x, t(2, 33, 64), t(5, 16), offsets=off)
     refused("gate_up", nqg.moe_gated_linear, x, w, t(5, 16), gate_up=t(5, 16), offsets=off)
 
 
