@@ -20,6 +20,10 @@
 //
 // CTAs stay (one pair for two SMs) and take every P-th tile.  Within an expert, blocks of 8 tiles of one side pass along
 // the other, so that the pairs at work share their operands in L2.
+//
+// Few tiles with a long contraction leave most SMs idle.  There, 2 or 4 pairs form a cluster and share a tile's contraction:
+// each makes sums of its part, sends them to the pair that writes their columns (chunks of columns in turns), through
+// distributed shared memory, and that one adds them up in the shares' order.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -52,6 +56,8 @@ struct Params {
     int32_t E, width, out_width;
     int32_t fold;                              // Product::fold; each step of the contraction is then made twice, once for each part
     int32_t m_tiles, n_tiles, n_columns;       // n_*: the weights' gradient's N side
+    int32_t cap;                               // columns of a tile at most (not the weights' gradient)
+    int32_t shares;                            // pairs that share a tile's contraction
     int32_t wide_a, wide_b;                    // an operand across comes in boxes of 128 columns (two chunks), not 64
     const int32_t *offsets;
     uint8_t *out, *gate_up;
@@ -80,6 +86,10 @@ struct Tile {
     int32_t n;       // columns of the matrix instruction
     int32_t m0, n0;  // first of the 256, first column (weights' gradient)
     int32_t steps;
+    int32_t begin, end;  // this pair's
+
+    // The first step of share i of n.
+    __device__ int32_t first_of(int i, int n) const { return static_cast<int32_t>(static_cast<int64_t>(steps) * i / n); }
 
     // Whether a step of the weights' gradient reads beyond the expert's rows.
     __device__ bool beyond(int k, int32_t fold) const { return rows % kStep != 0 && k >= steps - (fold ? 2 : 1); }
@@ -89,9 +99,10 @@ template <int KIND>
 struct Schedule {
     const Params &p;
     const int32_t *first, *tile0;  // rows and (not for the weights' gradient) tiles of rows before each expert
+    int share, shares;             // this pair's part of the contraction
     uint32_t total;  // below 2^31
 
-    __device__ Schedule(const Params &q, const int32_t *f, const int32_t *t) : p(q), first(f), tile0(t)
+    __device__ Schedule(const Params &q, const int32_t *f, const int32_t *t, int i, int n) : p(q), first(f), tile0(t), share(i), shares(n)
     {
         total = static_cast<uint32_t>(KIND == kWeight ? p.E * p.n_tiles : tile0[p.E]) * p.m_tiles;
     }
@@ -138,6 +149,8 @@ struct Schedule {
             t.n0 = 0;
             t.steps = (p.width + kStep - 1) / kStep * (p.fold ? 2 : 1);
         }
+        t.begin = t.first_of(share, shares);
+        t.end = t.first_of(share + 1, shares);
         return t;
     }
 };
@@ -173,7 +186,7 @@ __device__ bool read_offsets(const Params &p, int32_t *first, int32_t *tile0, in
             int32_t prev = __shfl_up_sync(0xffffffffu, most, 1);
             prev = lane == 0 ? before : prev;
             // tiles of expert i - 1
-            int32_t n = i == 0 || i > p.E ? 0 : (most - prev + kMaxN - 1) / kMaxN;
+            int32_t n = i == 0 || i > p.E ? 0 : (most - prev + p.cap - 1) / p.cap;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
                 const int32_t u = __shfl_up_sync(0xffffffffu, n, o);
@@ -209,24 +222,107 @@ __device__ __forceinline__ void store_lines(const uint8_t *staging, uint8_t *out
     }
 }
 
+// Sums that other pairs made of parts of a tile's contraction.  A unit is 32 values a thread: 32 columns of a warp's 32 lanes,
+// or 64 of 16 lanes.  `inbox` holds, for every share, quarter and unit that this CTA writes, 32 values of 32 threads.
+struct Shares {
+    float *inbox;
+    int count, mine, rank;  // pairs, this one, this CTA's place in it
+    int units;              // most of a quarter's units that one pair writes
+
+    __device__ int at(int share, int quarter, int unit) const { return ((share * 4 + quarter) * units + unit) * 1024; }
+
+    // This CTA's part of a unit to the CTA that writes it.
+    __device__ void send(int owner, int quarter, int unit, int lane, const uint32_t *v) const
+    {
+        const uint32_t to = cluster_map(smem_u32(inbox + at(mine, quarter, unit) + lane), 2 * owner + rank);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            store_cluster(to + 128 * i, v[i]);
+    }
+
+    // Adds what the others sent, in their order.
+    __device__ void add(const Tile &t, int quarter, int unit, int lane, uint32_t *v) const
+    {
+        for (int s = 0; s < count; ++s) {
+            if (s == mine || t.first_of(s, count) == t.first_of(s + 1, count))
+                continue;
+            const float *from = inbox + at(s, quarter, unit) + lane;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = __float_as_uint(__uint_as_float(v[i]) + from[32 * i]);
+        }
+    }
+};
+
 // A tile of the weights' gradient: lanes are rows of the result, so a warp has whole lines of it, 64 columns (32 of fp32) of
 // 16 rows at a time.
-template <bool BF16>
-__device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, uint32_t sums, int quarter, int part, int lane, int rank,
-                                               uint8_t *staging, bool lost)
+// 64 columns from c on of 16 of the warp's lanes; zeros where there are no steps, NaN where they were lost.
+__device__ __forceinline__ void load_unit64(uint32_t (&raw)[32], const Tile &t, uint32_t sums, int quarter, int h, int c, bool lost)
 {
-    for (int c = 64 * part; c < t.n; c += 128) {
+    if (t.begin < t.end && !lost) {
+        tmem_load_fragments(sums + (static_cast<uint32_t>(32 * quarter + 16 * h) << 16) + c, raw);
+        tmem_load_wait();
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            raw[j] = lost ? 0x7FC00000u : 0u;
+    }
+}
+
+// 32 columns from c on of the warp's lanes, 16 and then 16, the same way.
+__device__ __forceinline__ void load_unit32(uint32_t (&raw)[2][16], const Tile &t, uint32_t sums, int quarter, int c, bool lost)
+{
+    if (t.begin < t.end && !lost) {
+        const uint32_t from = sums + (static_cast<uint32_t>(quarter) << 21) + c;
+        tmem_load_fragments(from, raw[0]);
+        tmem_load_fragments(from + (16u << 16), raw[1]);
+        tmem_load_wait();
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            raw[0][j] = raw[1][j] = lost ? 0x7FC00000u : 0u;
+    }
+}
+
+// What this pair made of a shared tile and others write.
+template <int KIND>
+__device__ __forceinline__ void send_sums(const Tile &t, uint32_t sums, int quarter, int part, int lane, const Shares &shares, bool lost)
+{
+    if (t.begin == t.end)
+        return;
+    if constexpr (KIND == kWeight) {
+        for (int q = 0; 64 * q < t.n; ++q) {  // the two warps of a quarter take 16 lanes each
+            uint32_t raw[32];
+            if (q % shares.count == shares.mine)
+                continue;
+            __syncwarp();
+            load_unit64(raw, t, sums, quarter, part, 64 * q, lost);
+            shares.send(q % shares.count, quarter, 2 * (q / shares.count) + part, lane, raw);
+        }
+    } else {
+        for (int q = part; 32 * q < t.n; q += 2) {
+            uint32_t raw[2][16];
+            if (q % shares.count == shares.mine)
+                continue;
+            __syncwarp();
+            load_unit32(raw, t, sums, quarter, 32 * q, lost);
+            shares.send(q % shares.count, quarter, q / shares.count, lane, &raw[0][0]);
+        }
+    }
+}
+
+template <bool BF16, bool SPLIT>
+__device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, uint32_t sums, int quarter, int part, int lane, int rank,
+                                               uint8_t *staging, const Shares &shares, bool lost)
+{
+    for (int q = SPLIT ? shares.mine + shares.count * part : part; 64 * q < t.n; q += SPLIT ? 2 * shares.count : 2) {
+        const int c = 64 * q;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             uint32_t raw[32];
-            if (t.steps > 0 && !lost) {
-                tmem_load_fragments(sums + (static_cast<uint32_t>(32 * quarter + 16 * h) << 16) + c, raw);
-                tmem_load_wait();
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    raw[j] = lost ? 0x7FC00000u : 0u;
-            }
+            load_unit64(raw, t, sums, quarter, h, c, lost);
+            if constexpr (SPLIT)
+                shares.add(t, quarter, 2 * (q / shares.count) + h, lane, raw);
             const auto sum = [&](int s, int b, int j) { return __uint_as_float(raw[4 * b + 2 * s + j]); };
             const int row = t.m0 + rank * kSide + 32 * quarter + 16 * h, left = p.out_width - t.n0 - c;
             const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
@@ -262,25 +358,19 @@ __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, u
 // A tile of rows to its place: warps `quarter` (0 to 3) of the CTA of rank `rank` have lanes 32 quarter on, and take turns.
 // Lanes are columns of the result here.  Sums come as fragments of 8 x 8, and two warps put the 64 columns of theirs together
 // in a staging, so that whole lines are written.
-template <int KIND, bool BF16, int ACT>
+template <int KIND, bool BF16, int ACT, bool SPLIT>
 __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint32_t sums, int quarter, int part, int lane, int rank,
-                                           uint8_t *staging, float *exchange, bool lost)
+                                           uint8_t *staging, float *exchange, const Shares &shares, bool lost)
 {
-    const uint32_t from = sums + (static_cast<uint32_t>(quarter) << 21);
     const int second = quarter & 1;  // of the two warps
     const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16 + 64 * second;
-    for (int c = 32 * part; c < t.n; c += 64) {
+    for (int q = SPLIT ? shares.mine + shares.count * part : part; 32 * q < t.n; q += SPLIT ? 2 * shares.count : 2) {
+        const int c = 32 * q;
         __syncwarp();
         uint32_t raw[2][16];
-        if (!lost) {
-            tmem_load_fragments(from + c, raw[0]);
-            tmem_load_fragments(from + (16u << 16) + c, raw[1]);
-            tmem_load_wait();
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                raw[0][j] = raw[1][j] = 0x7FC00000u;
-        }
+        load_unit32(raw, t, sums, quarter, c, lost);
+        if constexpr (SPLIT)
+            shares.add(t, quarter, q / shares.count, lane, &raw[0][0]);
         // the sum of lane 8 i + (lane / 4), column 8 b + 2 (lane % 4) + j of the chunk
         const auto sum = [&](int i, int b, int j) { return __uint_as_float(raw[i / 2][4 * b + 2 * (i % 2) + j]); };
         const auto pair = [&](int i, int b) { return pack2<BF16>(sum(i, b, 0), sum(i, b, 1)); };
@@ -343,14 +433,16 @@ __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint3
     }
 }
 
-template <int KIND, bool BF16, int ACT>
+// SPLIT: clusters of several pairs, a tile each; otherwise clusters of a pair, which take many.
+template <int KIND, bool BF16, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p)
 {
     constexpr bool kAcrossA = KIND == kInput || KIND == kWeight, kAcrossB = KIND == kWeight;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(cluster_rank());
+    const int cta = static_cast<int>(cluster_rank()), rank = cta & 1, leader = SPLIT ? cta & ~1 : 0;
+    const uint32_t both = 3u << leader;
     int32_t *first = reinterpret_cast<int32_t *>(smem + Layout::first), *tile0 = first + p.E + 1;
     const uint32_t full = base + Layout::full, empty = base + Layout::empty, tail = base + Layout::tail,
                    sums_full = base + Layout::sums_full, sums_empty = base + Layout::sums_empty, done = base + Layout::done;
@@ -382,13 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     cluster_wait_acq();
     tcgen05_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + Layout::tmem);
-    const Schedule<KIND> plan(p, first, tile0);
+    const Schedule<KIND> plan(p, first, tile0, SPLIT ? cta / 2 : 0, SPLIT ? p.shares : 1);
     const uint32_t pair = cluster_id_x(), pairs = cluster_count_x();
+    bool lost = false;  // writing warps: a wait has run out
 
     if (warp == 0) {
         // copies: this CTA's 128 of the tile's 256 and half of its N
-        const uint32_t full_of_pair = cluster_map(full, 0);
-        int64_t left = pair == 0 && rank == 0 && p.stall >= 0 ? p.stall : INT64_MAX;  // test hook (moe_debug_stall)
+        const uint32_t full_of_pair = cluster_map(full, leader);
+        int64_t left = pair == 0 && cta == 0 && p.stall >= 0 ? p.stall : INT64_MAX;  // test hook (moe_debug_stall)
         uint32_t slot = 0, phase = 1, used = 0;
         bool good = true;
         for (uint32_t q = pair; q < plan.total && good; q += pairs) {
@@ -396,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int half = t.n / 2;
             const int chunks = (half + 63) / 64;
             const uint32_t bytes = kOperand + static_cast<uint32_t>(kAcrossB ? (p.wide_b ? 2 * kChunk : chunks * kChunk) : half * kLine);
-            for (int k = 0; k < t.steps; ++k) {
+            for (int k = t.begin; k < t.end; ++k) {
                 if (left-- <= 0 || !warp_wait(empty + 8 * slot, phase)) {
                     good = false;
                     break;
@@ -464,13 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         bool good = true;
         for (uint32_t q = pair; q < plan.total && good; q += pairs) {
             const Tile t = plan.at(q);
-            if (t.steps == 0)
+            if (t.begin == t.end)
                 continue;
             const uint32_t idesc = mma_f16_descriptor(BF16, kAcrossA, kAcrossB, 256, static_cast<uint32_t>(t.n));
             const uint32_t sums = tmem + (turn & 1) * kMaxN;
             good = warp_wait(sums_empty + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1);
             tcgen05_fence_after();
-            for (int k = 0; k < t.steps && good; ++k) {
+            for (int k = t.begin; k < t.end && good; ++k) {
                 good = warp_wait(full + 8 * slot, phase);
                 if (!good)
                     break;
@@ -484,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
                     for (int j = 0; j < kStep / 16; ++j)
                         if (KIND != kWeight || j < sixteens)
-                            mma_pair_f16(sums, a + j * (kAcrossA ? 16 * kLine / 16 : 2), b + j * (kAcrossB ? 16 * kLine / 16 : 2), idesc, k > 0 || j > 0);
-                    mma_pair_commit(empty + 8 * slot);
+                            mma_pair_f16(sums, a + j * (kAcrossA ? 16 * kLine / 16 : 2), b + j * (kAcrossB ? 16 * kLine / 16 : 2), idesc, k > t.begin || j > 0);
+                    mma_pair_commit(empty + 8 * slot, both);
                 }
                 __syncwarp();
                 if (++slot == kStages) {
@@ -494,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 }
             }
             if (good && elect_lane())
-                mma_pair_commit(sums_full + 8 * (turn & 1));
+                mma_pair_commit(sums_full + 8 * (turn & 1), both);
             __syncwarp();
             ++turn;
         }
@@ -502,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             // what is in flight ends before the pair leaves: matrix instructions, and copies (those of a slot that only one CTA
             // filled never complete its barrier, and have long landed after the wait)
             if (elect_lane())
-                mma_pair_commit(done);
+                mma_pair_commit(done, both);
             __syncwarp();
             warp_wait(done, 0);
             const uint64_t t0 = globaltimer_ns();
@@ -518,15 +611,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp == 2 && KIND == kWeight) {
         // the last step of an expert's rows: lines behind them, in both operands, become zeros (a neighbour's values
         // times zero would not do, as they may be infinities)
-        const uint32_t full_of_pair = cluster_map(full, 0);
+        const uint32_t full_of_pair = cluster_map(full, leader);
         uint32_t slot = 0, phases = 0;
         bool good = true;
         for (uint32_t q = pair; q < plan.total && good; q += pairs) {
             const Tile t = plan.at(q);
-            if (t.steps == 0)
+            if (t.begin == t.end)
                 continue;
-            const int rest = t.rows % kStep, last = rest != 0 ? (p.fold ? 2 : 1) : 0;  // steps of the tile that read beyond
-            slot = static_cast<uint32_t>((slot + t.steps - last) % kStages);
+            // steps of this pair that read beyond
+            const int rest = t.rows % kStep, until = t.steps - (p.fold ? 2 : 1),
+                      last = rest != 0 && t.end > until ? t.end - (t.begin > until ? t.begin : until) : 0;
+            slot = static_cast<uint32_t>((slot + t.end - t.begin - last) % kStages);
             for (int i = 0; i < last && good; ++i) {
                 good = mbar_wait_bounded(tail + 8 * slot, (phases >> slot) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
                 good = __all_sync(0xffffffffu, good);
@@ -550,25 +645,26 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
     } else if (warp >= 4) {
         const int quarter = warp & 3, part = warp / 4 - 1;
-        const uint32_t empty_of_pair = cluster_map(sums_empty, 0);
+        const uint32_t empty_of_pair = cluster_map(sums_empty, leader);
         uint8_t *staging = smem + Layout::staging + (KIND == kWeight ? warp - 4 : (KIND == kGated ? 1 : 2) * (warp / 2 - 2)) * 16 * kPitch;
         float *exchange = reinterpret_cast<float *>(smem + Layout::exchange);
         uint32_t turn = 0;
-        bool lost = false;
         for (uint32_t q = pair; q < plan.total; q += pairs) {
             const Tile t = plan.at(q);
             const uint32_t i = turn & 1;
-            if (t.steps > 0 && !lost) {
+            if (t.begin < t.end && !lost) {
                 // a long contraction takes longer than the limit alone
                 lost = !mbar_wait_bounded(sums_full + 8 * i, (turn >> 1) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
                 lost = __any_sync(0xffffffffu, lost);
                 tcgen05_fence_after();
             }
+            if constexpr (SPLIT)
+                break;  // the tile is written below
             if constexpr (KIND == kWeight)
-                write_gradient<BF16>(p, t, tmem + i * kMaxN, quarter, part, lane, rank, staging, lost);
+                write_gradient<BF16, false>(p, t, tmem + i * kMaxN, quarter, part, lane, rank, staging, {}, lost);
             else
-                write_tile<KIND, BF16, ACT>(p, t, tmem + i * kMaxN, quarter, part, lane, rank, staging, exchange, lost);
-            if (t.steps > 0) {
+                write_tile<KIND, BF16, ACT, false>(p, t, tmem + i * kMaxN, quarter, part, lane, rank, staging, exchange, {}, lost);
+            if (t.begin < t.end) {
                 tcgen05_fence_before();
                 __syncwarp();
                 if (lane == 0 && !lost)
@@ -578,6 +674,30 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         if (lost && lane == 0 && p.status)
             atomicCAS(p.status, 0, MOE_ERR_DEVICE_TIMEOUT);
+    }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        // every pair's matrix instructions are complete, and the slots' memory is free for sums
+        cluster_arrive_rel();
+        cluster_wait_acq();
+        const int quarter = warp & 3, part = warp / 4 - 1;
+        const bool writes = warp >= 4 && pair < plan.total;
+        const Tile t = writes ? plan.at(pair) : Tile{};
+        const Shares shares{reinterpret_cast<float *>(smem), p.shares, cta / 2, rank,
+                            KIND == kWeight ? 2 * ((t.n / 64 + p.shares - 1) / p.shares) : (t.n / 32 + p.shares - 1) / p.shares};
+        if (writes)
+            send_sums<KIND>(t, tmem, quarter, part, lane, shares, lost);
+        __syncwarp();
+        cluster_arrive_rel();
+        cluster_wait_acq();
+        if (writes) {
+            uint8_t *staging = smem + Layout::staging + (KIND == kWeight ? warp - 4 : (KIND == kGated ? 1 : 2) * (warp / 2 - 2)) * 16 * kPitch;
+            if constexpr (KIND == kWeight)
+                write_gradient<BF16, true>(p, t, tmem, quarter, part, lane, rank, staging, shares, lost);
+            else
+                write_tile<KIND, BF16, ACT, true>(p, t, tmem, quarter, part, lane, rank, staging, reinterpret_cast<float *>(smem + Layout::exchange),
+                                                  shares, lost);
+        }
     }
     __syncwarp();
     tcgen05_fence_before();
@@ -591,11 +711,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
 // -------------------------------------------------------------------------------------------------- launch
 
+// Tiles at most, and exactly with one expert.
+int64_t tiles_of(int64_t rows, int64_t E, int cap, int64_t m_tiles)
+{
+    return (E == 1 ? (rows + cap - 1) / cap : rows / cap + (rows < E ? rows : E)) * m_tiles;
+}
+
 template <int KIND, bool BF16, int ACT>
 moe_status launch(const Product &a, moe_stream_t stream)
 {
-    static SmemLimit limit;
-    const auto kern = product_kernel<KIND, BF16, ACT>;
+    static SmemLimit limits[2];
     const int sms = sm_count();
     int dev = 0;
     Params p{};
@@ -620,8 +745,16 @@ moe_status launch(const Product &a, moe_stream_t stream)
         tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
     } else {
         p.m_tiles = KIND == kGated ? (a.out_width + 127) / 128 : (a.out_width + 255) / 256;
-        tiles = (a.n_rows / kMaxN + (a.n_rows < a.E ? a.n_rows : a.E)) * p.m_tiles;
+        // halves of tiles where that keeps more pairs at work: a step takes 0.26 us with 256 columns and 0.14 with up to 128
+        p.cap = tiles_of(a.n_rows, a.E, kMaxN / 2, p.m_tiles) <= sms / 2 ? kMaxN / 2 : kMaxN;
+        tiles = tiles_of(a.n_rows, a.E, p.cap, p.m_tiles);
     }
+    const int64_t steps = KIND == kWeight ? a.n_rows / a.E / kStep : (a.width + kStep - 1) / kStep * (a.fold ? 2 : 1);
+    // Pairs that share a tile, 1 / 2 / 4, us in a graph: 16 rows, N = 1024 (4 tiles), K = 2048: 8.9 / 10.0 / 9.1, 3008: 11.3 / 11.5
+    // / 10.1, 4096: 13.8 / 13.3 / 10.9, 8192: 23.6 / 20.0 / 14.3; weights' gradient of 2048 rows: 13.6 / 13.2 / 14.0, 8192: 38.8 /
+    // 25.9 / 20.3.  No more than 15 clusters of 8 CTAs run at once (16 tiles: 21 us instead of 11), and 36 of 4.
+    p.shares = tiles <= sms / 10 && steps >= 40 ? 4 : (tiles <= sms / 4 - 2 && steps >= 64 ? 2 : 1);
+    const auto kern = p.shares > 1 ? product_kernel<KIND, BF16, ACT, true> : product_kernel<KIND, BF16, ACT, false>;
     const int64_t W = a.width, F = a.out_width, held = a.fold ? 2 * a.fold : W;  // held: columns of `rows` in memory
     // [rows, columns] across, of `groups` matrices: chunks of 64 columns, two in a box where the columns are whole chunks
     const auto across = [](CUtensorMap &map, const void *at, int64_t columns, int64_t rows, int64_t groups, int64_t stride, bool wide) {
@@ -647,20 +780,20 @@ moe_status launch(const Product &a, moe_stream_t stream)
     for (int i = 0; KIND != kWeight && i < kRowBoxes; ++i)
         ok = ok && encode_tensor(p.b[i], a.rows, {3, {held, a.n_rows, 1}, {a.rows_stride, a.rows_stride}, {kStep, 16 << i, 1}});
     const size_t smem = static_cast<size_t>(Layout::bytes(a.E));
-    if (!ok || sms < 2 || cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limit) != cudaSuccess) {
+    if (!ok || sms < 2 || cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limits[p.shares > 1]) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
-    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    const int64_t clusters = p.shares > 1 || tiles < sms / 2 ? tiles : sms / 2;
     // an ordinary launch: pairs that were resident before the kernel in front of them had ended were not worth their risk (a
     // CTA holds all tensor memory of its SM)
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * p.shares);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < 1 ? 1 : pairs)));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * p.shares * (clusters < 1 ? 1 : clusters)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);

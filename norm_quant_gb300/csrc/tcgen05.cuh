@@ -91,11 +91,12 @@ __device__ __forceinline__ void mma_pair_f16(uint32_t d, uint64_t a, uint64_t b,
                  : "memory");
 }
 
-// Arrives at the barrier of this offset in both CTAs once every matrix instruction this thread has issued is complete.
-__device__ __forceinline__ void mma_pair_commit(uint32_t bar)
+// Arrives at the barrier of this offset in the cluster's CTAs of `ctas` (a bit each: the pair's two) once every matrix
+// instruction this thread has issued is complete.
+__device__ __forceinline__ void mma_pair_commit(uint32_t bar, uint32_t ctas)
 {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"(static_cast<uint16_t>(3))
+                 "h"(static_cast<uint16_t>(ctas))
                  : "memory");
 }
 
@@ -133,6 +134,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// A float to shared memory of a CTA of the cluster (address from cluster_map).
+__device__ __forceinline__ void store_cluster(uint32_t at, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 // A box of a three- or four-dimensional tensor to this CTA's shared memory, counted on a barrier of either CTA.

@@ -298,6 +298,35 @@ def test_larger_products(rows, K, N, E):
     check_linear_backward(bounds, rows, K, N, "bf16", "fp32")
 
 
+# few tiles with a long contraction, which several pairs share: 4 of them, 2, an odd number of steps, columns in several chunks
+@pytest.mark.parametrize("rows,K,N,E", [(1, 4096, 272, 1), (130, 3080, 512, 1), (256, 2600, 208, 1), (250, 3000, 64, 2),
+                                        (700, 4104, 1040, 1), (33, 8192, 1040, 1), (40, 4104, 2048, 2)])
+def test_shared_contractions(rows, K, N, E):
+    bounds = [0, rows] if E == 1 else [0, rows // 3, rows - 1]
+    g = gen(K + rows)
+    x, w = normal(g, rows, K), normal(g, E, N, K, std=K ** -0.5)
+    y, bound, _ = ref.product(x, w, bounds, "bf16")
+    (out, ob), (gu, gb) = ref.gated(x, w, bounds, "gelu_tanh", "bf16")
+    for _ in range(2):
+        o = Out(rows, N, "bf16")
+        nqg.moe_grouped_linear(x.to(DEV), w.to(DEV), o.view, offsets=dev_offsets(bounds))
+        o.check(y, bound, bounds)
+        o, s = Out(rows, N // 2, "bf16"), Out(rows, N, "bf16")
+        nqg.moe_gated_linear(x.to(DEV), w.to(DEV), o.view, offsets=dev_offsets(bounds), gate_up=s.view, activation="gelu_tanh")
+        o.check(out, ob, bounds)
+        s.check(gu, gb, bounds)
+    check_linear_backward(bounds, rows, K, N, "bf16", "bf16")
+    check_linear_backward(bounds, rows, N, K, "bf16", "fp32")
+
+
+# the weights' gradient of many rows with few columns
+@pytest.mark.parametrize("rows,K,N,E,grad", [(3001, 72, 64, 1, "bf16"), (5000, 264, 520, 1, "fp32"), (9000, 40, 1000, 2, "bf16"),
+                                             (12000, 136, 200, 3, "fp32"), (2600, 64, 256, 1, "bf16"), (4200, 1288, 1032, 1, "bf16")])
+def test_shared_rows(rows, K, N, E, grad):
+    bounds = {1: [0, rows], 2: [5, 100, rows], 3: [0, rows - 7, rows - 7, rows]}[E]
+    check_linear_backward(bounds, rows, K, N, "bf16", grad)
+
+
 def test_matrices_of_more_than_2_to_the_32_bytes():
     """Rows far beyond 2^31 elements from the first, of a matrix and of a gradient."""
     rows, K, N = 600_000, 4096, 64

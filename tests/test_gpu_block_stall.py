@@ -67,6 +67,27 @@ def test_copies_that_stop(what, slots):
     assert torch.equal(out, good) and int(status) == 0
 
 
+@pytest.mark.parametrize("slots", [0, 2])
+@pytest.mark.parametrize("rows,K,N", [(20, 4096, 256), (300, 4096, 1024)])
+def test_copies_that_stop_in_a_shared_tile(rows, K, N, slots):
+    """The pairs that share the tile make it NaN; other tiles are as they were."""
+    g = gen(rows)
+    x, w = normal(g, rows, K).to(DEV), normal(g, 1, N, K, std=K ** -0.5).to(DEV)
+    out, status = torch.empty((rows, N), dtype=torch.bfloat16, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    call = lambda: nqg.moe_grouped_linear(x, w, out, status=status)  # noqa: E731
+    call()
+    good = out.clone()
+    assert bool(good.isfinite().all())
+    stalled(slots, call)
+    assert int(status) == nqg.MOE_ERR_DEVICE_TIMEOUT
+    late = out.isnan()
+    assert bool(late[:20, :256].all()) and bool((late.sum() <= 256 * 128))
+    assert torch.equal(out[~late], good[~late])
+    status.zero_()
+    call()
+    assert torch.equal(out, good) and int(status) == 0
+
+
 @pytest.mark.parametrize("slots", [0, 1, 3])
 @pytest.mark.parametrize("H", [96, 4096, 16384])
 def test_norm_rows_that_stop(slots, H):
