@@ -745,8 +745,19 @@ moe_status launch(const Product &a, moe_stream_t stream)
         tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
     } else {
         p.m_tiles = KIND == kGated ? (a.out_width + 127) / 128 : (a.out_width + 255) / 256;
-        // halves of tiles where that keeps more pairs at work: a step takes 0.26 us with 256 columns and 0.14 with up to 128
-        p.cap = tiles_of(a.n_rows, a.E, kMaxN / 2, p.m_tiles) <= sms / 2 ? kMaxN / 2 : kMaxN;
+        // Narrower tiles where they make fewer or emptier rounds.  A step of a tile of n columns takes about as long as its
+        // operands' way from L2, (256 + n) lines a pair: R = 4096, N = 4096, K = 16384 is 4 rounds of 256 tiles or 4 of 304 with 224
+        // columns (317 and 300 us).  With several experts only the case of one round is known here.
+        p.cap = kMaxN;
+        const int64_t pairs = sms / 2;
+        int64_t least = INT64_MAX;
+        for (int cap = kMaxN; cap >= kMaxN / 2 && pairs > 0; cap -= 32) {
+            const int64_t rounds = (tiles_of(a.n_rows, a.E, cap, p.m_tiles) + pairs - 1) / pairs, cost = rounds * (kMaxN + cap);
+            if ((a.E == 1 || rounds == 1) && cost < least) {
+                least = cost;
+                p.cap = cap;
+            }
+        }
         tiles = tiles_of(a.n_rows, a.E, p.cap, p.m_tiles);
     }
     const int64_t steps = KIND == kWeight ? a.n_rows / a.E / kStep : (a.width + kStep - 1) / kStep * (a.fold ? 2 : 1);
