@@ -56,7 +56,7 @@ struct Params {
     int32_t E, width, out_width;
     int32_t fold;                              // Product::fold; each step of the contraction is then made twice, once for each part
     int32_t m_tiles, n_tiles, n_columns;       // n_*: the weights' gradient's N side
-    int32_t cap;                               // columns of a tile at most (not the weights' gradient)
+    int32_t cap;                               // columns of a tile at most
     int32_t shares;                            // pairs that share a tile's contraction
     int32_t wide_a, wide_b;                    // an operand across comes in boxes of 128 columns (two chunks), not 64
     const int32_t *offsets;
@@ -324,7 +324,7 @@ __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, u
             if constexpr (SPLIT)
                 shares.add(t, quarter, 2 * (q / shares.count) + h, lane, raw);
             const auto sum = [&](int s, int b, int j) { return __uint_as_float(raw[4 * b + 2 * s + j]); };
-            const int row = t.m0 + rank * kSide + 32 * quarter + 16 * h, left = p.out_width - t.n0 - c;
+            const int row = t.m0 + rank * kSide + 32 * quarter + 16 * h, left = (p.out_width - t.n0 < t.n ? p.out_width - t.n0 : t.n) - c;
             const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
             if (p.fp32_out) {
 #pragma unroll
@@ -737,34 +737,42 @@ moe_status launch(const Product &a, moe_stream_t stream)
     p.status = a.status;
     p.fp32_out = a.fp32_out;
     p.stall = a.stall;
-    int64_t tiles;
-    if (KIND == kWeight) {
-        p.n_columns = a.out_width > 128 ? 256 : (a.out_width > 64 ? 128 : 64);
-        p.m_tiles = (a.width + 255) / 256;
-        p.n_tiles = (a.out_width + p.n_columns - 1) / p.n_columns;
-        tiles = static_cast<int64_t>(a.E) * p.m_tiles * p.n_tiles;
-    } else {
-        p.m_tiles = KIND == kGated ? (a.out_width + 127) / 128 : (a.out_width + 255) / 256;
-        // Narrower tiles where they make fewer or emptier rounds.  A step of a tile of n columns takes about as long as its
-        // operands' way from L2, (256 + n) lines a pair: R = 4096, N = 4096, K = 16384 is 4 rounds of 256 tiles or 4 of 304 with 224
-        // columns (317 and 300 us).  With several experts only the case of one round is known here.
-        p.cap = kMaxN;
-        const int64_t pairs = sms / 2;
-        int64_t least = INT64_MAX;
-        for (int cap = kMaxN; cap >= kMaxN / 2 && pairs > 0; cap -= 32) {
-            const int64_t rounds = (tiles_of(a.n_rows, a.E, cap, p.m_tiles) + pairs - 1) / pairs, cost = rounds * (kMaxN + cap);
-            if ((a.E == 1 || rounds == 1) && cost < least) {
-                least = cost;
-                p.cap = cap;
-            }
-        }
-        tiles = tiles_of(a.n_rows, a.E, p.cap, p.m_tiles);
-    }
     const int64_t steps = KIND == kWeight ? a.n_rows / a.E / kStep : (a.width + kStep - 1) / kStep * (a.fold ? 2 : 1);
     // Pairs that share a tile, 1 / 2 / 4, us in a graph: 16 rows, N = 1024 (4 tiles), K = 2048: 8.9 / 10.0 / 9.1, 3008: 11.3 / 11.5
     // / 10.1, 4096: 13.8 / 13.3 / 10.9, 8192: 23.6 / 20.0 / 14.3; weights' gradient of 2048 rows: 13.6 / 13.2 / 14.0, 8192: 38.8 /
     // 25.9 / 20.3.  No more than 15 clusters of 8 CTAs run at once (16 tiles: 21 us instead of 11), and 36 of 4.
-    p.shares = tiles <= sms / 10 && steps >= 40 ? 4 : (tiles <= sms / 4 - 2 && steps >= 64 ? 2 : 1);
+    const auto shares_of = [&](int64_t count) { return count <= sms / 10 && steps >= 40 ? 4 : (count <= sms / 4 - 2 && steps >= 64 ? 2 : 1); };
+    // Narrower tiles where they make fewer or emptier rounds.  A step of a tile of n columns takes about as long as its
+    // operands' way from L2, (256 + n) lines a pair: R = 4096, N = 4096, K = 16384 is 4 rounds of 256 tiles or 4 of 304 with 224
+    // columns (319 and 298 us); the weights' gradient of R = N = K = 4096 82 and 77 us.  Tiles of rows of several experts are
+    // known here only where they make one round.
+    int64_t tiles, least = INT64_MAX;
+    const int64_t pairs = sms / 2;
+    const auto better = [&](int64_t count, int columns, bool known) {
+        const int64_t rounds = (count + pairs - 1) / (pairs > 0 ? pairs : 1), cost = rounds * (kMaxN + columns) * 4 / shares_of(count);
+        if (cost >= least || !(known || rounds == 1))
+            return false;
+        least = cost;
+        return true;
+    };
+    if (KIND == kWeight) {
+        p.m_tiles = (a.width + 255) / 256;
+        const auto count = [&](int columns) { return static_cast<int64_t>(a.E) * p.m_tiles * ((a.out_width + columns - 1) / columns); };
+        p.n_columns = a.out_width > 64 ? 128 : 64;
+        for (int columns = kMaxN; columns >= kMaxN / 2 && a.out_width > 128; columns -= 32)
+            if (better(count(columns), columns, true))
+                p.n_columns = columns;
+        p.n_tiles = (a.out_width + p.n_columns - 1) / p.n_columns;
+        tiles = count(p.n_columns);
+    } else {
+        p.m_tiles = KIND == kGated ? (a.out_width + 127) / 128 : (a.out_width + 255) / 256;
+        p.cap = kMaxN;
+        for (int cap = kMaxN; cap >= kMaxN / 2; cap -= 32)
+            if (better(tiles_of(a.n_rows, a.E, cap, p.m_tiles), cap, a.E == 1))
+                p.cap = cap;
+        tiles = tiles_of(a.n_rows, a.E, p.cap, p.m_tiles);
+    }
+    p.shares = shares_of(tiles);
     const auto kern = p.shares > 1 ? product_kernel<KIND, BF16, ACT, true> : product_kernel<KIND, BF16, ACT, false>;
     const int64_t W = a.width, F = a.out_width, held = a.fold ? 2 * a.fold : W;  // held: columns of `rows` in memory
     // [rows, columns] across, of `groups` matrices: chunks of 64 columns, two in a box where the columns are whole chunks

@@ -327,6 +327,26 @@ def test_shared_rows(rows, K, N, E, grad):
     check_linear_backward(bounds, rows, K, N, "bf16", grad)
 
 
+# tiles of 224, 192, 160 and 128 columns: of rows and, in the weights' gradient, of the other matrix
+@pytest.mark.parametrize("rows,K,N,E", [(450, 136, 1040, 1), (900, 264, 2064, 1), (1100, 136, 4112, 1), (640, 72, 4112, 1),
+                                        (130, 1400, 2064, 1), (70, 4000, 1040, 1), (203, 3304, 1040, 1), (190, 2000, 1040, 2)])
+def test_tiles_of_other_widths(rows, K, N, E):
+    bounds = [0, rows] if E == 1 else [3, 100, rows - 5]
+    g = gen(K + rows)
+    x, w = normal(g, rows, K), normal(g, E, N, K, std=K ** -0.5)
+    y, bound, _ = ref.product(x, w, bounds, "bf16")
+    o = Out(rows, N, "bf16", 8)
+    nqg.moe_grouped_linear(x.to(DEV), w.to(DEV), o.view, offsets=dev_offsets(bounds))
+    o.check(y, bound, bounds)
+    (out, ob), (gu, gb) = ref.gated(x, w, bounds, "silu", "bf16")
+    o, s = Out(rows, N // 2, "bf16"), Out(rows, N, "bf16", 8)
+    nqg.moe_gated_linear(x.to(DEV), w.to(DEV), o.view, offsets=dev_offsets(bounds), gate_up=s.view)
+    o.check(out, ob, bounds)
+    s.check(gu, gb, bounds)
+    check_linear_backward(bounds, rows, K, N, "bf16", "bf16")
+    check_linear_backward(bounds, rows, N, K, "bf16", "fp32")
+
+
 def test_matrices_of_more_than_2_to_the_32_bytes():
     """Rows far beyond 2^31 elements from the first, of a matrix and of a gradient."""
     rows, K, N = 600_000, 4096, 64
