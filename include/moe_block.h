@@ -30,6 +30,8 @@
  * Waits inside the products' kernels are bounded.  One that runs out (after 2 s,
  * which no healthy launch comes near) turns results that depend on it into NaN
  * and records MOE_ERR_DEVICE_TIMEOUT in *status; nothing faults or hangs.
+ * moe_debug_stall (moe_combine.h) stops the first thread block's copies of a product
+ * and the copies of a norm's first rows after its number of steps, to test that.
  */
 #ifndef MOE_BLOCK_H
 #define MOE_BLOCK_H
@@ -41,8 +43,10 @@ extern "C" {
 #endif
 
 /* Limits (validated on the host): H, I, K and N up to MOE_BLOCK_MAX_DIM and
- * multiples of 8, E up to MOE_LAYER_MAX_EXPERTS, rows below 2^31 - 2^16. */
+ * multiples of 8, E up to MOE_LAYER_MAX_EXPERTS, rows below 2^31 - 2^16, strides of the
+ * products' matrices up to MOE_BLOCK_MAX_STRIDE. */
 #define MOE_BLOCK_MAX_DIM 65536
+#define MOE_BLOCK_MAX_STRIDE ((INT64_C(1) << 39) - 8)
 
 /* ------------------------------------------------------------------------
  * Gated product of a feed-forward block, both projections in one kernel:

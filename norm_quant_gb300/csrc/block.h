@@ -45,10 +45,11 @@ moe_status run_product(ProductKind kind, const Product &p, moe_stream_t stream);
 
 inline bool valid_io(int32_t io) { return io == MOE_IO_BF16 || io == MOE_IO_FP16; }
 
-// A matrix of rows of `width` 16-bit elements: 16-byte aligned, with a stride that keeps every row so.
+// A matrix of rows of `width` 16-bit elements: 16-byte aligned, with a stride that keeps every row so and that a tensor map
+// takes (below 2^40 bytes).
 inline bool valid_rows(const void *p, int64_t stride, int32_t width)
 {
-    return p && aligned16(p) && stride >= width && stride % 8 == 0;
+    return p && aligned16(p) && stride >= width && stride <= MOE_BLOCK_MAX_STRIDE && stride % 8 == 0;
 }
 
 } // namespace nqg

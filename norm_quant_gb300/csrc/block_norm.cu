@@ -58,12 +58,6 @@ struct RingSmem {
 // Of each group, in dynamic shared memory: two buffers in turn, a value a warp.
 using GroupSums = float[2][kSums][kWarps];
 
-template <bool BF16>
-__device__ __forceinline__ void load8(float (&v)[8], const uint8_t *p)
-{
-    unpack8<BF16>(*reinterpret_cast<const uint4 *>(p), v);
-}
-
 // gamma + weight_bias of 8 columns (1 without gamma).
 template <bool BF16>
 __device__ __forceinline__ void gammas8(float (&v)[8], bool given, const uint4 &gamma, float bias)

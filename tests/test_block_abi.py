@@ -46,6 +46,18 @@ def test_gated_linear_refusals(L, kw, want):
     assert call(L, "moe_gated_linear", GATED, kw) == want
 
 
+# a stride that no tensor map takes (2^40 bytes and more), of every matrix of rows of the products
+@pytest.mark.parametrize("name,fields", [
+    ("moe_gated_linear", ["x", "out", "gate_up"]), ("moe_gated_linear_backward", ["x", "d_out", "gate_up", "d_x"]),
+    ("moe_grouped_linear", ["x", "out"]), ("moe_grouped_linear_backward", ["x", "d_out", "d_x"])])
+def test_strides_beyond_a_tensor_map(L, name, fields):
+    base = {"moe_gated_linear": dict(GATED, gate_up=0x5000, gate_up_stride=64), "moe_gated_linear_backward": GATED_GRAD,
+            "moe_grouped_linear": GROUPED, "moe_grouped_linear_backward": GROUPED_GRAD}[name]
+    for field in fields:
+        for stride in (1 << 39, (1 << 63) - 8):
+            assert call(L, name, base, {f"{field}_stride": stride}) == 1, (field, stride)
+
+
 GATED_GRAD = dict(rows=4, H=64, I=32, E=2, offsets=0x1000, d_out=0x2000, d_out_stride=32, gate_up=0x3000, gate_up_stride=64,
                   x=0x4000, x_stride=64, w13=0x5000, d_x=0x6000, d_x_stride=64, d_w13=0x7000, workspace=0x8000,
                   workspace_bytes=1024, grad_dtype=1)
