@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const bool writes = warp >= 4 && pair < plan.total;
         const Tile t = writes ? plan.at(pair) : Tile{};
         const Shares shares{reinterpret_cast<float *>(smem), p.shares, cta / 2, rank,
-                            KIND == kWeight ? 2 * ((t.n / 64 + p.shares - 1) / p.shares) : (t.n / 32 + p.shares - 1) / p.shares};
+                            KIND == kWeight ? 2 * (((t.n + 63) / 64 + p.shares - 1) / p.shares) : (t.n / 32 + p.shares - 1) / p.shares};
         if (writes)
             send_sums<KIND>(t, tmem, quarter, part, lane, shares, lost);
         __syncwarp();

@@ -321,7 +321,8 @@ def test_shared_contractions(rows, K, N, E):
 
 # the weights' gradient of many rows with few columns
 @pytest.mark.parametrize("rows,K,N,E,grad", [(3001, 72, 64, 1, "bf16"), (5000, 264, 520, 1, "fp32"), (9000, 40, 1000, 2, "bf16"),
-                                             (12000, 136, 200, 3, "fp32"), (2600, 64, 256, 1, "bf16"), (4200, 1288, 1032, 1, "bf16")])
+                                             (12000, 136, 200, 3, "fp32"), (2600, 64, 256, 1, "bf16"), (4200, 1288, 1032, 1, "bf16"),
+                                             (4104, 1200, 1024, 1, "bf16"), (4104, 1200, 1024, 1, "fp32"), (4130, 1344, 1536, 1, "bf16")])
 def test_shared_rows(rows, K, N, E, grad):
     bounds = {1: [0, rows], 2: [5, 100, rows], 3: [0, rows - 7, rows - 7, rows]}[E]
     check_linear_backward(bounds, rows, K, N, "bf16", grad)
