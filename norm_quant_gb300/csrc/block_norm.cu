@@ -937,10 +937,18 @@ moe_status launch_norm(NormParams &p, moe_stream_t stream)
     return PdlLaunch(static_cast<unsigned>(p.T < sms ? p.T : sms), threads, smem, stream).run(norm_kernel<BF16, VPT, FACTORS>, p);
 }
 
+// One for all forms that launch the kernel of wide rows: it is the kernel whose limit it keeps.
+template <bool BF16>
+SmemLimit &wide_limit()
+{
+    static SmemLimit limit;
+    return limit;
+}
+
 template <bool BF16, int VPT, bool ALL>
 moe_status launch_backward(NormParams &p, moe_stream_t stream)
 {
-    static SmemLimit limits[2];
+    static SmemLimit limit;
     int dev = 0;
     const int sms = sm_count();
     const bool wide = p.H > kMaxRingWidth;
@@ -960,7 +968,8 @@ moe_status launch_backward(NormParams &p, moe_stream_t stream)
         smem = smem > ring ? smem : ring;
     }
     const auto kern = wide ? norm_backward_wide_kernel<BF16> : norm_backward_kernel<BF16, VPT, ALL>;
-    if (sms <= 0 || cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limits[wide]) != cudaSuccess) {
+    if (sms <= 0 || cudaGetDevice(&dev) != cudaSuccess ||
+        ensure_dynamic_smem(kern, dev, static_cast<int>(smem), wide ? wide_limit<BF16>() : limit) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }

@@ -1,5 +1,9 @@
 """The norms around a block on the GPU, forward and backward, against 64-bit
 references: widths, gates, missing parts, outputs in place of inputs."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -237,3 +241,46 @@ def test_large_batch():
     for at in (slice(0, 100), slice(100, 2777), slice(2777, T)):
         nqg.moe_block_norm(y[at], r[at], post_gamma=gamma, pre_gamma=gamma, residual_out=parts[0][at], norm_out=parts[1][at])
     assert all(torch.equal(a, b) for a, b in zip(whole, parts))
+
+
+def test_offsets_beyond_32_bits():
+    """Matrices of more than 2^32 bytes: their last rows as a call of their own makes them, forward and backward."""
+    T, H, n = 530000, 4104, 1000
+    assert 2 * T * H > 2 ** 32 and T * H > 2 ** 31
+    g = gen(5)
+    gamma = (1 + 0.2 * torch.randn(H, generator=g)).to(torch.bfloat16).to(DEV)
+    y, r, ds, dn = (torch.zeros((T, H), dtype=torch.bfloat16, device=DEV) for _ in range(4))
+    for v in (y, r, ds, dn):
+        v[-n:] = normal(g, n, H).to(DEV)
+    kw = dict(post_gamma=gamma, pre_gamma=gamma, eps=1e-5)
+    out = [torch.full((T, H), 13.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    nqg.moe_block_norm(y, r, residual_out=out[0], norm_out=out[1], **kw)
+    few = [torch.empty_like(y[-n:]) for _ in range(2)]
+    nqg.moe_block_norm(y[-n:], r[-n:], residual_out=few[0], norm_out=few[1], **kw)
+    assert all(torch.equal(a[-n:], b) for a, b in zip(out, few)) and all(bool((a[:-n] == 0).all()) for a in out)
+    nqg.moe_block_norm_backward(y, r, d_residual_out=ds, d_norm_out=dn, d_y=out[0], d_residual=out[1], **kw)
+    nqg.moe_block_norm_backward(y[-n:], r[-n:], d_residual_out=ds[-n:], d_norm_out=dn[-n:], d_y=few[0], d_residual=few[1], **kw)
+    assert all(torch.equal(a[-n:], b) for a, b in zip(out, few)) and all(bool((a[:-n] == 0).all()) for a in out)
+
+
+WIDE = """
+import torch, norm_quant_gb300 as nqg
+def run(H, io, whole):
+    dt = torch.bfloat16 if io == "bf16" else torch.float16
+    v = [torch.ones((3, H), dtype=dt, device="cuda") for _ in range(6)]
+    gamma, sums = torch.ones(H, dtype=dt, device="cuda"), torch.empty(H, device="cuda")
+    ws = torch.empty(nqg.moe_block_norm_backward_workspace_size(3, H), dtype=torch.uint8, device="cuda")
+    more = dict(d_residual_out=v[3], d_residual=v[5]) if whole else {}
+    nqg.moe_block_norm_backward(v[0], v[1], post_gamma=gamma, pre_gamma=gamma, d_norm_out=v[2], d_y=v[4], d_post_gamma=sums,
+                                workspace=ws, io_dtype=io, **more)
+for io in ("bf16", "fp16"):
+    for H, whole in ((16384, True), (8200, False), (16384, True), (12000, False), (8208, True), (16384, False)):
+        run(H, io, whole)
+torch.cuda.synchronize()
+"""
+
+
+def test_wide_rows_of_all_forms_in_turn():
+    """The widest rows after narrower ones of another form, in a process that has made no call yet."""
+    subprocess.run([sys.executable, "-c", WIDE], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                   timeout=90)
