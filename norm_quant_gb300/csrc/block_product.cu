@@ -161,48 +161,65 @@ struct Schedule {
 };
 
 // The offsets as the kernels take them (none below its predecessor, all within [0, rows]) and, with TILES, the tiles of
-// rows before each expert.  One warp, 32 at a time.  Returns whether all were as they should be.
-template <bool TILES>
+// rows before each expert.  One warp, EACH neighbours a lane at a time, whose loads are in flight together (196 experts, a few
+// rows: 6.0 us, 8.1 with one a lane).  Returns whether all were as they should be.
+template <bool TILES, int EACH>
 __device__ bool read_offsets(const Params &p, int32_t *first, int32_t *tile0, int lane)
 {
     bool good = true;
-    int32_t low = 0, tiles = 0, before = 0;
-    for (int base = 0; base <= p.E; base += 32) {
-        const int i = base + lane;
-        int32_t v = 0;
-        if (i <= p.E) {
-            v = p.offsets ? p.offsets[i] : (i == 0 ? 0 : static_cast<int32_t>(p.n_rows));
-            const int32_t c = v < 0 ? 0 : (v > p.n_rows ? static_cast<int32_t>(p.n_rows) : v);
-            good = good && c == v;
-            v = c;
+    int32_t low = 0, tiles = 0;  // the offset and the tiles before these
+    for (int base = 0; base <= p.E; base += 32 * EACH) {
+        int32_t v[EACH], most = 0;
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            const int i = base + EACH * lane + k;
+            v[k] = i > p.E ? 0 : (p.offsets ? p.offsets[i] : (i == 0 ? 0 : static_cast<int32_t>(p.n_rows)));
         }
-        int32_t most = v;
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            const int32_t c = v[k] < 0 ? 0 : (v[k] > p.n_rows ? static_cast<int32_t>(p.n_rows) : v[k]);
+            most = c > most ? c : most;
+            good = good && (base + EACH * lane + k > p.E || most == v[k]);
+            v[k] = most;  // of this lane's up to here
+        }
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
             const int32_t u = __shfl_up_sync(0xffffffffu, most, o);
             if (lane >= o)
                 most = u > most ? u : most;
         }
-        most = most > low ? most : low;
-        good = good && (i > p.E || most == v);
-        if (i <= p.E)
-            first[i] = most;
+        int32_t before = __shfl_up_sync(0xffffffffu, most, 1);
+        before = lane == 0 || before < low ? low : before;
+        good = good && (base + EACH * lane > p.E || v[0] >= before);
+        int32_t sum = 0, prev = before, n[EACH];
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            const int i = base + EACH * lane + k;
+            const int32_t at = v[k] > before ? v[k] : before;
+            if (i <= p.E)
+                first[i] = at;
+            if constexpr (TILES) {
+                // tiles of expert i - 1
+                sum += i == 0 || i > p.E ? 0 : (at - prev + p.cap - 1) / p.cap;
+                n[k] = sum;
+                prev = at;
+            }
+        }
         if constexpr (TILES) {
-            int32_t prev = __shfl_up_sync(0xffffffffu, most, 1);
-            prev = lane == 0 ? before : prev;
-            // tiles of expert i - 1
-            int32_t n = i == 0 || i > p.E ? 0 : (most - prev + p.cap - 1) / p.cap;
+            int32_t all = sum;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
-                const int32_t u = __shfl_up_sync(0xffffffffu, n, o);
-                n += lane >= o ? u : 0;
+                const int32_t u = __shfl_up_sync(0xffffffffu, all, o);
+                all += lane >= o ? u : 0;
             }
-            if (i <= p.E)
-                tile0[i] = tiles + n;
-            tiles += __shfl_sync(0xffffffffu, n, 31);
-            before = __shfl_sync(0xffffffffu, most, 31);
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+                if (base + EACH * lane + k <= p.E)
+                    tile0[base + EACH * lane + k] = tiles + all - sum + n[k];
+            tiles += __shfl_sync(0xffffffffu, all, 31);
         }
-        low = __shfl_sync(0xffffffffu, most, 31);
+        most = __shfl_sync(0xffffffffu, most, 31);
+        low = most > low ? most : low;
     }
     return __all_sync(0xffffffffu, good);
 }
@@ -320,42 +337,44 @@ template <bool BF16, bool SPLIT>
 __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, uint32_t sums, int quarter, int part, int lane, int rank,
                                                uint8_t *staging, const Shares &shares, bool lost)
 {
-    for (int q = SPLIT ? shares.mine + shares.count * part : part; 64 * q < t.n; q += SPLIT ? 2 * shares.count : 2) {
-        const int c = 64 * q;
+    // The two warps of a quarter take every other chunk of 64 columns, or half of the lanes each where there is an odd number of
+    // chunks (59 rows, K = 576, N = 2528, E = 125, three chunks a tile: 67 us, 77 with a warp taking two of them).
+    const int columns = p.out_width - t.n0 < t.n ? p.out_width - t.n0 : t.n;
+    const int step = SPLIT ? shares.count : 1, mine = SPLIT ? shares.mine : 0, chunks = ((columns + 63) / 64 - mine + step - 1) / step;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            uint32_t raw[32];
-            load_unit64(raw, t, sums, quarter, h, c, lost);
-            if constexpr (SPLIT)
-                shares.add(t, quarter, 2 * (q / shares.count) + h, lane, raw);
-            const auto sum = [&](int s, int b, int j) { return __uint_as_float(raw[4 * b + 2 * s + j]); };
-            const int row = t.m0 + rank * kSide + 32 * quarter + 16 * h, left = (p.out_width - t.n0 < t.n ? p.out_width - t.n0 : t.n) - c;
-            const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
-            if (p.fp32_out) {
+    for (int u = 0; u < chunks; ++u) {
+        const int h = chunks % 2 ? part : u % 2, q = mine + step * (chunks % 2 ? u : u - h + part), c = 64 * q;
+        uint32_t raw[32];
+        load_unit64(raw, t, sums, quarter, h, c, lost);
+        if constexpr (SPLIT)
+            shares.add(t, quarter, 2 * (q / shares.count) + h, lane, raw);
+        const auto sum = [&](int s, int b, int j) { return __uint_as_float(raw[4 * b + 2 * s + j]); };
+        const int row = t.m0 + rank * kSide + 32 * quarter + 16 * h, left = columns - c;
+        const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
+        if (p.fp32_out) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            *reinterpret_cast<float2 *>(staging + (8 * s + lane / 4) * kPitch + 32 * b + 8 * (lane % 4)) =
-                                make_float2(sum(s, 4 * x + b, 0), sum(s, 4 * x + b, 1));
-                    __syncwarp();
-                    store_lines<16>(staging, p.out + 4 * (at + 32 * x), 4 * static_cast<int64_t>(p.out_width), p.width - row, 4 * (left - 32 * x), lane);
-                    __syncwarp();
-                }
-            } else {
-                const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16;
-                const auto pair = [&](int s, int b) { return pack2<BF16>(sum(s, b, 0), sum(s, b, 1)); };
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int b = 0; b < 8; b += 4)
-                        store_fragments<false>(at_lane + 8 * s * kPitch + 16 * b, pair(s, b), pair(s, b + 1), pair(s, b + 2), pair(s, b + 3));
+                    for (int b = 0; b < 4; ++b)
+                        *reinterpret_cast<float2 *>(staging + (8 * s + lane / 4) * kPitch + 32 * b + 8 * (lane % 4)) =
+                            make_float2(sum(s, 4 * x + b, 0), sum(s, 4 * x + b, 1));
                 __syncwarp();
-                store_lines<16>(staging, p.out + 2 * at, 2 * static_cast<int64_t>(p.out_width), p.width - row, 2 * left, lane);
+                store_lines<16>(staging, p.out + 4 * (at + 32 * x), 4 * static_cast<int64_t>(p.out_width), p.width - row, 4 * (left - 32 * x), lane);
                 __syncwarp();
             }
+        } else {
+            const uint32_t at_lane = smem_u32(staging) + (lane % 8) * kPitch + (lane / 8) * 16;
+            const auto pair = [&](int s, int b) { return pack2<BF16>(sum(s, b, 0), sum(s, b, 1)); };
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int b = 0; b < 8; b += 4)
+                    store_fragments<false>(at_lane + 8 * s * kPitch + 16 * b, pair(s, b), pair(s, b + 1), pair(s, b + 2), pair(s, b + 3));
+            __syncwarp();
+            store_lines<16>(staging, p.out + 2 * at, 2 * static_cast<int64_t>(p.out_width), p.width - row, 2 * left, lane);
+            __syncwarp();
         }
     }
 }
@@ -470,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (warp == 2)
         tmem_alloc_pair(base + Layout::tmem, 512);
     if (warp == 0) {
-        if (!read_offsets<KIND != kWeight>(p, first, tile0, lane) && lane == 0 && p.status && blockIdx.x == 0)
+        const bool good = p.E < 32 ? read_offsets<KIND != kWeight, 1>(p, first, tile0, lane) : read_offsets<KIND != kWeight, 9>(p, first, tile0, lane);
+        if (!good && lane == 0 && p.status && blockIdx.x == 0)
             atomicCAS(p.status, 0, MOE_ERR_ROW_OUT_OF_RANGE);
     }
     tcgen05_fence_before();

@@ -263,6 +263,30 @@ def test_offsets_out_of_order_or_range(bad, meant):
     assert int(status) == nqg.MOE_ERR_ROW_OUT_OF_RANGE
 
 
+@pytest.mark.parametrize("E", [31, 32, 287, 288, 700])
+def test_offsets_of_many_experts_out_of_order(E):
+    """The same, where a lane reads several offsets and there are several turns of them."""
+    rows, K, N = 90, 64, 72
+    g = gen(E)
+    bad = torch.randint(0, rows + 1, (E + 1,), generator=g).sort().values
+    wrong = torch.randint(0, E + 1, (E // 10,), generator=g)
+    bad[wrong] = torch.randint(-20, rows + 20, (E // 10,), generator=g)
+    meant = bad.clamp(0, rows).cummax(0).values.tolist()
+    x, w, dy = normal(g, rows, K), normal(g, E, N, K, std=K ** -0.5), normal(g, rows, N)
+    for given, code in ((bad.tolist(), nqg.MOE_ERR_ROW_OUT_OF_RANGE if meant != bad.tolist() else 0), (meant, 0)):
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        o, dw = Out(rows, N, "bf16"), torch.full((E, N, K), CANARY, dtype=torch.float32, device=DEV)
+        nqg.moe_grouped_linear(x.to(DEV), w.to(DEV), o.view, offsets=dev_offsets(given), status=status)
+        assert int(status) == code
+        y, bound, _ = ref.product(x, w, meant, "bf16")
+        o.check(y, bound, meant)
+        status.zero_()
+        nqg.moe_grouped_linear_backward(dy.to(DEV), x=x.to(DEV), d_w=dw, offsets=dev_offsets(given), status=status, grad_dtype="fp32")
+        assert int(status) == code
+        want, bound = ref.weight_grad(dy.double(), torch.zeros(rows, N, dtype=torch.float64), x, meant, "bf16", "fp32")
+        near(dw, want, bound)
+
+
 def test_no_rows():
     e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
     off = dev_offsets([0, 0, 0])
