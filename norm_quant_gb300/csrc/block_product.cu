@@ -26,7 +26,7 @@
 // CTAs stay (one pair for two SMs) and take every P-th tile.  Within an expert, blocks of 8 tiles of one side pass along
 // the other, so that the pairs at work share their operands in L2.
 //
-// Few tiles with a long contraction leave most SMs idle.  There, 2 or 4 pairs form a cluster and share a tile's contraction:
+// Few tiles with a long contraction leave most SMs idle.  There, 2 to 4 pairs form a cluster and share a tile's contraction:
 // each makes sums of its part, sends them to the pair that writes their columns (chunks of columns in turns), through
 // distributed shared memory, and that one adds them up in the shares' order.
 #include <cstdint>
@@ -763,10 +763,18 @@ moe_status launch(const Product &a, moe_stream_t stream)
     p.fp32_out = a.fp32_out;
     p.stall = a.stall;
     const int64_t steps = KIND == kWeight ? a.n_rows / a.E / kStep : (a.width + kStep - 1) / kStep * (a.fold ? 2 : 1);
-    // Pairs that share a tile, 1 / 2 / 4, us in a graph: 16 rows, N = 1024 (4 tiles), K = 2048: 8.9 / 10.0 / 9.1, 3008: 11.3 / 11.5
-    // / 10.1, 4096: 13.8 / 13.3 / 10.9, 8192: 23.6 / 20.0 / 14.3; weights' gradient of 2048 rows: 13.6 / 13.2 / 14.0, 8192: 38.8 /
-    // 25.9 / 20.3.  No more than 15 clusters of 8 CTAs run at once (16 tiles: 21 us instead of 11), and 36 of 4.
-    const auto shares_of = [&](int64_t count) { return count <= sms / 10 && steps >= 40 ? 4 : (count <= sms / 4 - 2 && steps >= 64 ? 2 : 1); };
+    // Pairs that share a tile, 1 / 2 / 3 / 4, us in a graph: 16 rows, N = 2048 (8 tiles), K = 2048: 9.1 / 10.0 / 9.4 / 9.2, 2560:
+    // 10.3 / 10.8 / 10.0 / 9.7, 4096: 14.0 / 13.4 / 11.6 / 11.0, 8192: 23.6 / 20.1 / 16.0 / 14.4; weights' gradient of 1024 x 1024,
+    // 2048 rows: 13.6 / 13.2 / - / 14.0, 4096: - / 17.8 / 18.8 / -, 8192: 38.8 / 27.0 / 25.2 / 20.3.  Tiles of many rows have too many
+    // sums to send for three (256 rows, K = N = 4096: 14.9 with two and 128 columns, 17.2 with three and 256).  No more than 15 clusters
+    // of 8 CTAs run at once (16 tiles: 21 us instead of 11), 23 of 6 and 36 of 4.
+    const auto shares_of = [&](int64_t count, int columns) {
+        if (count <= sms / 10 && steps >= 40)
+            return 4;
+        if (count <= sms / 6 - 2 && (KIND == kWeight ? steps >= 80 : columns <= kMaxN / 2 && steps >= 48))
+            return 3;
+        return count <= sms / 4 - 2 && steps >= 64 ? 2 : 1;
+    };
     // Narrower tiles where they make fewer or emptier rounds.  A step of a tile of n columns takes about as long as its
     // operands' way from L2, (256 + n) lines a pair: R = 4096, N = 4096, K = 16384 is 4 rounds of 256 tiles or 4 of 304 with 224
     // columns (319 and 298 us); the weights' gradient of R = N = K = 4096 82 and 77 us.  Tiles of rows of several experts are
@@ -774,7 +782,7 @@ moe_status launch(const Product &a, moe_stream_t stream)
     int64_t tiles, least = INT64_MAX;
     const int64_t pairs = sms / 2;
     const auto better = [&](int64_t count, int columns, bool known) {
-        const int64_t rounds = (count + pairs - 1) / (pairs > 0 ? pairs : 1), cost = rounds * (kMaxN + columns) * 4 / shares_of(count);
+        const int64_t rounds = (count + pairs - 1) / (pairs > 0 ? pairs : 1), cost = rounds * (kMaxN + columns) * 12 / shares_of(count, columns);
         if (cost >= least || !(known || rounds == 1))
             return false;
         least = cost;
@@ -797,7 +805,7 @@ moe_status launch(const Product &a, moe_stream_t stream)
                 p.cap = cap;
         tiles = tiles_of(a.n_rows, a.E, p.cap, p.m_tiles);
     }
-    p.shares = shares_of(tiles);
+    p.shares = shares_of(tiles, KIND == kWeight ? p.n_columns : p.cap);
     const auto kern = p.shares > 1 ? product_kernel<KIND, BF16, ACT, true> : product_kernel<KIND, BF16, ACT, false>;
     const int64_t W = a.width, F = a.out_width, held = a.fold ? 2 * a.fold : W;  // held: columns of `rows` in memory
     // [rows, columns] across, of `groups` matrices: chunks of 64 columns, two in a box where the columns are whole chunks

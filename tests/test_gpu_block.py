@@ -322,9 +322,9 @@ def test_larger_products(rows, K, N, E):
     check_linear_backward(bounds, rows, K, N, "bf16", "fp32")
 
 
-# few tiles with a long contraction, which several pairs share: 4 of them, 2, an odd number of steps, columns in several chunks
+# few tiles with a long contraction, which several pairs share: 4 of them, 3, 2, an odd number of steps, columns in several chunks
 @pytest.mark.parametrize("rows,K,N,E", [(1, 4096, 272, 1), (130, 3080, 512, 1), (256, 2600, 208, 1), (250, 3000, 64, 2),
-                                        (700, 4104, 1040, 1), (33, 8192, 1040, 1), (40, 4104, 2048, 2)])
+                                        (700, 4104, 1040, 1), (33, 8192, 1040, 1), (40, 4104, 2048, 2), (16, 2568, 4112, 1), (120, 4096, 5136, 1)])
 def test_shared_contractions(rows, K, N, E):
     bounds = [0, rows] if E == 1 else [0, rows // 3, rows - 1]
     g = gen(K + rows)
@@ -346,7 +346,8 @@ def test_shared_contractions(rows, K, N, E):
 # the weights' gradient of many rows with few columns
 @pytest.mark.parametrize("rows,K,N,E,grad", [(3001, 72, 64, 1, "bf16"), (5000, 264, 520, 1, "fp32"), (9000, 40, 1000, 2, "bf16"),
                                              (12000, 136, 200, 3, "fp32"), (2600, 64, 256, 1, "bf16"), (4200, 1288, 1032, 1, "bf16"),
-                                             (4104, 1200, 1024, 1, "bf16"), (4104, 1200, 1024, 1, "fp32"), (4130, 1344, 1536, 1, "bf16")])
+                                             (4104, 1200, 1024, 1, "bf16"), (4104, 1200, 1024, 1, "fp32"), (4130, 1344, 1536, 1, "bf16"),
+                                             (6000, 512, 1288, 1, "bf16"), (5300, 640, 1032, 1, "fp32")])
 def test_shared_rows(rows, K, N, E, grad):
     bounds = {1: [0, rows], 2: [5, 100, rows], 3: [0, rows - 7, rows - 7, rows]}[E]
     check_linear_backward(bounds, rows, K, N, "bf16", grad)
