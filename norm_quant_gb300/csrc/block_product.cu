@@ -775,14 +775,15 @@ moe_status launch(const Product &a, moe_stream_t stream)
             return 3;
         return count <= sms / 4 - 2 && steps >= 64 ? 2 : 1;
     };
-    // Narrower tiles where they make fewer or emptier rounds.  A step of a tile of n columns takes about as long as its
-    // operands' way from L2, (256 + n) lines a pair: R = 4096, N = 4096, K = 16384 is 4 rounds of 256 tiles or 4 of 304 with 224
-    // columns (319 and 298 us); the weights' gradient of R = N = K = 4096 82 and 77 us.  Tiles of rows of several experts are
-    // known here only where they make one round.
+    // Narrower tiles where they make fewer or emptier rounds.  A step of a tile of n columns takes about as long as its way through
+    // an SM's shared memory, in lines of 128 bytes: 128 + n / 2 written and 128 + n read (153 ns at n = 32, 230 at 128, 308 at
+    // 256).  R = 4096, N = 4096, K = 16384 is 4 rounds of 256 tiles or 4 of 304 with 224 columns (319 and 298 us); the weights'
+    // gradient of R = N = K = 4096 took 82 and 77 us.  Tiles of rows of several experts are known here only where they make one
+    // round.
     int64_t tiles, least = INT64_MAX;
     const int64_t pairs = sms / 2;
     const auto better = [&](int64_t count, int columns, bool known) {
-        const int64_t rounds = (count + pairs - 1) / (pairs > 0 ? pairs : 1), cost = rounds * (kMaxN + columns) * 12 / shares_of(count, columns);
+        const int64_t rounds = (count + pairs - 1) / (pairs > 0 ? pairs : 1), cost = rounds * (2 * kMaxN + 3 * columns) * 12 / shares_of(count, columns);
         if (cost >= least || !(known || rounds == 1))
             return false;
         least = cost;
