@@ -232,7 +232,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
 
 // ROWS rows of 128 bytes in shared memory to global memory: row r to out + r * stride (bytes) for r < rows, and of each the first
 // `left` bytes (a multiple of 16).  Whole lines: lines written half by half, by whichever warps, took twice the time (a weights' gradient of 1.07 GB 311
-// us, 3.5 TB/s; whole lines 174 us).
+// us, 3.5 TB/s; whole lines 164 us).
 template <int ROWS>
 __device__ __forceinline__ void store_lines(const uint8_t *staging, uint8_t *out, int64_t stride, int rows, int left, int lane)
 {
@@ -338,9 +338,13 @@ __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, u
                                                uint8_t *staging, const Shares &shares, bool lost)
 {
     // The two warps of a quarter take every other chunk of 64 columns, or half of the lanes each where there is an odd number of
-    // chunks (59 rows, K = 576, N = 2528, E = 125, three chunks a tile: 67 us, 77 with a warp taking two of them).
+    // chunks (59 rows, K = 576, N = 2528, E = 125, three chunks a tile: 67 us, 77 with a warp taking two of them; 56
+    // with the addresses' products made once a tile).
     const int columns = p.out_width - t.n0 < t.n ? p.out_width - t.n0 : t.n;
     const int step = SPLIT ? shares.count : 1, mine = SPLIT ? shares.mine : 0, chunks = ((columns + 63) / 64 - mine + step - 1) / step;
+    const int size = p.fp32_out ? 4 : 2, row = t.m0 + rank * kSide + 32 * quarter;
+    const int64_t stride = size * static_cast<int64_t>(p.out_width);
+    uint8_t *const out = p.out + (static_cast<int64_t>(t.e) * p.width + row) * stride + size * t.n0;
 #pragma unroll 1
     for (int u = 0; u < chunks; ++u) {
         const int h = chunks % 2 ? part : u % 2, q = mine + step * (chunks % 2 ? u : u - h + part), c = 64 * q;
@@ -349,8 +353,8 @@ __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, u
         if constexpr (SPLIT)
             shares.add(t, quarter, 2 * (q / shares.count) + h, lane, raw);
         const auto sum = [&](int s, int b, int j) { return __uint_as_float(raw[4 * b + 2 * s + j]); };
-        const int row = t.m0 + rank * kSide + 32 * quarter + 16 * h, left = columns - c;
-        const int64_t at = (static_cast<int64_t>(t.e) * p.width + row) * p.out_width + t.n0 + c;
+        uint8_t *const to = out + 16 * h * stride + size * c;
+        const int rows = p.width - row - 16 * h, left = size * (columns - c);
         if (p.fp32_out) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -361,7 +365,7 @@ __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, u
                         *reinterpret_cast<float2 *>(staging + (8 * s + lane / 4) * kPitch + 32 * b + 8 * (lane % 4)) =
                             make_float2(sum(s, 4 * x + b, 0), sum(s, 4 * x + b, 1));
                 __syncwarp();
-                store_lines<16>(staging, p.out + 4 * (at + 32 * x), 4 * static_cast<int64_t>(p.out_width), p.width - row, 4 * (left - 32 * x), lane);
+                store_lines<16>(staging, to + kLine * x, stride, rows, left - kLine * x, lane);
                 __syncwarp();
             }
         } else {
@@ -373,7 +377,7 @@ __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, u
                 for (int b = 0; b < 8; b += 4)
                     store_fragments<false>(at_lane + 8 * s * kPitch + 16 * b, pair(s, b), pair(s, b + 1), pair(s, b + 2), pair(s, b + 3));
             __syncwarp();
-            store_lines<16>(staging, p.out + 2 * at, 2 * static_cast<int64_t>(p.out_width), p.width - row, 2 * left, lane);
+            store_lines<16>(staging, to, stride, rows, left, lane);
             __syncwarp();
         }
     }
