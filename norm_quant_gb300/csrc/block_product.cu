@@ -34,6 +34,7 @@
 
 #include "block.h"
 #include "block_math.cuh"
+#include "ring_place.h"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
 
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // copies: this CTA's 128 of the tile's 256 and half of its N
         const uint32_t full_of_pair = cluster_map(full, leader);
         int64_t left = pair == 0 && cta == 0 && p.stall >= 0 ? p.stall : INT64_MAX;  // test hook (moe_debug_stall)
-        uint32_t slot = 0, phase = 1, used = 0;
+        RingPlace<kStages> place;
         bool good = true;
         for (uint32_t q = pair; q < plan.total && good; q += pairs) {
             const Tile t = plan.at(q);
@@ -519,17 +520,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int chunks = (half + 63) / 64;
             const uint32_t bytes = kOperand + static_cast<uint32_t>(kAcrossB ? (p.wide_b ? 2 * kChunk : chunks * kChunk) : half * kLine);
             for (int k = t.begin; k < t.end; ++k) {
-                if (left-- <= 0 || !warp_wait(empty + 8 * slot, phase)) {
+                if (left-- <= 0 || !warp_wait(empty + 8 * place.slot, place.phase)) {
                     good = false;
                     break;
                 }
-                const uint32_t a = base + slot * kStage, b = a + kOperand;
-                uint32_t bar = full_of_pair + 8 * slot;
-                ++used;
-                if (++slot == kStages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+                const uint32_t a = base + place.slot * kStage, b = a + kOperand;
+                uint32_t bar = full_of_pair + 8 * place.slot;
+                place.next();
                 if (!elect_lane())
                     continue;
                 if (KIND == kWeight && t.beyond(k, p.fold)) {
@@ -574,13 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
         }
         // the last arrivals at this CTA's barriers land before it leaves
-        for (uint32_t i = 0; good && i < (used < kStages ? used : kStages); ++i) {
-            good = warp_wait(empty + 8 * slot, phase);
-            if (++slot == kStages) {
-                slot = 0;
-                phase ^= 1;
-            }
-        }
+        if (good)
+            place.drain([&](uint32_t slot, uint32_t phase) { return warp_wait(empty + 8 * slot, phase); });
     } else if (warp == 1 && rank == 0) {
         uint32_t slot = 0, phase = 0, turn = 0;
         bool good = true;
