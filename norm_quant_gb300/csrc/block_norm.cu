@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(2 * kMaxThreads / VPT, 1) norm_backward_kernel
             back = sum[1] * p.inv_h * rs * rs * rs;
             dot = sum[2] + rs * sum[3] - back * sum[4];
         } else if (with_post || p.gate_kind == MOE_GATE_TOKEN) {
-            float sum[1] = {total(re)};
+            // `lost` too: without a norm after the block nothing else in a token's d_gate is NaN where its row never came
+            float sum[1] = {total(re) + lost};
             g.sum(sum);
             dot = sum[0];
         }
