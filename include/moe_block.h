@@ -27,9 +27,10 @@
  * the same result every time.  A NaN or infinity of a row reaches that row's
  * results and its expert's weight gradient only.
  *
- * Waits inside the products' kernels are bounded.  One that runs out (after 2 s,
- * which no healthy launch comes near) turns results that depend on it into NaN
- * and records MOE_ERR_DEVICE_TIMEOUT in *status; nothing faults or hangs.
+ * Waits inside the products' kernels are bounded.  One that runs out (after 2 s and
+ * 4 us for each 64 of the contraction that is multiplied while it lasts, more than ten
+ * times what a healthy launch takes) turns results that depend on it into NaN and
+ * records MOE_ERR_DEVICE_TIMEOUT in *status; nothing faults or hangs.
  * moe_debug_stall (moe_combine.h) stops the first thread block's copies of a product
  * and the copies of a norm's first rows after its number of steps, to test that.
  */

@@ -55,6 +55,10 @@ constexpr int kRowBoxes = 4;
 constexpr int kPitch = 144;                 // bytes from row to row of a staging: 16 more than a line, so that eight rows meet no bank twice
 constexpr int kBlock = 8;                   // tiles of one side that pass along the other together
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kStepLimitNs = 4000;     // a step takes 0.15 to 0.31 us
+
+// How long a wait may last that ends only when so many steps have been made.
+__device__ __forceinline__ uint64_t wait_limit(int64_t steps) { return kWaitLimitNs + static_cast<uint64_t>(steps) * kStepLimitNs; }
 
 struct Params {
     CUtensorMap a, b[kRowBoxes];  // b: of rows in boxes of 16, 32, 64 and 128; the weights' gradient has one
@@ -634,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // times zero would not do, as they may be infinities)
         const uint32_t full_of_pair = cluster_map(full, leader);
         uint32_t slot = 0, phases = 0;
+        int64_t ahead = 0;  // steps that this pair makes before the next wait ends: tiles that end on a whole step are passed over
         bool good = true;
         for (uint32_t q = pair; q < plan.total && good; q += pairs) {
             const Tile t = plan.at(q);
@@ -643,11 +648,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int rest = t.rows % kStep, until = t.steps - (p.fold ? 2 : 1),
                       last = rest != 0 && t.end > until ? t.end - (t.begin > until ? t.begin : until) : 0;
             slot = static_cast<uint32_t>((slot + t.end - t.begin - last) % kStages);
+            ahead += t.end - t.begin;
             for (int i = 0; i < last && good; ++i) {
-                good = mbar_wait_bounded(tail + 8 * slot, (phases >> slot) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
+                good = mbar_wait_bounded(tail + 8 * slot, (phases >> slot) & 1, wait_limit(ahead));
                 good = __all_sync(0xffffffffu, good);
                 if (!good)
                     break;
+                ahead = 0;
                 phases ^= 1u << slot;
                 const int chunks = 2 + (t.n / 2 + 63) / 64;
                 const int end = (rest + 15) / 16 * 16;  // the matrix instructions take no more of them
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint32_t i = turn & 1;
             if (t.begin < t.end && !lost) {
                 // a long contraction takes longer than the limit alone
-                lost = !mbar_wait_bounded(sums_full + 8 * i, (turn >> 1) & 1, kWaitLimitNs + static_cast<uint64_t>(t.steps) * 4000);
+                lost = !mbar_wait_bounded(sums_full + 8 * i, (turn >> 1) & 1, wait_limit(t.steps));
                 lost = __any_sync(0xffffffffu, lost);
                 tcgen05_fence_after();
             }
