@@ -87,7 +87,7 @@ size_t moe_gated_linear_args_size(void);
  *   d_w13[e] = the sum of [dg; du][r] x[r]^T over the expert's rows (0 where it has none)
  *
  * dg and du are rounded once to io_dtype between (they are the products'
- * operands), or held as sums of two io_dtype values where they are few (rows <= 64
+ * operands), or held as sums of two io_dtype values where they are few (rows <= 32
  * and rows * (I + 56) <= 4096), as the errors of few roundings do not average out;
  * in fp16, values below 2^-24 vanish there and values beyond 65504 become
  * infinities, so losses are scaled as usual.  Either of d_x and d_w13 may be NULL; w13 is
@@ -96,7 +96,8 @@ size_t moe_gated_linear_args_size(void);
  *
  * workspace: device memory of moe_gated_linear_backward_workspace_size(...)
  * bytes, 16-byte aligned, not shared by calls that may overlap; it holds dg and du
- * of every row, and what it holds before a call does not matter.
+ * of every row, and what it holds before a call does not matter.  The
+ * size never falls as rows grow: one made for the largest batch serves every smaller one.
  * ---------------------------------------------------------------------- */
 typedef struct moe_gated_linear_backward_args {
     int64_t rows;

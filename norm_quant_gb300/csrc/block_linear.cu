@@ -82,9 +82,29 @@ moe_status launch_gate_grad(const GateGradParams &p, int sms, moe_stream_t strea
 // Where dg and du are so few that the errors of their roundings do not average out in the gradients (a gradient was off by up
 // to 1.7 times what its own rounding costs, not the 1.4 of many), they are held as sums of two 16-bit values, and the
 // products, which are a few microseconds of latency there, take every step twice.  The columns of each part, or 0.
+constexpr int64_t kHeldRows = 32, kHeldValues = 4096;  // rows, and rows * (I + 56)
+
+int32_t part_columns(int32_t I) { return (2 * I + 63) / 64 * 64; }
+
 int32_t fold_of(int64_t rows, int32_t I)
 {
-    return rows <= 64 && rows * (I + 56) <= 4096 ? (2 * I + 63) / 64 * 64 : 0;
+    return rows <= kHeldRows && rows * (I + 56) <= kHeldValues ? part_columns(I) : 0;
+}
+
+// What a call of so many rows writes, and the most that one of as many or fewer rows does.
+int64_t workspace_of(int64_t rows, int32_t I)
+{
+    const int32_t fold = fold_of(rows, I);
+    return rows * (fold ? fold : I) * 4;
+}
+
+int64_t workspace_up_to(int64_t rows, int32_t I)
+{
+    int64_t held = kHeldValues / (I + 56);
+    held = held < kHeldRows ? held : kHeldRows;
+    held = held < rows ? held : rows;
+    const int64_t a = workspace_of(rows, I), b = held * part_columns(I) * 4;
+    return a > b ? a : b;
 }
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - (1 << 16);
@@ -162,8 +182,7 @@ extern "C" moe_status moe_gated_linear_backward_workspace_size(int64_t rows, int
         return MOE_ERR_INVALID_ARG;
     if (rows >= kMaxRows || I > MOE_BLOCK_MAX_DIM)
         return MOE_ERR_UNSUPPORTED;
-    const int32_t fold = fold_of(rows, I);
-    *bytes = static_cast<size_t>(rows) * static_cast<size_t>(fold ? fold : I) * 4;
+    *bytes = static_cast<size_t>(workspace_up_to(rows, I));
     return MOE_OK;
 }
 
@@ -190,9 +209,7 @@ extern "C" moe_status moe_gated_linear_backward(const moe_gated_linear_backward_
         return MOE_ERR_INVALID_ARG;
     if (a->d_w13 && !valid_rows(a->x, a->x_stride, a->H))
         return MOE_ERR_INVALID_ARG;
-    size_t need = 0;
-    moe_gated_linear_backward_workspace_size(a->rows, a->I, &need);
-    if (!a->workspace || a->workspace_bytes < need)
+    if (!a->workspace || a->workspace_bytes < static_cast<size_t>(workspace_of(a->rows, a->I)))
         return MOE_ERR_WORKSPACE;
     if (!aligned16(a->workspace))
         return MOE_ERR_INVALID_ARG;
