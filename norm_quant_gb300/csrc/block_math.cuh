@@ -68,8 +68,10 @@ __device__ __forceinline__ void act_and_slope(float g, float &a, float &slope)
         slope = p + a * (1.0f - p);
     } else {
         const float p = sigmoid(kSqrt8OverPi * (g + 0.044715f * g * g * g));
+        // beyond |g| = 100 the factor in front of the square is 0, and an infinite square would make it NaN
+        const float m = fminf(fabsf(g), 100.0f);
         a = g * p;
-        slope = p + a * (1.0f - p) * kSqrt8OverPi * (1.0f + 0.134145f * g * g);
+        slope = p + a * (1.0f - p) * kSqrt8OverPi * (1.0f + 0.134145f * m * m);
     }
 }
 
