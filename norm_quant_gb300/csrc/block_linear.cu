@@ -79,13 +79,17 @@ moe_status launch_gate_grad(const GateGradParams &p, int sms, moe_stream_t strea
     return PdlLaunch(static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream).run(gate_grad_kernel<BF16, ACT>, p);
 }
 
-// Where dg and du are so few that the errors of their roundings do not average out in the gradients (a gradient was off by up
-// to 1.7 times what its own rounding costs, not the 1.4 of many), they are held as sums of two 16-bit values, and the
-// products, which are a few microseconds of latency there, take every step twice.  The columns of each part, or 0.
+// dg and du of small calls are held as sums of two 16-bit values, and the products take every step twice.  That leaves a gradient
+// no more error than its own rounding has, at any number of rows (relative, bf16: 1.65e-3 for 2.35e-3, and 2.5e-3 where sums are
+// shortest; fp16: 2.1e-4 for 2.95e-4), so the limits are of cost alone: up to the rows of the narrowest tile, and up to 8192
+// values a part with the columns that it is padded by.  bf16, us held / rounded once, in a graph: 32 rows, H = 256, I = 72: 13.0 /
+// 12.1; 16, 2048, 200: 14.3 / 12.7; 8, 2048, 456, E = 8: 25.3 / 21.6; 2, 4096, 1984: 33.2 / 25.4; 1, 4096, 4040: 51.1 / 40.9;
+// beyond: 32, 2048, 512: 17.4 / 14.5; 128, 2048, 1408, E = 8: 54.3 / 46.4; 1, 4096, 8192: 88.6 / 66.9; 2048, 2048, 4096: 173 / 100.
 constexpr int64_t kHeldRows = 32, kHeldValues = 4096;  // rows, and rows * (I + 56)
 
 int32_t part_columns(int32_t I) { return (2 * I + 63) / 64 * 64; }
 
+// The columns of each part, or 0.
 int32_t fold_of(int64_t rows, int32_t I)
 {
     return rows <= kHeldRows && rows * (I + 56) <= kHeldValues ? part_columns(I) : 0;
