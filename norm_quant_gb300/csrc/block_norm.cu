@@ -58,8 +58,11 @@ struct RingSmem {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
 };
 
-// Of each group, in dynamic shared memory: two buffers in turn, a value a warp.
-using GroupSums = float[2][kSums][kWarps];
+// Of each group, in shared memory: two buffers in turn, a value a warp.  Four of them are read at once.
+struct alignas(16) GroupSums {
+    float turns[2][kSums][kWarps];
+};
+static_assert(kWarps % 4 == 0 && sizeof(GroupSums) == 2 * kSums * kWarps * sizeof(float), "rows of whole vectors, one after the other");
 
 // gamma + weight_bias of 8 columns (1 without gamma).
 template <bool BF16>
@@ -191,7 +194,7 @@ __device__ __forceinline__ void store8(uint8_t *p, const uint4 &v) { *reinterpre
 // A group of warps that share a row.
 struct Group {
     int warps, warp, lane, index;
-    float (*red)[kSums][kWarps];
+    GroupSums &red;
     int turn;
 
     // Sums of N <= 2 values over the group, in every thread.  One barrier: two buffers in turn, and a thread that
@@ -209,11 +212,11 @@ struct Group {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (lane == 0)
-                red[turn][i][warp] = v[i];
+                red.turns[turn][i][warp] = v[i];
         named_barrier_sync(1 + index, 32 * warps);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = lane < warps ? red[turn][i][lane] : 0.0f;
+            v[i] = lane < warps ? red.turns[turn][i][lane] : 0.0f;
 #pragma unroll
             for (int o = 8; o; o >>= 1)
                 v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
@@ -240,9 +243,9 @@ struct Group {
         if (warps > 1) {
             const int which = lane / 4 < kSums ? lane / 4 : kSums - 1;
             if (lane % 4 == 0 && lane / 4 < kSums)
-                red[turn][which][warp] = mine;
+                red.turns[turn][which][warp] = mine;
             named_barrier_sync(1 + index, 32 * warps);
-            const float4 w = *reinterpret_cast<const float4 *>(&red[turn][which][4 * (lane % 4)]);
+            const float4 w = *reinterpret_cast<const float4 *>(&red.turns[turn][which][4 * (lane % 4)]);
             mine = (w.x + w.y) + (w.z + w.w);
             mine += __shfl_xor_sync(0xffffffffu, mine, 2);
             mine += __shfl_xor_sync(0xffffffffu, mine, 1);
@@ -265,7 +268,7 @@ __device__ __forceinline__ void ring_init(const NormParams &p, RingSmem &r, Grou
         fence_mbar_init();
     }
     for (int i = threadIdx.x; i < p.groups * 2 * kSums * kWarps; i += blockDim.x)
-        (&red[0][0][0][0])[i] = 0.0f;
+        (&red[0].turns[0][0][0])[i] = 0.0f;
     __syncthreads();
 }
 
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_wide_kernel(cons
 {
     constexpr int VPT = MOE_MAX_HIDDEN / 8 / kMaxThreads;
     extern __shared__ __align__(128) uint8_t dynamic[];
-    __shared__ float red[2][kSums][kWarps];
+    __shared__ GroupSums red;
     float *A = reinterpret_cast<float *>(dynamic), *B = A + p.H;
     grid_dependency_wait();
     const int vectors = p.H / 8, half = p.H / 2;
