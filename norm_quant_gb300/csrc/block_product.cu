@@ -16,7 +16,7 @@
 // 256, six such stages), which is what the matrix instruction of a pair wants: 64 bytes a cycle and SM instead of the 96 that a
 // 128 x 256 tile alone would take from L2.  Sums are in tensor memory, in two buffers of 256 columns, so that one
 // tile is written out while the next is multiplied.  Warps: 0 copies (TMA), 1 issues matrix instructions (in the
-// pair's first CTA, for both), 2 clears what a weight gradient's last step reads beyond its expert's rows, 4 to 11 write results.
+// pair's first CTA, for both), 4 to 11 write results.
 //
 // What bounds it: with many rows an expert the matrix instruction (R = 8192, K = 4096, N = 8192, bf16: forward 276 us, 1990
 // TFLOP/s, gated 274, rows' gradient 282, weights' gradient 279; the tensor pipe is active 93 % of the time at K = N = 4096),
@@ -52,6 +52,7 @@ constexpr int kStage = 2 * kOperand;
 constexpr int kChunk = 64 * kLine;          // 64 rows of an operand across
 constexpr int kMaxN = 256;
 constexpr int kRowBoxes = 4;
+constexpr int kEndBoxes = 9;                // 1, 2, 3, 4, 8, 12, 16, 32 and 48 rows: the digits of fewer than 64 to the base of 4
 constexpr int kPitch = 144;                 // bytes from row to row of a staging: 16 more than a line, so that eight rows meet no bank twice
 constexpr int kBlock = 8;                   // tiles of one side that pass along the other together
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -60,8 +61,19 @@ constexpr uint64_t kStepLimitNs = 4000;     // a step takes 0.15 to 0.31 us
 // How long a wait may last that ends only when so many steps have been made.
 __device__ __forceinline__ uint64_t wait_limit(int64_t steps) { return kWaitLimitNs + static_cast<uint64_t>(steps) * kStepLimitNs; }
 
+// b: of rows in boxes of 16, 32, 64 and 128.
+template <int KIND>
+struct Maps {
+    CUtensorMap a, b[kRowBoxes];
+};
+
+// a, b: of both operands' rows in boxes of 64; end_*: of 64 columns of fewer rows, those at an expert's end.
+template <>
+struct Maps<kWeight> {
+    CUtensorMap a, b[1], end_a[kEndBoxes], end_b[kEndBoxes];
+};
+
 struct Params {
-    CUtensorMap a, b[kRowBoxes];  // b: of rows in boxes of 16, 32, 64 and 128; the weights' gradient has one
     int64_t n_rows;
     int32_t E, width, out_width;
     int32_t fold;                              // Product::fold; each step of the contraction is then made twice, once for each part
@@ -82,8 +94,8 @@ struct Layout {
     static constexpr int staging = kStages * kStage;  // 32 lines for two writing warps, or 16 where sums are exchanged
     static constexpr int exchange = staging + kWriters / 2 * 16 * kPitch;  // gated: 2 KB a writing warp
     static constexpr int bars = exchange + kWriters * 2048;
-    static constexpr int full = bars, empty = full + 8 * kStages, tail = empty + 8 * kStages, sums_full = tail + 8 * kStages,
-                         sums_empty = sums_full + 16, done = sums_empty + 16, tmem = done + 8, first = tmem + 8;
+    static constexpr int full = bars, empty = full + 8 * kStages, sums_full = empty + 8 * kStages, sums_empty = sums_full + 16,
+                         done = sums_empty + 16, tmem = done + 8, first = tmem + 8;
     static int bytes(int E) { return first + 2 * 4 * (E + 1); }
 };
 static_assert(kWriters * 2048 >= kWriters / 2 * 16 * kPitch, "stagings of 32 lines reach into the room of the exchange");
@@ -101,8 +113,8 @@ struct Tile {
     // The first step of share i of n.
     __device__ int32_t first_of(int i, int n) const { return static_cast<int32_t>(static_cast<int64_t>(steps) * i / n); }
 
-    // Whether a step of the weights' gradient reads beyond the expert's rows.
-    __device__ bool beyond(int k, int32_t fold) const { return rows % kStep != 0 && k >= steps - (fold ? 2 : 1); }
+    // Whether a step of the weights' gradient takes the last of the expert's rows and there are not 64 of them.
+    __device__ bool ends(int k, int32_t fold) const { return rows % kStep != 0 && k >= steps - (fold ? 2 : 1); }
 };
 
 template <int KIND>
@@ -466,9 +478,24 @@ __device__ __forceinline__ void write_tile(const Params &p, const Tile &t, uint3
     }
 }
 
+// 64 columns of `rows` rows, fewer than 64, to shared memory, in a box for each digit of their number.  step 0: `row` is behind the
+// tensor's last, and zeros are copied.
+__device__ __forceinline__ void load_rows(uint32_t to, const CUtensorMap *boxes, int32_t column, int32_t row, int rows, int step, uint32_t bar)
+{
+#pragma unroll
+    for (int place = 2; place >= 0; --place) {
+        const int digit = (rows >> (2 * place)) & 3, n = digit << (2 * place);
+        if (digit == 0)
+            continue;
+        tensor_load_pair(to, &boxes[3 * place + digit - 1], column, row, 0, 0, bar);
+        to += n * kLine;
+        row += n * step;
+    }
+}
+
 // SPLIT: clusters of several pairs, a tile each; otherwise clusters of a pair, which take many.
 template <int KIND, bool BF16, int ACT, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps<KIND> maps)
 {
     constexpr bool kAcrossA = KIND == kInput || KIND == kWeight, kAcrossB = KIND == kWeight;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -477,13 +504,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int cta = static_cast<int>(cluster_rank()), rank = cta & 1, leader = SPLIT ? cta & ~1 : 0;
     const uint32_t both = 3u << leader;
     int32_t *first = reinterpret_cast<int32_t *>(smem + Layout::first), *tile0 = first + p.E + 1;
-    const uint32_t full = base + Layout::full, empty = base + Layout::empty, tail = base + Layout::tail,
-                   sums_full = base + Layout::sums_full, sums_empty = base + Layout::sums_empty, done = base + Layout::done;
+    const uint32_t full = base + Layout::full, empty = base + Layout::empty, sums_full = base + Layout::sums_full,
+                   sums_empty = base + Layout::sums_empty, done = base + Layout::done;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full + 8 * s, 2);   // both CTAs' copies (or the clearing of their last rows)
+            mbar_init(full + 8 * s, 2);   // both CTAs' copies
             mbar_init(empty + 8 * s, 1);
-            mbar_init(tail + 8 * s, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sums_full + 8 * i, 1);
@@ -491,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         mbar_init(done, 1);
         fence_mbar_init();
-        prefetch_map(&p.a);
+        prefetch_map(&maps.a);
         for (int i = 0; i < (kAcrossB ? 1 : kRowBoxes); ++i)
-            prefetch_map(&p.b[i]);
+            prefetch_map(&maps.b[i]);
     }
     if (warp == 2)
         tmem_alloc_pair(base + Layout::tmem, 512);
@@ -529,38 +555,53 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     break;
                 }
                 const uint32_t a = base + place.slot * kStage, b = a + kOperand;
-                uint32_t bar = full_of_pair + 8 * place.slot;
+                const uint32_t bar = full_of_pair + 8 * place.slot;
                 place.next();
                 if (!elect_lane())
                     continue;
-                if (KIND == kWeight && t.beyond(k, p.fold)) {
-                    bar = tail + (a - base) / kStage * 8;  // warp 2 clears what lies behind the rows, and then says that the slot is full
-                    mbar_arrive_expect_tx(bar, bytes);
-                } else {
-                    mbar_arrive_expect_tx_cluster(bar, bytes);
-                }
                 const int x = (p.fold ? k / 2 : k) * kStep, part = p.fold && k % 2 ? p.fold : 0;
                 const int32_t row = static_cast<int32_t>(t.row) + (KIND == kWeight ? x : rank * half);
+                if constexpr (KIND == kWeight) {
+                    // The last rows of an expert, and zeros up to a multiple of 16, all that the matrix instructions take (a
+                    // neighbour's values times zero would not do, as they may be infinities).  The zeros are copies too, of
+                    // rows that the tensor does not have, so that one barrier announces all of it to the pair: zeros stored by a
+                    // warp of either CTA had to be released to the pair, which waits for the writing warps' stores as well (R =
+                    // 8191, K = 2048, N = 2816, E = 64: 177 us; 138 this way; 136 with zeros that nothing orders for the other CTA).
+                    // An expert whose rows end with the tensor has them without this.
+                    if (t.ends(k, p.fold) && t.row + t.rows < p.n_rows) {
+                        const int rest = t.rows % kStep, zeros = -rest & 15;
+                        mbar_arrive_expect_tx_cluster(bar, static_cast<uint32_t>((2 + chunks) * (rest + zeros) * kLine));
+#pragma unroll 1
+                        for (int c = 0; c < 2 + chunks; ++c) {
+                            const CUtensorMap *boxes = c < 2 ? maps.end_a : maps.end_b;
+                            const int32_t column = c < 2 ? t.m0 + rank * kSide + part + 64 * c : t.n0 + rank * half + 64 * (c - 2);
+                            load_rows(a + c * kChunk, boxes, column, row, rest, 1, bar);
+                            load_rows(a + c * kChunk + rest * kLine, maps.end_a, 0, static_cast<int32_t>(p.n_rows), zeros, 0, bar);
+                        }
+                        continue;
+                    }
+                }
+                mbar_arrive_expect_tx_cluster(bar, bytes);
                 if constexpr (KIND == kForward) {
-                    tensor_load_pair(a, &p.a, x, t.m0 + rank * kSide, t.e, bar);
+                    tensor_load_pair(a, &maps.a, x, t.m0 + rank * kSide, t.e, bar);
                 } else if constexpr (KIND == kGated) {
-                    tensor_load_pair(a, &p.a, x, t.m0 + rank * 64, 0, t.e, bar);  // 64 rows of W1 and the same of W3
+                    tensor_load_pair(a, &maps.a, x, t.m0 + rank * 64, 0, t.e, bar);  // 64 rows of W1 and the same of W3
                 } else {
                     const int y = KIND == kInput ? x : row, e = KIND == kInput ? t.e : 0, column = t.m0 + rank * kSide + (KIND == kWeight ? part : 0);
                     if (p.wide_a) {
-                        tensor_load_pair(a, &p.a, 0, y, column / 64, e, bar);
+                        tensor_load_pair(a, &maps.a, 0, y, column / 64, e, bar);
                     } else {
-                        tensor_load_pair(a, &p.a, column, y, 0, e, bar);
-                        tensor_load_pair(a + kChunk, &p.a, column + 64, y, 0, e, bar);
+                        tensor_load_pair(a, &maps.a, column, y, 0, e, bar);
+                        tensor_load_pair(a + kChunk, &maps.a, column + 64, y, 0, e, bar);
                     }
                 }
                 if constexpr (kAcrossB) {
                     const int column = t.n0 + rank * half;
                     if (p.wide_b) {
-                        tensor_load_pair(b, &p.b[0], 0, row, column / 64, 0, bar);
+                        tensor_load_pair(b, &maps.b[0], 0, row, column / 64, 0, bar);
                     } else {
                         for (int c = 0; c < chunks; ++c)
-                            tensor_load_pair(b + c * kChunk, &p.b[0], column + 64 * c, row, 0, 0, bar);
+                            tensor_load_pair(b + c * kChunk, &maps.b[0], column + 64 * c, row, 0, 0, bar);
                     }
                 } else {
                     // half is a multiple of 16: one box for each of its bits
@@ -568,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
                     for (int i = kRowBoxes - 1; i >= 0; --i)
                         if (half & (16 << i)) {
-                            tensor_load_pair(b + at * kLine, &p.b[i], x + part, row + at, 0, bar);
+                            tensor_load_pair(b + at * kLine, &maps.b[i], x + part, row + at, 0, bar);
                             at += 16 << i;
                         }
                 }
@@ -597,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 const uint64_t a = kAcrossA ? operand_across(at, kChunk) : operand_along(at);
                 const uint64_t b = kAcrossB ? operand_across(at + kOperand, kChunk) : operand_along(at + kOperand);
                 // 16 of the contraction each: 32 bytes of a line, or 16 lines; of the rows that end in this step, what there is of them
-                const int sixteens = KIND == kWeight && t.beyond(k, p.fold) ? (t.rows % kStep + 15) / 16 : kStep / 16;
+                const int sixteens = KIND == kWeight && t.ends(k, p.fold) ? (t.rows % kStep + 15) / 16 : kStep / 16;
                 if (elect_lane()) {
 #pragma unroll
                     for (int j = 0; j < kStep / 16; ++j)
@@ -631,44 +672,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     slot = 0;
                     phase ^= 1;
                 }
-            }
-        }
-    } else if (warp == 2 && KIND == kWeight) {
-        // the last step of an expert's rows: lines behind them, in both operands, become zeros (a neighbour's values
-        // times zero would not do, as they may be infinities)
-        const uint32_t full_of_pair = cluster_map(full, leader);
-        uint32_t slot = 0, phases = 0;
-        int64_t ahead = 0;  // steps that this pair makes before the next wait ends: tiles that end on a whole step are passed over
-        bool good = true;
-        for (uint32_t q = pair; q < plan.total && good; q += pairs) {
-            const Tile t = plan.at(q);
-            if (t.begin == t.end)
-                continue;
-            // steps of this pair that read beyond
-            const int rest = t.rows % kStep, until = t.steps - (p.fold ? 2 : 1),
-                      last = rest != 0 && t.end > until ? t.end - (t.begin > until ? t.begin : until) : 0;
-            slot = static_cast<uint32_t>((slot + t.end - t.begin - last) % kStages);
-            ahead += t.end - t.begin;
-            for (int i = 0; i < last && good; ++i) {
-                good = mbar_wait_bounded(tail + 8 * slot, (phases >> slot) & 1, wait_limit(ahead));
-                good = __all_sync(0xffffffffu, good);
-                if (!good)
-                    break;
-                ahead = 0;
-                phases ^= 1u << slot;
-                const int chunks = 2 + (t.n / 2 + 63) / 64;
-                const int end = (rest + 15) / 16 * 16;  // the matrix instructions take no more of them
-                for (int c = 0; c < chunks; ++c)
-                    for (int at = 8 * rest + lane; at < 8 * end; at += 32)
-                        *reinterpret_cast<uint4 *>(smem + slot * kStage + c * kChunk + 16 * at) = make_uint4(0, 0, 0, 0);
-                // the zeros are this SM's own, written, fenced for its tensor core and then announced; nothing of another CTA's memory
-                // has to be ordered, which a release and an acquire for the whole pair would wait for (a gradient of R = 32768, K = 1024,
-                // N = 4096, E = 128 took 303 us with them, 252 without)
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(full_of_pair + 8 * slot);
-                slot = (slot + 1) % kStages;
             }
         }
     } else if (warp >= 4) {
@@ -752,6 +755,7 @@ moe_status launch(const Product &a, moe_stream_t stream)
     const int sms = sm_count();
     int dev = 0;
     Params p{};
+    Maps<KIND> maps{};
     p.n_rows = a.n_rows;
     p.E = a.E;
     p.width = a.width;
@@ -813,28 +817,34 @@ moe_status launch(const Product &a, moe_stream_t stream)
     const auto kern = p.shares > 1 ? product_kernel<KIND, BF16, ACT, true> : product_kernel<KIND, BF16, ACT, false>;
     const int64_t W = a.width, F = a.out_width, held = a.fold ? 2 * a.fold : W;  // held: columns of `rows` in memory
     // [rows, columns] across, of `groups` matrices: chunks of 64 columns, two in a box where the columns are whole chunks
-    const auto across = [](CUtensorMap &map, const void *at, int64_t columns, int64_t rows, int64_t groups, int64_t stride, bool wide) {
+    const auto across = [](CUtensorMap &map, const void *at, int64_t columns, int64_t rows, int64_t groups, int64_t stride, bool wide,
+                           int box = kStep) {
         if (wide)
-            return encode_tensor(map, at, {4, {64, rows, columns / 64, groups}, {stride, 64, groups > 1 ? rows * stride : stride}, {64, kStep, 2, 1}});
-        return encode_tensor(map, at, {4, {columns, rows, 1, groups}, {stride, stride, groups > 1 ? rows * stride : stride}, {64, kStep, 1, 1}});
+            return encode_tensor(map, at, {4, {64, rows, columns / 64, groups}, {stride, 64, groups > 1 ? rows * stride : stride}, {64, box, 2, 1}});
+        return encode_tensor(map, at, {4, {columns, rows, 1, groups}, {stride, stride, groups > 1 ? rows * stride : stride}, {64, box, 1, 1}});
     };
     if (tiles >= int64_t{1} << 31)
         return MOE_ERR_UNSUPPORTED;
     bool ok = true;
-    if (KIND == kForward) {
-        ok = encode_tensor(p.a, a.other, {3, {W, F, a.E}, {W, F * W}, {kStep, kSide, 1}});
-    } else if (KIND == kGated) {
-        ok = encode_tensor(p.a, a.other, {4, {W, F, 2, a.E}, {W, F * W, 2 * F * W}, {kStep, 64, 2, 1}});
-    } else if (KIND == kInput) {
+    if constexpr (KIND == kForward) {
+        ok = encode_tensor(maps.a, a.other, {3, {W, F, a.E}, {W, F * W}, {kStep, kSide, 1}});
+    } else if constexpr (KIND == kGated) {
+        ok = encode_tensor(maps.a, a.other, {4, {W, F, 2, a.E}, {W, F * W, 2 * F * W}, {kStep, 64, 2, 1}});
+    } else if constexpr (KIND == kInput) {
         p.wide_a = F % 64 == 0;
-        ok = across(p.a, a.other, F, W, a.E, F, p.wide_a);
-    } else {
+        ok = across(maps.a, a.other, F, W, a.E, F, p.wide_a);
+    }
+    if constexpr (KIND == kWeight) {
         p.wide_a = held % 64 == 0;
         p.wide_b = F % 64 == 0 && p.n_columns == 256;
-        ok = across(p.a, a.rows, held, a.n_rows, 1, a.rows_stride, p.wide_a) && across(p.b[0], a.other, F, a.n_rows, 1, a.other_stride, p.wide_b);
+        ok = across(maps.a, a.rows, held, a.n_rows, 1, a.rows_stride, p.wide_a) && across(maps.b[0], a.other, F, a.n_rows, 1, a.other_stride, p.wide_b);
+        for (int i = 0; a.offsets && i < kEndBoxes; ++i)  // without offsets the only expert's rows end with the tensor
+            ok = ok && across(maps.end_a[i], a.rows, held, a.n_rows, 1, a.rows_stride, false, (i % 3 + 1) << (i / 3 * 2)) &&
+                 across(maps.end_b[i], a.other, F, a.n_rows, 1, a.other_stride, false, (i % 3 + 1) << (i / 3 * 2));
+    } else {
+        for (int i = 0; i < kRowBoxes; ++i)
+            ok = ok && encode_tensor(maps.b[i], a.rows, {3, {held, a.n_rows, 1}, {a.rows_stride, a.rows_stride}, {kStep, 16 << i, 1}});
     }
-    for (int i = 0; KIND != kWeight && i < kRowBoxes; ++i)
-        ok = ok && encode_tensor(p.b[i], a.rows, {3, {held, a.n_rows, 1}, {a.rows_stride, a.rows_stride}, {kStep, 16 << i, 1}});
     const size_t smem = static_cast<size_t>(Layout::bytes(a.E));
     if (!ok || sms < 2 || cudaGetDevice(&dev) != cudaSuccess || ensure_dynamic_smem(kern, dev, static_cast<int>(smem), limits[p.shares > 1]) != cudaSuccess) {
         cudaGetLastError();
@@ -855,7 +865,7 @@ moe_status launch(const Product &a, moe_stream_t stream)
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, kern, p, maps) == cudaSuccess)
         return MOE_OK;
     cudaGetLastError();
     return MOE_ERR_CUDA;

@@ -124,8 +124,8 @@ __device__ __forceinline__ uint64_t operand_across(uint32_t at, uint32_t chunk)
 
 // ----------------------------------------------------------------- the pair's barriers
 
-// Arrives at a barrier of either CTA (address from cluster_map).  These order nothing beyond this CTA: the data that they
-// announce is tensor memory, this SM's own shared memory, or a copy's (whose transaction bytes say when it is there).
+// Arrives at a barrier of either CTA (address from cluster_map).  These order nothing beyond this CTA: what they announce is
+// tensor memory (with its own fences) or a copy's data (whose transaction bytes say when it is there).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
