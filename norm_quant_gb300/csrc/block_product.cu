@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             // what is in flight ends before the pair leaves: matrix instructions, and copies (those of a slot that only one CTA
             // filled never complete its barrier, and have long landed after the wait)
             if (elect_lane())
-                mma_pair_commit(done, both);
+                mma_pair_commit(done, 1u << leader);  // the other CTA does not wait for it
             __syncwarp();
             warp_wait(done, 0);
             const uint64_t t0 = globaltimer_ns();
