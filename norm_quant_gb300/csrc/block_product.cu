@@ -549,6 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int half = t.n / 2;
             const int chunks = (half + 63) / 64;
             const uint32_t bytes = kOperand + static_cast<uint32_t>(kAcrossB ? (p.wide_b ? 2 * kChunk : chunks * kChunk) : half * kLine);
+            // the first step whose rows have boxes of their own
+            const bool within = KIND == kWeight && t.rows % kStep != 0 && t.row + t.rows < p.n_rows;
+            const int apart = within ? t.steps - (p.fold ? 2 : 1) : INT32_MAX;
             for (int k = t.begin; k < t.end; ++k) {
                 if (left-- <= 0 || !warp_wait(empty + 8 * place.slot, place.phase)) {
                     good = false;
@@ -566,9 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     // neighbour's values times zero would not do, as they may be infinities).  The zeros are copies too, of
                     // rows that the tensor does not have, so that one barrier announces all of it to the pair: zeros stored by a
                     // warp of either CTA had to be released to the pair, which waits for the writing warps' stores as well (R =
-                    // 8191, K = 2048, N = 2816, E = 64: 177 us; 138 this way; 136 with zeros that nothing orders for the other CTA).
+                    // 8191, K = 2048, N = 2816, E = 64: 177 us; 137 this way; 136 with zeros that nothing orders for the other CTA).
                     // An expert whose rows end with the tensor has them without this.
-                    if (t.ends(k, p.fold) && t.row + t.rows < p.n_rows) {
+                    if (k >= apart) {
                         const int rest = t.rows % kStep, zeros = -rest & 15;
                         mbar_arrive_expect_tx_cluster(bar, static_cast<uint32_t>((2 + chunks) * (rest + zeros) * kLine));
 #pragma unroll 1
