@@ -30,7 +30,9 @@
  * Waits inside the products' kernels are bounded.  One that runs out (after 2 s and
  * 4 us for each 64 of the contraction that is multiplied while it lasts, more than ten
  * times what a healthy launch takes) turns results that depend on it into NaN and
- * records MOE_ERR_DEVICE_TIMEOUT in *status; nothing faults or hangs.
+ * records MOE_ERR_DEVICE_TIMEOUT in *status; nothing faults or hangs.  The norms have no
+ * status: a wait that runs out there (2 s) shows in NaN alone, in its row's results and in the
+ * sums over tokens.
  * moe_debug_stall (moe_combine.h) stops the first thread block's copies of a product
  * and the copies of a norm's first rows after its number of steps, to test that.
  */
@@ -99,7 +101,8 @@ size_t moe_gated_linear_args_size(void);
  * workspace: device memory of moe_gated_linear_backward_workspace_size(...)
  * bytes, 16-byte aligned, not shared by calls that may overlap; it holds dg and du
  * of every row, and what it holds before a call does not matter.  The
- * size never falls as rows grow: one made for the largest batch serves every smaller one.
+ * size never falls as rows grow, so one made for the largest batch serves every smaller
+ * one, and is at most 32 KB more than the 4 rows I bytes of dg and du.
  * ---------------------------------------------------------------------- */
 typedef struct moe_gated_linear_backward_args {
     int64_t rows;

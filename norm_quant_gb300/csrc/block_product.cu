@@ -18,10 +18,10 @@
 // tile is written out while the next is multiplied.  Warps: 0 copies (TMA), 1 issues matrix instructions (in the
 // pair's first CTA, for both), 4 to 11 write results.
 //
-// What bounds it: with many rows an expert the matrix instruction (R = 8192, K = 4096, N = 8192, bf16: forward 276 us, 1990
-// TFLOP/s, gated 274, rows' gradient 282, weights' gradient 279; the tensor pipe is active 93 % of the time at K = N = 4096),
-// with few the weights' bytes (gated, R = 32768, H = 7168, I = 2048, E = 256: 14.2 GB in 2.07 ms, 6.9 TB/s), between the two the
-// operands' way from L2 (R = 32768, K = 1024, N = 4096, E = 128: 225 us, some 15 TB/s out of L2).
+// What bounds it: with many rows an expert the matrix instruction (R = 8192, K = 4096, N = 8192, bf16: forward 287 us, 1918
+// TFLOP/s, gated 283, rows' gradient 290, weights' gradient 287, where the power limit holds cuBLAS at 271; the tensor pipe is active
+// 93 % of the time at K = N = 4096), with few the weights' bytes (gated, R = 32768, H = 7168, I = 2048, E = 256: 14.2 GB in 2.12 ms,
+// 6.7 TB/s), between the two the operands' way from L2 (R = 32768, K = 1024, N = 4096, E = 128: 255 us, some 13 TB/s out of L2).
 //
 // CTAs stay (one pair for two SMs) and take every P-th tile.  Within an expert, blocks of 8 tiles of one side pass along
 // the other, so that the pairs at work share their operands in L2.
@@ -355,7 +355,7 @@ __device__ __forceinline__ void write_gradient(const Params &p, const Tile &t, u
                                                uint8_t *staging, const Shares &shares, bool lost)
 {
     // The two warps of a quarter take every other chunk of 64 columns, or half of the lanes each where there is an odd number of
-    // chunks (59 rows, K = 576, N = 2528, E = 125, three chunks a tile: 67 us, 77 with a warp taking two of them; 56
+    // chunks (59 rows, K = 576, N = 2528, E = 125, three chunks a tile: 67 us, 77 with a warp taking two of them; 57
     // with the addresses' products made once a tile).
     const int columns = p.out_width - t.n0 < t.n ? p.out_width - t.n0 : t.n;
     const int step = SPLIT ? shares.count : 1, mine = SPLIT ? shares.mine : 0, chunks = ((columns + 63) / 64 - mine + step - 1) / step;
